@@ -328,6 +328,88 @@ int moe_unpermute_combine(const void* y, int y_dtype, const float* gates,
                           const int32_t* pair_row, int64_t T, int32_t topk, int64_t H,
                           void* out, int out_dtype, mxf_stream stream);
 
+/* FP4 weight formats of the calls that take both: E2M1 codes with one UE8M0 scale per 32
+ * K-elements, or with one UE4M3 scale per 16 (as in nvfp4_gemm_w4a16). */
+typedef enum { MXF_W_MXFP4 = 0, MXF_W_NVFP4 = 1 } mxf_weight;
+
+/*
+ * moe_grouped_gemm_w4a16 - ragged grouped GEMM of bf16 activations with FP4 expert weights:
+ *   y[r] = a[src(r)] * W_hat_e^T   for every expert e and row r in
+ *                                  [expert_offsets[e], expert_offsets[e+1])
+ * the grouped form of mxfp4_gemm_w4a16 / nvfp4_gemm_w4a16: no activation quantisation,
+ * products exact, fp32 accumulation. An expert may have any number of rows, none included.
+ *   a            [a_rows][K] bf16
+ *   sorted_pair  NULL: src(r) = r (a_rows must be R); else [R] int32 and src(r) =
+ *                sorted_pair[r] / topk (as moe_route_permute writes it; topk is ignored
+ *                when it is NULL). An entry outside [0, a_rows * topk) reads some row of a
+ *                or zeros, never anything else.
+ *   expert_offsets [E+1] int32, ascending, within [0, R]; values outside are held to it
+ *   w, w_scale   [E][N][K/2] codes, [E][N][K/32] UE8M0 (bytes 2..252) or [E][N][K/16] UE4M3
+ *   swiglu       0: y [R][N]; 1: rows 0..N/2-1 of W are gate rows, the others the up rows,
+ *                and y [R][N/2] = silu(gate) * up, in fp32 before the one rounding to y_dtype
+ *   y            fp32 or bf16 (y_dtype; round to nearest even). Rows of y outside
+ *                [expert_offsets[0], expert_offsets[E]) are left as they were.
+ * Deterministic: no atomics, a fixed summation order; a row's result does not depend on
+ * the other experts' rows. Requires K % 128 == 0, N % 16 == 0 (swiglu: N % 32 == 0),
+ * E <= 1024, and the bytes of one expert's codes below 4 GiB with a margin of 257 rows;
+ * with sorted_pair also a below 4 GiB. R == 0 is a no-op.
+ * Errors: NULL, SHAPE, ALIGN, FORMAT, UNSUPPORTED.
+ */
+int moe_grouped_gemm_w4a16(const uint16_t* a, int64_t a_rows, int64_t R, const int32_t* sorted_pair, int32_t topk,
+                           const int32_t* expert_offsets, int32_t E, int64_t N, int64_t K, int w_fmt,
+                           const uint8_t* w, const uint8_t* w_scale, int swiglu, void* y, int y_dtype,
+                           mxf_stream stream);
+
+/*
+ * fp4_gemm_w4a16_lora - a shared FP4 projection with the low-rank adapters of many requests:
+ *   c[t] = a[t] * W_hat^T + scaling[l] * (a[t] * lora_a[l]^T) * lora_b[l]^T
+ * where l = seg_adapter[s] for the segment s with seg_offsets[s] <= t < seg_offsets[s+1].
+ * A segment whose adapter is outside [0, L) (say -1), and rows in no segment, get the
+ * projection alone.
+ *   a            [M][K] bf16;  w, w_scale as for mxfp4_gemm_w4a16 / nvfp4_gemm_w4a16
+ *   seg_offsets  [S+1] int32, ascending (a request's rows are consecutive); seg_adapter [S]
+ *   lora_a       [L][rank][K] bf16;  lora_b [L][N][rank] bf16;  scaling [L] fp32. An adapter
+ *                of a smaller rank is padded with zero rows of lora_a.
+ *   c            [M][N] fp32 or bf16 (c_dtype), one rounding at the end; the low-rank
+ *                product is kept in fp32 between its two factors
+ *   workspace    fp4_w4a16_lora_workspace_bytes() bytes, 16-byte aligned, contents
+ *                irrelevant; calls that may overlap need one each
+ * Requires K % 512 == 0, N % 16 == 0, rank % 8 == 0, 8 <= rank <= 128. S == 0 (with L == 0
+ * or not): the projection alone. M == 0 is a no-op.
+ * Errors: NULL, SHAPE, ALIGN, FORMAT, UNSUPPORTED, WORKSPACE.
+ */
+size_t fp4_w4a16_lora_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t rank);
+int fp4_gemm_w4a16_lora(const uint16_t* a, int64_t M, int64_t N, int64_t K, int w_fmt, const uint8_t* w,
+                        const uint8_t* w_scale, const int32_t* seg_offsets, const int32_t* seg_adapter, int32_t S,
+                        const uint16_t* lora_a, const uint16_t* lora_b, const float* scaling, int32_t L,
+                        int32_t rank, void* c, int c_dtype, void* workspace, size_t workspace_bytes,
+                        mxf_stream stream);
+
+/*
+ * moe_block_norm - the step between two blocks of a decoder layer, one pass over each row:
+ *   b = y[t], or with topk > 0 the combine sum_j expert_gates[t][j] * y[pair_row[t*topk+j]]
+ *       (fp32, slot order, as moe_unpermute_combine; an entry of pair_row outside
+ *       [0, y_rows) is a dropped pair and adds nothing)
+ *   p = post_weight * b / sqrt(mean(b^2) + eps)   (post_weight NULL: p = b)
+ *   r = residual_scale * x[t] + gate * p          (x NULL: r = gate * p)
+ *   n = pre_weight * r / sqrt(mean(r^2) + eps)    (pre_weight NULL: weights of one)
+ *   q, q_scale = n quantised as by mxfp4_quantize_act (from the fp32 n)
+ * All in fp32; each result is rounded once, when it is stored.
+ *   y            [T][H], or with topk > 0 [y_rows][H] (y_dtype)
+ *   x, r         [T][H] (x_dtype, both); r may be x itself
+ *   post_weight, pre_weight  [H] (weight_dtype)
+ *   gate         gate_mode 0: none (gate ignored), 1: [H], 2: [T], 3: [T][H] (gate_dtype)
+ *   r, n, q      any may be NULL (not wanted), not all; n [T][H] (n_dtype); q [T][H] (E4M3)
+ *                or [T][H/2] (E2M1) by fmt, with q_scale [T][H/32]
+ * Requires H % 8 == 0 (H % 32 == 0 with q), H <= 65536, eps > 0, topk <= 8; with topk == 0
+ * y_rows must be T. T == 0 is a no-op. Errors: NULL, SHAPE, ALIGN, FORMAT, UNSUPPORTED.
+ */
+int moe_block_norm(const void* y, int y_dtype, int64_t y_rows, const float* expert_gates, const int32_t* pair_row,
+                   int32_t topk, int64_t T, int64_t H, const void* x, int x_dtype, float residual_scale,
+                   const void* post_weight, const void* pre_weight, int weight_dtype, float eps, const void* gate,
+                   int gate_dtype, int gate_mode, void* r, void* n, int n_dtype, int fmt, uint8_t* q,
+                   uint8_t* q_scale, mxf_stream stream);
+
 #ifdef __cplusplus
 }
 #endif

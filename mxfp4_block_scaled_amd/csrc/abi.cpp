@@ -6,6 +6,7 @@
 #include <hip/hip_runtime.h>
 
 #include "launch.hpp"
+#include "w4a16_tile.hpp"
 
 namespace {
 
@@ -14,11 +15,13 @@ inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 
 inline hipStream_t as_stream(mxf_stream s) { return reinterpret_cast<hipStream_t>(s); }
 
 inline bool valid_elem(int f) { return f == MXF_E4M3 || f == MXF_E2M1; }
+inline bool valid_weight(int f) { return f == MXF_W_MXFP4 || f == MXF_W_NVFP4; }
 inline bool valid_dtype(int d) { return d == MXF_F32 || d == MXF_BF16; }
 
 inline size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 constexpr int64_t kMaxRows = (int64_t(1) << 31) - 1;
+constexpr int64_t kMaxOffset = int64_t(1) << 32;  // byte offsets that kernels keep in 32 bits stay below
 
 }  // namespace
 
@@ -252,6 +255,119 @@ int moe_unpermute_combine(const void* y, int y_dtype, const float* gates, const 
   int rc = mxf::launch_combine(y, y_dtype == MXF_BF16, gates, pair_row, T, topk, H, out, out_dtype == MXF_BF16,
                                as_stream(stream));
   return rc ? MXF_ERR_LAUNCH : MXF_OK;
+}
+
+int moe_grouped_gemm_w4a16(const uint16_t* a, int64_t a_rows, int64_t R, const int32_t* sorted_pair, int32_t topk,
+                           const int32_t* expert_offsets, int32_t E, int64_t N, int64_t K, int w_fmt,
+                           const uint8_t* w, const uint8_t* w_scale, int swiglu, void* y, int y_dtype,
+                           mxf_stream stream) {
+  if (!valid_weight(w_fmt) || !valid_dtype(y_dtype)) return MXF_ERR_FORMAT;
+  if (R < 0 || a_rows < 0 || E < 1 || (swiglu != 0 && swiglu != 1)) return MXF_ERR_SHAPE;
+  if (N <= 0 || N % (swiglu ? 32 : 16) != 0 || K <= 0 || K % 128 != 0) return MXF_ERR_SHAPE;
+  if (sorted_pair ? topk < 1 || (R > 0 && a_rows < 1) : a_rows != R) return MXF_ERR_SHAPE;
+  if (E > 1024 || R > kMaxRows || a_rows > kMaxRows) return MXF_ERR_UNSUPPORTED;
+  // 32-bit byte offsets: a unit's rows of a, one expert's codes (and the tile rows past N)
+  if (K >= (int64_t(1) << 22) || N > kMaxRows || (N + 257) * (K / 2) >= kMaxOffset) return MXF_ERR_UNSUPPORTED;
+  if (sorted_pair && (a_rows + 2) * K * 2 >= kMaxOffset) return MXF_ERR_UNSUPPORTED;
+  // the grid: at most E + R / 64 units of ceil(N / 64) workgroups
+  if ((E + R / 64) * mxf::cdiv(N, 64) > kMaxRows - 8) return MXF_ERR_UNSUPPORTED;
+  if (R == 0) return MXF_OK;
+  if (!a || !expert_offsets || !w || !w_scale || !y) return MXF_ERR_NULL;
+  const void* ptrs[] = {a, sorted_pair, expert_offsets, w, w_scale, y};
+  for (const void* p : ptrs)
+    if (!aligned16(p)) return MXF_ERR_ALIGN;
+  mxf::W16TileArgs t{};
+  t.a = a;
+  t.a_rows = a_rows;
+  t.offsets = expert_offsets;
+  t.pair = sorted_pair;
+  t.topk = topk;
+  t.E = E;
+  t.R = R;
+  t.w = w;
+  t.ws = w_scale;
+  t.N = N;
+  t.K = K;
+  t.out = y;
+  return mxf::launch_w16_grouped(t, w_fmt == MXF_W_NVFP4, swiglu != 0, y_dtype == MXF_BF16, as_stream(stream))
+             ? MXF_ERR_LAUNCH
+             : MXF_OK;
+}
+
+size_t fp4_w4a16_lora_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t rank) {
+  if (M <= 0 || N <= 0 || K <= 0 || rank <= 0) return 0;
+  const size_t base = (size_t)mxf::lora_base_slices(M, N, K) * (size_t)M * (size_t)N;
+  const size_t low = (size_t)mxf::lora_shrink_slices(M, K) * (size_t)M * (size_t)rank;
+  return round_up((base + low) * sizeof(float), 256);
+}
+
+int fp4_gemm_w4a16_lora(const uint16_t* a, int64_t M, int64_t N, int64_t K, int w_fmt, const uint8_t* w,
+                        const uint8_t* w_scale, const int32_t* seg_offsets, const int32_t* seg_adapter, int32_t S,
+                        const uint16_t* lora_a, const uint16_t* lora_b, const float* scaling, int32_t L,
+                        int32_t rank, void* c, int c_dtype, void* workspace, size_t workspace_bytes,
+                        mxf_stream stream) {
+  if (!valid_weight(w_fmt) || !valid_dtype(c_dtype)) return MXF_ERR_FORMAT;
+  if (M < 0 || M > kMaxRows || N <= 0 || N % 16 != 0 || K <= 0 || K % 512 != 0) return MXF_ERR_SHAPE;
+  if (S < 0 || L < 0 || rank < 8 || rank > 128 || rank % 8 != 0) return MXF_ERR_SHAPE;
+  if (K >= (int64_t(1) << 22) || N > kMaxRows || (N + 257) * (K / 2) >= kMaxOffset) return MXF_ERR_UNSUPPORTED;
+  if (mxf::cdiv(M, 64) * mxf::cdiv(N, 128) > kMaxRows - 8) return MXF_ERR_UNSUPPORTED;
+  if (M == 0) return MXF_OK;
+  if (!a || !w || !w_scale || !c) return MXF_ERR_NULL;
+  if (S > 0 && (!seg_offsets || !seg_adapter)) return MXF_ERR_NULL;
+  if (S > 0 && L > 0 && (!lora_a || !lora_b || !scaling)) return MXF_ERR_NULL;
+  const void* ptrs[] = {a, w, w_scale, c, seg_offsets, seg_adapter, lora_a, lora_b, scaling, workspace};
+  for (const void* p : ptrs)
+    if (!aligned16(p)) return MXF_ERR_ALIGN;
+  const size_t need = fp4_w4a16_lora_workspace_bytes(M, N, K, rank);
+  if (!workspace || workspace_bytes < need) return MXF_ERR_WORKSPACE;
+  mxf::W16LoraArgs p{a,       w,   w_scale, seg_offsets, seg_adapter, lora_a, lora_b, scaling,
+                     c,       static_cast<float*>(workspace), M, N, K, rank, L, L > 0 ? S : 0};
+  return mxf::launch_w16_lora(p, w_fmt == MXF_W_NVFP4, c_dtype == MXF_BF16, as_stream(stream)) ? MXF_ERR_LAUNCH
+                                                                                               : MXF_OK;
+}
+
+int moe_block_norm(const void* y, int y_dtype, int64_t y_rows, const float* expert_gates, const int32_t* pair_row,
+                   int32_t topk, int64_t T, int64_t H, const void* x, int x_dtype, float residual_scale,
+                   const void* post_weight, const void* pre_weight, int weight_dtype, float eps, const void* gate,
+                   int gate_dtype, int gate_mode, void* r, void* n, int n_dtype, int fmt, uint8_t* q,
+                   uint8_t* q_scale, mxf_stream stream) {
+  if (!valid_dtype(y_dtype) || !valid_dtype(x_dtype) || !valid_dtype(weight_dtype) || !valid_dtype(gate_dtype) ||
+      !valid_dtype(n_dtype) || !valid_elem(fmt) || gate_mode < 0 || gate_mode > 3)
+    return MXF_ERR_FORMAT;
+  if (T < 0 || H <= 0 || H % (q ? 32 : 8) != 0 || topk < 0 || topk > 8 || y_rows < 0) return MXF_ERR_SHAPE;
+  if (!(eps > 0.0f) || (topk == 0 && y_rows != T)) return MXF_ERR_SHAPE;
+  if (H > 65536 || T > kMaxRows || y_rows > kMaxRows || T * topk > kMaxRows) return MXF_ERR_UNSUPPORTED;
+  if (T == 0) return MXF_OK;
+  if (!y || (topk > 0 && (!expert_gates || !pair_row)) || (gate_mode > 0 && !gate)) return MXF_ERR_NULL;
+  if ((!r && !n && !q) || (q == nullptr) != (q_scale == nullptr)) return MXF_ERR_NULL;
+  const void* ptrs[] = {y, expert_gates, pair_row, x, post_weight, pre_weight, gate, r, n, q, q_scale};
+  for (const void* p : ptrs)
+    if (!aligned16(p)) return MXF_ERR_ALIGN;
+  mxf::BlockNormArgs b{};
+  b.y = y;
+  b.expert_gates = expert_gates;
+  b.pair_row = pair_row;
+  b.x = x;
+  b.post_weight = post_weight;
+  b.pre_weight = pre_weight;
+  b.gate = gate;
+  b.r = r;
+  b.n = n;
+  b.q = q;
+  b.q_scale = q_scale;
+  b.T = T;
+  b.H = H;
+  b.y_rows = y_rows;
+  b.residual_scale = residual_scale;
+  b.eps = eps;
+  b.topk = topk;
+  b.gate_mode = gate_mode;
+  b.x_bf16 = x_dtype == MXF_BF16;
+  b.weight_bf16 = weight_dtype == MXF_BF16;
+  b.gate_bf16 = gate_dtype == MXF_BF16;
+  b.n_bf16 = n_dtype == MXF_BF16;
+  b.q_fp4 = fmt == MXF_E2M1;
+  return mxf::launch_block_norm(b, y_dtype == MXF_BF16, as_stream(stream)) ? MXF_ERR_LAUNCH : MXF_OK;
 }
 
 }  // extern "C"

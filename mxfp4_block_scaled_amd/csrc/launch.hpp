@@ -54,6 +54,47 @@ int w4a16_ksplit(int64_t M, int64_t N, int64_t K);
 int launch_w4a16_gemm(bool nvfp4, const uint16_t* a, int64_t M, int64_t N, int64_t K, const uint8_t* w,
                       const uint8_t* ws, float* c, float* partials, hipStream_t stream);
 
+// the same for at most 64 rows, leaving its w4a16_ksplit K slices [S][M][N] in partials
+void launch_w4a16_slices(bool nvfp4, const uint16_t* a, int64_t M, int64_t N, int64_t K, const uint8_t* w,
+                         const uint8_t* ws, float* partials, hipStream_t stream);
+
+// ragged grouped products of bf16 activations and FP4 expert weights (w4a16_grouped.hip)
+struct W16TileArgs;
+int launch_w16_grouped(W16TileArgs a, bool nvfp4, bool swiglu, bool out_bf16, hipStream_t stream);
+
+// a shared FP4 projection with low-rank adapters (w4a16_lora.hip); the workspace holds
+// lora_base_slices x M x N and lora_shrink_slices x M x rank fp32
+struct W16LoraArgs {
+  const uint16_t* a;
+  const uint8_t *w, *ws;
+  const int32_t *seg_off, *seg_adapter;
+  const uint16_t *lora_a, *lora_b;
+  const float* scaling;
+  void* out;
+  float* workspace;
+  int64_t M, N, K;
+  int rank, L, S;
+};
+int lora_shrink_slices(int64_t M, int64_t K);
+int lora_base_slices(int64_t M, int64_t N, int64_t K);
+int launch_w16_lora(const W16LoraArgs& a, bool nvfp4, bool out_bf16, hipStream_t stream);
+
+// post-norm, gate, residual, pre-norm and quantisation of a block's output (block_norm.hip)
+enum { kGateNone = 0, kGateChannel = 1, kGateToken = 2, kGateFull = 3 };
+struct BlockNormArgs {
+  const void* y;                // [T][H], or with topk > 0 [y_rows][H]
+  const float* expert_gates;    // [T][topk]
+  const int32_t* pair_row;      // [T*topk]
+  const void *x, *post_weight, *pre_weight, *gate;
+  void *r, *n;
+  uint8_t *q, *q_scale;
+  int64_t T, H, y_rows;
+  float residual_scale, eps;
+  int topk, gate_mode;
+  bool x_bf16, weight_bf16, gate_bf16, n_bf16, q_fp4;
+};
+int launch_block_norm(const BlockNormArgs& a, bool y_bf16, hipStream_t stream);
+
 // the lookup-table route (gemm_q8.hip): Q8 activations and int8-expanded MXFP4 weights
 int launch_q8_quantize(const uint16_t* x, int64_t rows, int64_t K, int8_t* q, uint16_t* d, hipStream_t stream);
 int launch_q8_gemm(const int8_t* q, const uint16_t* d, int64_t M, int64_t N, int64_t K, const uint8_t* w,

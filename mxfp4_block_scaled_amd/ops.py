@@ -17,6 +17,7 @@ _lib = None
 MXF_E4M3, MXF_E2M1 = 0, 1
 MXF_F32, MXF_BF16 = 0, 1
 FMTS = {"e4m3": MXF_E4M3, "e2m1": MXF_E2M1}
+WEIGHT_FMTS = {"mxfp4": 0, "nvfp4": 1}
 DTYPES = {torch.float32: MXF_F32, torch.bfloat16: MXF_BF16}
 
 _c_i64, _c_i32, _c_int, _p, _sz = ctypes.c_int64, ctypes.c_int32, ctypes.c_int, ctypes.c_void_p, ctypes.c_size_t
@@ -43,6 +44,13 @@ SIGNATURES = {
                                     _p, _p]),
     "moe_grouped_mxfp4_gemm_combine": (_c_int, [_p, _p, _c_int, _c_i64, _c_i32, _c_i64, _c_i64, _c_i32, _p, _p,
                                                 _p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _c_int, _p]),
+    "moe_grouped_gemm_w4a16": (_c_int, [_p, _c_i64, _c_i64, _p, _c_i32, _p, _c_i32, _c_i64, _c_i64, _c_int, _p, _p,
+                                        _c_int, _p, _c_int, _p]),
+    "fp4_w4a16_lora_workspace_bytes": (_sz, [_c_i64, _c_i64, _c_i64, _c_i32]),
+    "fp4_gemm_w4a16_lora": (_c_int, [_p, _c_i64, _c_i64, _c_i64, _c_int, _p, _p, _p, _p, _c_i32, _p, _p, _p, _c_i32,
+                                     _c_i32, _p, _c_int, _p, _sz, _p]),
+    "moe_block_norm": (_c_int, [_p, _c_int, _c_i64, _p, _p, _c_i32, _c_i64, _c_i64, _p, _c_int, ctypes.c_float, _p, _p,
+                                _c_int, ctypes.c_float, _p, _c_int, _c_int, _p, _p, _c_int, _c_int, _p, _p, _p]),
     # include/mxf_ceilings.h: achievable-rate probes (measurement helpers)
     "mxf_ceiling_mfma_flops": (_c_i64, [_c_int]),
     "mxf_ceiling_mfma": (_c_int, [_c_int, _p, _c_i64, _c_int, _c_int, _p, _p]),
@@ -110,6 +118,43 @@ def _need(t, name, dtypes, shape):
         ok = got >= want[1] if isinstance(want, tuple) else got == want
         if not ok:
             raise RuntimeError(f"{name}: shape {tuple(t.shape)}, expected {shape} (dimension {i})")
+
+
+def _dev_all(*tensors):
+    """The one GPU that all the given tensors (None skipped) are on; they must be contiguous."""
+    dev = None
+    for t in tensors:
+        if t is None:
+            continue
+        if not t.is_cuda or not t.is_contiguous():
+            _dev(t)
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise RuntimeError(f"tensors are on {dev} and {t.device}, expected one GPU")
+    return dev
+
+
+def _call(name, dev, *args):
+    """The C function `name` with the tensors' GPU current and its current stream as the last argument."""
+    fn = getattr(load(), name)
+    if torch.cuda.current_device() == dev.index:
+        rc = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    if rc:
+        _check(rc, name)
+
+
+def _at(t):
+    return t.data_ptr() if t is not None else None
+
+
+def _one_of(value, table, name):
+    if value not in table:
+        raise RuntimeError(f"{name}: {value!r}, expected {' or '.join(str(k) for k in table)}")
+    return table[value]
 
 
 def mxfp4_quantize_act(x, fmt="e4m3"):
@@ -389,12 +434,161 @@ def moe_grouped_mxfp4_gemm_combine(q, q_scale, act_fmt, T, topk, expert_offsets,
     return h[:R], h_scale[:R], out[:T]
 
 
+def moe_grouped_gemm_w4a16(a, expert_offsets, w, w_scale, fmt="mxfp4", sorted_pair=None, topk=1, swiglu=False,
+                           out_dtype=torch.bfloat16, out=None):
+    """Ragged grouped GEMM of bf16 activations with FP4 expert weights: rows expert_offsets[e] ..
+    expert_offsets[e + 1] of the result are a's rows times expert e's weights. w [E][N][K/2] uint8, w_scale
+    [E][N][K/32] (fmt "mxfp4") or [E][N][K/16] (fmt "nvfp4") uint8. a [R][K], or with sorted_pair [R] (from
+    moe_route_permute) a [R/topk][K] and row r reads a[sorted_pair[r] // topk]. swiglu: the first N/2 weight rows
+    are gate rows and the result is silu(gate) * up. Returns y [R][N] or [R][N/2]; with `out` given, rows outside
+    every expert keep what it holds (in a new tensor they are uninitialised)."""
+    dev = _dev_all(a, expert_offsets, w, w_scale, sorted_pair, out)
+    if a.dim() != 2 or w.dim() != 3:
+        raise RuntimeError("a must be [rows][K] and w [E][N][K/2]")
+    rows, K = a.shape
+    E, N, _ = w.shape
+    f = _one_of(fmt, WEIGHT_FMTS, "fmt")
+    R = rows * topk if sorted_pair is not None else rows
+    _need(a, "a", torch.bfloat16, (rows, K))
+    _need(expert_offsets, "expert_offsets", torch.int32, (E + 1,))
+    _need(w, "w", torch.uint8, (E, N, K // 2))
+    _need(w_scale, "w_scale", torch.uint8, (E, N, K // (16 if f else 32)))
+    if sorted_pair is not None:
+        _need(sorted_pair, "sorted_pair", torch.int32, (R,))
+    shape = (R, N // 2 if swiglu else N)
+    if out is None:
+        _one_of(out_dtype, DTYPES, "out_dtype")
+        out = torch.empty(shape, dtype=out_dtype, device=dev)
+    else:
+        _need(out, "out", (torch.float32, torch.bfloat16), shape)
+    _call("moe_grouped_gemm_w4a16", dev, a.data_ptr(), rows, R, _at(sorted_pair), topk, expert_offsets.data_ptr(), E, N,
+          K, f, w.data_ptr(), w_scale.data_ptr(), int(swiglu), out.data_ptr(), DTYPES[out.dtype])
+    return out
+
+
+def fp4_gemm_w4a16_lora(a, w, w_scale, seg_offsets, seg_adapter, lora_a, lora_b, scaling, fmt="mxfp4",
+                        out_dtype=torch.float32, out=None, workspace=None):
+    """A shared FP4 projection with low-rank adapters of many requests: a [M][K] bf16, w and w_scale as for
+    fp4_gemm_w4a16, segment s (rows seg_offsets[s] .. seg_offsets[s + 1]) adds
+    scaling[l] * (a lora_a[l]^T) lora_b[l]^T of its adapter l = seg_adapter[s]; a negative l, and rows in no
+    segment, get the projection alone. seg_offsets [S+1], seg_adapter [S] int32; lora_a [L][rank][K], lora_b
+    [L][N][rank] bf16; scaling [L] fp32. Returns c [M][N] in out_dtype (fp32 or bf16)."""
+    dev = _dev_all(a, w, w_scale, seg_offsets, seg_adapter, lora_a, lora_b, scaling, out, workspace)
+    if a.dim() != 2 or w.dim() != 2 or lora_a.dim() != 3 or seg_adapter.dim() != 1:
+        raise RuntimeError("a must be [M][K], w [N][K/2], lora_a [L][rank][K] and seg_adapter [S]")
+    M, K = a.shape
+    N = w.shape[0]
+    L, rank, _ = lora_a.shape
+    S = seg_adapter.shape[0]
+    f = _one_of(fmt, WEIGHT_FMTS, "fmt")
+    _need(a, "a", torch.bfloat16, (M, K))
+    _need(w, "w", torch.uint8, (N, K // 2))
+    _need(w_scale, "w_scale", torch.uint8, (N, K // (16 if f else 32)))
+    _need(seg_offsets, "seg_offsets", torch.int32, (S + 1,))
+    _need(seg_adapter, "seg_adapter", torch.int32, (S,))
+    _need(lora_a, "lora_a", torch.bfloat16, (L, rank, K))
+    _need(lora_b, "lora_b", torch.bfloat16, (L, N, rank))
+    _need(scaling, "scaling", torch.float32, (L,))
+    if out is None:
+        _one_of(out_dtype, DTYPES, "out_dtype")
+        out = torch.empty((M, N), dtype=out_dtype, device=dev)
+    else:
+        _need(out, "out", (torch.float32, torch.bfloat16), (M, N))
+    need = load().fp4_w4a16_lora_workspace_bytes(M, N, K, rank)
+    if workspace is None:
+        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+    else:
+        _need(workspace, "workspace", torch.uint8, ((">=", need),))
+    _call("fp4_gemm_w4a16_lora", dev, a.data_ptr(), M, N, K, f, w.data_ptr(), w_scale.data_ptr(), _at(seg_offsets),
+          _at(seg_adapter), S, _at(lora_a), _at(lora_b), _at(scaling), L, rank, out.data_ptr(), DTYPES[out.dtype],
+          workspace.data_ptr(), workspace.numel())
+    return out
+
+
+def moe_block_norm(y, x=None, post_weight=None, gate=None, residual_scale=1.0, pre_weight=None, eps=1e-6, act_fmt=None,
+                   want_r=True, want_n=True, n_dtype=torch.bfloat16, expert_gates=None, pair_row=None, r_dtype=None,
+                   r=None):
+    """The step between two blocks: r = residual_scale * x + gate * postnorm(y), n = prenorm(r), optionally its MX
+    quantisation. y [T][H] bf16/fp32, or with expert_gates [T][topk] fp32 and pair_row [T*topk] int32 the expert
+    rows [rows][H] that moe_unpermute_combine would sum (entries of pair_row outside them add nothing). x [T][H]
+    bf16/fp32 (None: no residual); post_weight [H] (None: no post-norm), pre_weight [H] (None: ones), fp32 or
+    bf16, both alike; gate [H], [T][1] or [T][H] bf16/fp32. RMS norms: v / sqrt(mean(v^2) + eps) * weight.
+    act_fmt "e4m3" / "e2m1" also quantises n (from fp32) as mxfp4_quantize_act. `r` may be given as the output
+    (x itself: updated in place). Returns a dict of r (x's dtype, without x r_dtype or y's), n (n_dtype), q and
+    q_scale; what is not wanted is None."""
+    dev = _dev_all(y, x, post_weight, gate, pre_weight, expert_gates, pair_row, r)
+    if y.dim() != 2:
+        raise RuntimeError("y must be 2-d [rows][H]")
+    floats = (torch.bfloat16, torch.float32)
+    y_rows, H = y.shape
+    _need(y, "y", floats, (y_rows, H))
+    topk = 0
+    T = y_rows
+    if (expert_gates is None) != (pair_row is None):
+        raise RuntimeError("expert_gates and pair_row go together")
+    if expert_gates is not None:
+        if expert_gates.dim() != 2 or expert_gates.shape[1] < 1:
+            raise RuntimeError("expert_gates must be [T][topk]")
+        T, topk = expert_gates.shape
+        _need(expert_gates, "expert_gates", torch.float32, (T, topk))
+        _need(pair_row, "pair_row", torch.int32, (T * topk,))
+    if x is not None:
+        _need(x, "x", floats, (T, H))
+        r_dtype = x.dtype
+    elif r_dtype is None:
+        r_dtype = y.dtype if r is None else r.dtype
+    x_dtype = _one_of(r_dtype, DTYPES, "r_dtype")
+    w_dtype = torch.float32
+    for name, t in (("post_weight", post_weight), ("pre_weight", pre_weight)):
+        if t is not None:
+            _need(t, name, floats, (H,))
+            w_dtype = t.dtype
+    if post_weight is not None and post_weight.dtype != w_dtype:
+        raise RuntimeError(f"post_weight is {post_weight.dtype} and pre_weight {w_dtype}, expected one dtype")
+    mode, g_dtype = 0, torch.float32
+    if gate is not None:
+        g_dtype = gate.dtype
+        if gate.dim() == 1:
+            mode = 1
+        elif gate.dim() == 2 and gate.shape[1] == 1 and H != 1:
+            mode = 2
+        else:
+            mode = 3
+        _need(gate, "gate", floats, {1: (H,), 2: (T, 1), 3: (T, H)}[mode])
+    fmt = None if act_fmt is None else _one_of(act_fmt, FMTS, "act_fmt")
+    if r is not None:
+        _need(r, "r", r_dtype, (T, H))
+    elif want_r:
+        r = torch.empty((T, H), dtype=r_dtype, device=dev)
+    n_code = _one_of(n_dtype, DTYPES, "n_dtype")
+    n = torch.empty((T, H), dtype=n_dtype, device=dev) if want_n else None
+    q = qs = None
+    if fmt is not None:
+        q = torch.empty((T, H // 2 if fmt == MXF_E2M1 else H), dtype=torch.uint8, device=dev)
+        qs = torch.empty((T, H // 32), dtype=torch.uint8, device=dev)
+    _call("moe_block_norm", dev, y.data_ptr(), DTYPES[y.dtype], y_rows, _at(expert_gates), _at(pair_row), topk, T, H,
+          _at(x), x_dtype, residual_scale, _at(post_weight), _at(pre_weight), DTYPES[w_dtype], eps, _at(gate),
+          DTYPES[g_dtype], mode, _at(r), _at(n), n_code, fmt or 0, _at(q), _at(qs))
+    return dict(r=r, n=n, q=q, q_scale=qs)
+
+
 def moe_layer(x, logits, w1, w1_scale, w2, w2_scale, topk, act_fmt="e4m3", y_dtype=torch.bfloat16,
               out_dtype=torch.bfloat16, fused=False):
     """The whole expert layer through the C-ABI calls (one stream, no host sync).
     fused=True (T <= 64): quantisation and routing in one launch (E <= 256), FC2 and
-    the combine in one kernel; y is not formed (None)."""
+    the combine in one kernel; y is not formed (None).
+    act_fmt="bf16": the activations enter the expert products as they are (no
+    quantisation: q, q_scale and h_scale are None, h is bf16)."""
     T = x.shape[0]
+    if act_fmt == "bf16":
+        if fused:
+            raise RuntimeError("fused: the bf16 layer has no fused form")
+        ids, gates, offs, sp, pr = moe_route_permute(logits, topk)
+        h = moe_grouped_gemm_w4a16(x, offs, w1, w1_scale, sorted_pair=sp, topk=topk, swiglu=True)
+        y = moe_grouped_gemm_w4a16(h, offs, w2, w2_scale, out_dtype=y_dtype)
+        out = moe_unpermute_combine(y, gates, pr, T, topk, out_dtype)
+        return dict(q=None, q_scale=None, topk_ids=ids, gates=gates, expert_offsets=offs, sorted_pair=sp, pair_row=pr,
+                    h=h, h_scale=None, y=y, out=out)
     if fused and logits.shape[1] <= 256:
         q, qs, ids, gates, offs, sp, pr = moe_quantize_route(x, logits, topk, act_fmt)
     else:

@@ -1,0 +1,133 @@
+"""GPU parity of fp4_gemm_w4a16_lora against the formula in 64 bits.
+
+Tolerance, from arithmetic: the projection is off by (K / 16 + 32) 2^-23 sum |a w| (weights and
+products exact, see test_gpu_w4a16_grouped.py) and by 2^-24 for each of its K slices' sums. The low-rank product
+of the first factor is off by the same with sum |a A|, scaled, plus one rounding; through the
+second factor that is sum_r dlow |B|, to which come 2^-16 of sum |low B| where low is split into two
+bf16 terms (each rounds by 2^-8 of what it holds) and (rank + 32) 2^-23 of it for the sum."""
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from mxfp4_block_scaled_amd import datagen as dg
+from mxfp4_block_scaled_amd import ops
+from tests.test_gpu_w4a16_grouped import weights
+
+pytestmark = pytest.mark.gpu
+
+
+def adapters(L, rank, N, K, seed):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(L, rank, K, generator=g).mul(K ** -0.5).to(torch.bfloat16),
+            torch.randn(L, N, rank, generator=g).to(torch.bfloat16), torch.rand(L, generator=g) + 0.5)
+
+
+def reference(a, hat, offs, adapter, la, lb, scaling):
+    K, rank = a.shape[1], la.shape[1]
+    x = a.double()
+    c = (K / 16 + 32) * 2.0 ** -23
+    y = x @ hat.T
+    d = (c + 32 * 2.0 ** -24) * (x.abs() @ hat.abs().T)
+    for s, l in enumerate(adapter):
+        if not 0 <= l < la.shape[0]:
+            continue
+        rows = slice(max(offs[s], 0), max(offs[s + 1], 0))
+        A, B, sc = la[l].double(), lb[l].double(), float(scaling[l])
+        low = sc * (x[rows] @ A.T)
+        dlow = abs(sc) * (c + 16 * 2.0 ** -24) * (x[rows].abs() @ A.abs().T) + 2.0 ** -23 * low.abs()
+        y[rows] += low @ B.T
+        d[rows] += dlow @ B.abs().T + (2.0 ** -16 + (rank + 32) * 2.0 ** -23) * (low.abs() @ B.abs().T)
+    return y, d
+
+
+def close(got, want, d):
+    half = 2.0 ** -8 if got.dtype == torch.bfloat16 else 2.0 ** -24
+    err, lim = (got.cpu().double() - want).abs(), d + half * (want.abs() + d)
+    assert (err <= lim).all(), f"error {float((err / lim).max()):.3g} of its bound"
+
+
+def bf16(seed, M, K):
+    return torch.from_numpy(dg.activations(seed, M, K).view(np.int16)).view(torch.bfloat16)
+
+
+CASES = [
+    # segment lengths; rows before and behind them; N, K, rank, L, fmt, dtype
+    ([1], 0, 0, 16, 512, 8, 1, "mxfp4", torch.float32),
+    ([1], 0, 0, 4096, 2048, 32, 3, "nvfp4", torch.bfloat16),
+    ([1] * 64, 0, 0, 272, 3584, 16, 24, "mxfp4", torch.float32),
+    ([3, 0, 20, 0, 1, 17], 2, 5, 80, 1024, 24, 4, "mxfp4", torch.float32),
+    ([64], 0, 0, 336, 512, 128, 2, "nvfp4", torch.float32),
+    ([65], 0, 0, 144, 512, 8, 2, "mxfp4", torch.float32),
+    ([1] * 70, 1, 3, 256, 512, 40, 9, "mxfp4", torch.bfloat16),
+    ([100, 0, 0, 31, 200, 1, 7], 0, 20, 528, 1536, 72, 5, "nvfp4", torch.float32),
+    ([5, 700, 60], 0, 0, 1040, 512, 64, 2, "mxfp4", torch.bfloat16),
+    ([900, 3200], 0, 4, 4352, 512, 16, 2, "mxfp4", torch.float32),  # large tiles
+    ([2049, 1, 2046], 0, 0, 4096, 512, 120, 3, "nvfp4", torch.bfloat16),
+]
+
+
+@pytest.mark.parametrize("case", CASES, ids=lambda c: f"{len(c[0])}s{sum(c[0])}r-{c[3]}x{c[4]}-r{c[5]}-{c[7]}")
+def test_against_64_bits(case):
+    lens, before, behind, N, K, rank, L, fmt, dtype = case
+    M, S = sum(lens) + before + behind, len(lens)
+    offs = [before + int(v) for v in np.cumsum([0] + lens)]
+    adapter = [(i * 7 + 1) % (L + 1) - 1 for i in range(S)]  # -1 among them
+    if S == 1:
+        adapter = [L - 1]
+    w, s, hat = weights(1, N, K, fmt, M + N)
+    la, lb, scaling = adapters(L, rank, N, K, M)
+    a = bf16(M, M, K)
+    c = ops.fp4_gemm_w4a16_lora(a.cuda(), w[0], s[0], torch.tensor(offs, dtype=torch.int32).cuda(),
+                                torch.tensor(adapter, dtype=torch.int32).cuda(), la.cuda(), lb.cuda(), scaling.cuda(),
+                                fmt, out_dtype=dtype)
+    want, d = reference(a, hat[0], offs, adapter, la, lb, scaling)
+    close(c, want, d)
+
+
+@pytest.mark.parametrize("M", [9, 130])
+def test_no_adapter_is_the_projection(M):
+    """S = 0, L = 0, every adapter -1 or outside [0, L), or segments that hold no row: the projection alone."""
+    N, K, rank = 96, 1024, 16
+    w, s, hat = weights(1, N, K, "mxfp4", 2)
+    la, lb, scaling = (t.cuda() for t in adapters(2, rank, N, K, 4))
+    a = bf16(1, M, K)
+    want, d = reference(a, hat[0], [], [], la, lb, scaling)
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32).cuda()  # noqa: E731
+    first = None
+    for offs, ad, L in (([0], [], 2), ([0, M], [-1], 2), ([0, 4, M], [2, -9], 2), ([0, M], [0], 0), ([M, M], [1], 2),
+                        ([0, 0, 0], [0, 1], 2)):
+        c = ops.fp4_gemm_w4a16_lora(a.cuda(), w[0], s[0], i32(offs), i32(ad), la[:L], lb[:L], scaling[:L])
+        close(c, want, d)
+        first = c if first is None else first
+        assert torch.equal(c, first)
+
+
+@pytest.mark.parametrize("M", [8, 200])
+def test_rows_and_adapters_stay_apart(M):
+    """NaN in one request's rows, in an adapter nobody names and in the old workspace changes no other row."""
+    N, K, rank, L = 272, 512, 24, 3
+    w, s, _ = weights(1, N, K, "mxfp4", 6)
+    la, lb, scaling = (t.cuda() for t in adapters(L, rank, N, K, 7))
+    a = bf16(2, M, K).cuda()
+    cut = M // 2 + 1
+    offs = torch.tensor([0, cut, M], dtype=torch.int32).cuda()
+    ad = torch.tensor([1, 0], dtype=torch.int32).cuda()
+    want = ops.fp4_gemm_w4a16_lora(a, w[0], s[0], offs, ad, la, lb, scaling)
+    need = ops.load().fp4_w4a16_lora_workspace_bytes(M, N, K, rank)
+    ws = torch.full((need,), 255, dtype=torch.uint8, device="cuda")
+    la[2], lb[2], scaling[2] = float("nan"), float("nan"), float("nan")
+    a[cut + 1] = float("nan")
+    got = ops.fp4_gemm_w4a16_lora(a, w[0], s[0], offs, ad, la, lb, scaling, workspace=ws)
+    keep = [t for t in range(M) if t != cut + 1]
+    assert torch.equal(got[keep], want[keep]) and torch.isnan(got[cut + 1]).all()
+
+
+def test_no_rows():
+    w, s, _ = weights(1, 32, 512, "mxfp4", 1)
+    la, lb, scaling = (t.cuda() for t in adapters(1, 8, 32, 512, 1))
+    z = torch.zeros(2, dtype=torch.int32, device="cuda")
+    c = ops.fp4_gemm_w4a16_lora(torch.empty(0, 512, dtype=torch.bfloat16, device="cuda"), w[0], s[0], z, z[:1], la, lb,
+                                scaling)
+    assert c.shape == (0, 32)

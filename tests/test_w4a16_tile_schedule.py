@@ -1,0 +1,192 @@
+"""Host replay of the tiled FP4 x bf16 kernel's copy schedule and lane layout (csrc/w4a16_tile.hip), for each tile
+shape it is built in: every copy's source and LDS bytes, coverage of a slot, what each fragment read returns (every
+row's k of the stage exactly once, the same k for both operands), the scale byte it is multiplied with, and the
+hand-over of the three slots."""
+
+import pytest
+
+SHAPES = [(256, 256, 8, False), (256, 256, 8, True), (64, 256, 4, False), (64, 256, 4, True), (64, 128, 4, False)]
+
+
+def swz_a(r):
+    return (r & 7) ^ ((r >> 3) & 1)
+
+
+def swz_b(r):
+    return (r >> 3) & 1
+
+
+def copies(BM, BN, NW):
+    """(operand, wave, lane) -> LDS byte offset and (row, 16-byte chunk of the row's stage bytes)."""
+    IA, IB = BM * 8 // 64 // NW, BN * 2 // 64 // NW
+    for wave in range(NW):
+        for q in range(IB):
+            for lane in range(64):
+                chunk = (wave * IB + q) * 64 + lane
+                r = chunk >> 1
+                yield "B", (wave * IB + q) * 1024 + 16 * lane, (r, (chunk & 1) ^ swz_b(r))
+        for q in range(IA):
+            for lane in range(64):
+                chunk = (wave * IA + q) * 64 + lane
+                r = chunk >> 3
+                yield "A", (wave * IA + q) * 1024 + 16 * lane, (r, (chunk & 7) ^ swz_a(r))
+        if wave < BN // 64:
+            for lane in range(64):
+                yield "S", wave * 256 + 4 * lane, (64 * wave + lane, 0)
+
+
+@pytest.mark.parametrize("BM,BN,NW,swiglu", SHAPES)
+def test_slot_is_filled_and_read_in_one_layout(BM, BN, NW, swiglu):
+    WMN = BM // 64
+    WNN = NW // WMN
+    FN = BN // WNN // 32
+    slot = {"A": {}, "B": {}, "S": {}}
+    for op, at, what in copies(BM, BN, NW):
+        assert at not in slot[op]
+        slot[op][at] = what
+    assert sorted(slot["A"]) == list(range(0, BM * 128, 16))
+    assert sorted(slot["B"]) == list(range(0, BN * 32, 16))
+    assert sorted(slot["S"]) == list(range(0, BN * 4, 4))
+    for name, per in (("A", 8), ("B", 2)):
+        assert sorted(slot[name].values()) == [(r, c) for r in range(len(slot[name]) // per) for c in range(per)]
+    rows_seen, cols_seen = [], []
+    for wave in range(NW):
+        wm, wn = wave // WNN, wave % WNN
+        for f in range(FN):
+            for r32 in range(32):
+                if swiglu:
+                    row = (0 if f < FN // 2 else BN // 2) + FN * 16 * wn + 32 * (f % (FN // 2)) + r32
+                else:
+                    row = 32 * (FN * wn + f) + r32
+                assert slot["S"][4 * row] == (row, 0)
+                for g in range(2):
+                    assert slot["B"][row * 32 + 16 * (g ^ swz_b(row))] == (row, g)  # the 32 codes k = 32 g + ...
+                if wm == 0:
+                    cols_seen.append(row)
+        for f in range(2):
+            for r32 in range(32):
+                r = 64 * wm + 32 * f + r32
+                if wn == 0:
+                    rows_seen.append(r)
+                for g in range(2):
+                    base = r * 128 + 16 * ((4 * g) ^ swz_a(r))
+                    for j in range(4):
+                        # MFMA j, group g: k = 32 g + 8 j + [0, 8), 16 bytes of bf16
+                        assert slot["A"][base ^ (16 * j)] == (r, 4 * g + j)
+    assert sorted(rows_seen) == list(range(BM)) and sorted(cols_seen) == list(range(BN))
+
+
+@pytest.mark.parametrize("BM,BN,NW,swiglu", SHAPES)
+def test_output_columns_are_those_of_the_weight_rows(BM, BN, NW, swiglu):
+    WNN = NW // (BM // 64)
+    FN = BN // WNN // 32
+    OF = FN // 2 if swiglu else FN
+    half = 4096
+    seen = []
+    for n_tile in (0, 3):
+        for wn in range(WNN):
+            col0 = (n_tile * BN >> (1 if swiglu else 0)) + OF * 32 * wn
+            for f in range(OF):
+                for c in range(32):
+                    def src(frag):
+                        if swiglu:
+                            r = (0 if frag < FN // 2 else BN // 2) + FN * 16 * wn + 32 * (frag % (FN // 2)) + c
+                            return (0 if r < BN // 2 else half - BN // 2) + n_tile * (BN // 2) + r
+                        return n_tile * BN + 32 * (FN * wn + frag) + c
+                    assert src(f) == col0 + 32 * f + c
+                    if swiglu:
+                        assert src(f + FN // 2) == half + col0 + 32 * f + c
+                    seen.append(col0 + 32 * f + c)
+    assert len(seen) == len(set(seen))
+
+
+@pytest.mark.parametrize("es", [2, 4])
+@pytest.mark.parametrize("OF", [1, 2, 4])
+def test_epilogue_staging_round_trip(OF, es):
+    """32 rows x PF fragments through 8 KB: the 8- or 16-byte runs written are what the 16-byte pieces read back."""
+    PF = 256 // (32 * es) if OF * 32 * es > 256 else OF
+    assert OF % PF == 0
+    RB, NCH = PF * 32 * es, PF * 32 * es // 16
+    assert 32 * RB <= 8192
+    lds = {}
+    for r in range(32):
+        for f in range(PF):
+            for j in range(4):
+                for g in range(2):
+                    cols = [32 * f + 8 * j + 4 * g + i for i in range(4)]
+                    if es == 2:
+                        at = RB * r + 16 * ((4 * f + j) ^ (r & (NCH - 1))) + 8 * g
+                    else:
+                        at = RB * r + 16 * ((8 * f + 2 * j + g) ^ (r & (NCH - 1)))
+                    for i, c in enumerate(cols):
+                        assert at + i * es not in lds
+                        lds[at + i * es] = (r, c)
+    for k in range(NCH // 2):
+        for lane in range(64):
+            idx = lane + 64 * k
+            rr, c = idx // NCH, idx % NCH
+            got = [lds[RB * rr + 16 * (c ^ (rr & (NCH - 1))) + i * es] for i in range(16 // es)]
+            assert got == [(rr, c * (16 // es) + i) for i in range(16 // es)]
+    assert 64 * (NCH // 2) == 32 * NCH
+
+
+@pytest.mark.parametrize("nst", [2, 4, 6, 32, 112])
+@pytest.mark.parametrize("per", [6, 7, 9])  # copies of a wave per stage
+def test_slots_are_handed_over(nst, per):
+    """A slot is computed only after its stage's copies landed and refilled only after every wave is done with it."""
+    issued, holds = 0, {}
+    outstanding = []  # stages in issue order, `per` copies each
+
+    def issue(st):
+        nonlocal issued
+        assert st == issued
+        issued += 1
+        holds[st % 3] = st
+        outstanding.extend([st] * per)
+
+    issue(0)
+    if nst > 1:
+        issue(1)
+    for st in range(nst):
+        allowed = per if st + 1 < nst else 0
+        del outstanding[:max(0, len(outstanding) - allowed)]
+        assert st not in outstanding  # this wave's copies of the stage have landed before the barrier
+        # after the barrier every wave is past stage st - 1: its slot may be refilled
+        if st + 2 < nst:
+            assert (st + 2) % 3 == (st - 1) % 3
+            issue(st + 2)
+        assert holds[st % 3] == st
+    assert issued == nst and not outstanding
+
+
+@pytest.mark.parametrize("nv", [False, True])
+def test_scale_bytes(nv):
+    """Stage st of 64 k copies the row's scale dword that holds the scales of its two 32-k groups."""
+    for st in range(8):
+        dword = st if nv else st >> 1
+        for g in range(2):
+            for k in range(0, 32, 8):
+                byte = 16 * g // 8 + (k // 16) if nv else 2 * (st & 1) + g
+                per = 16 if nv else 32
+                assert 4 * dword + byte == (64 * st + 32 * g + k) // per
+
+
+def first_segment(ends, S, t):
+    """The kernel's 64-way search over seg_off[1:]."""
+    lo, hi = 0, S
+    while lo < hi:
+        step = (hi - lo + 63) // 64
+        p = [lo + lane * step < hi and ends[lo + lane * step] > t for lane in range(64)]
+        probes = (hi - lo + step - 1) // step
+        f = p.index(True) if any(p) else probes
+        lo, hi = (lo if f == 0 else lo + (f - 1) * step + 1), (hi if f == probes else lo + f * step)
+        if step == 1:
+            break
+    return lo
+
+
+@pytest.mark.parametrize("S", [0, 1, 2, 63, 64, 65, 130, 4097])
+def test_segment_search(S):
+    ends = [(i * 5) // 3 for i in range(S)]  # some empty
+    for t in range(-1, (ends[-1] if S else 0) + 2):
+        assert first_segment(ends, S, t) == next((s for s in range(S) if ends[s] > t), S)
