@@ -18,89 +18,127 @@ namespace {
 constexpr int kStgStride = 1152;  // odd load instructions 128 B (mod 256) apart
 constexpr int kStgBytes = 4 * kStgStride;
 
+// A wave's LDS: one weight fragment on its way into the lane layout (afterwards the wave's
+// partial sums), one step's activations, the super-step's scales
+template <bool kNV>
+struct alignas(16) W16StreamLds {
+  uint8_t w[kStgBytes];
+  uint8_t a[16 * 256];
+  uint8_t s[64 * (kNV ? 32 : 16)];
+};
+
 template <bool kNV, bool kSwiglu, bool kOutBF16>
-__global__ void __launch_bounds__(256) w16_stream_kernel(W16TileArgs a) {
-  __shared__ v4i lds[4][4 * kStgBytes / 16];  // >= 4 KB per wave for the partial sums
+__global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(kNV ? 2 : 3))) w16_stream_kernel(W16TileArgs a) {
+  __shared__ W16StreamLds<kNV> lds[4];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lane = threadIdx.x & 63, g = lane >> 4, r16 = lane & 15;
   int e, n_tile, m;
   int64_t row0;
-  if (!w16_item<0>(a.offsets, a.E, a.R, a.min_rows, a.max_rows, a.ntiles, (int)(blockIdx.x & 7u),
-                   (int)(blockIdx.x >> 3), e, n_tile, row0, m))
+  if (!w16_item<16>(a.offsets, a.E, a.R, a.min_rows, a.max_rows, a.ntiles, (int)(blockIdx.x & 7u),
+                    (int)(blockIdx.x >> 3), e, n_tile, row0, m))
     return;
   const int64_t K = a.K, N = a.N, half = N / 2, wrow = K / 2, srow = kNV ? K / 16 : K / 32;
 
   // four 16-row weight fragments; those past the end read the first one again (not stored)
   const int64_t i0 = (int64_t)n_tile * (kSwiglu ? 32 : 64);
   const int64_t ocols = kSwiglu ? half : N;
-  int64_t frow[4];
-#pragma unroll
-  for (int f = 0; f < 4; ++f) {
+  auto frag_row = [&](int f) -> int64_t {
     const int64_t c = i0 + 16 * (kSwiglu ? f & 1 : f);
-    frow[f] = (c < ocols ? c : i0) + (kSwiglu && f >= 2 ? half : 0);
-  }
-  buf_rsrc wr[4], sr[4];
-#pragma unroll
-  for (int f = 0; f < 4; ++f) {
-    wr[f] = make_rsrc(a.w + ((int64_t)e * N + frow[f]) * wrow, (uint32_t)(16 * wrow));
-    sr[f] = make_rsrc(a.ws + ((int64_t)e * N + frow[f]) * srow, (uint32_t)(16 * srow));
-  }
+    return (c < ocols ? c : i0) + (kSwiglu && f >= 2 ? half : 0);
+  };
+  const buf_rsrc wr = make_rsrc(a.w + (int64_t)e * N * wrow, (uint32_t)(N * wrow));
+  const buf_rsrc sr = make_rsrc(a.ws + (int64_t)e * N * srow, (uint32_t)(N * srow));
   const int q = lane >> 3, rot = ((lane & 7) + q) & 7;
   const uint32_t wvoff = (uint32_t)(q * wrow + 16 * rot);
-  const uint32_t svoff = (uint32_t)(r16 * srow);
-  uint8_t* const stg = reinterpret_cast<uint8_t*>(&lds[wave][0]);
+  const uint32_t svoff = (uint32_t)(frag_row(g) * srow + r16 * srow);  // lane 16 f + r: row r of fragment f
+  uint8_t *const stg = lds[wave].w, *const sta = lds[wave].a, *const sts = lds[wave].s;
   int rd[4];
 #pragma unroll
   for (int s = 0; s < 4; ++s)
     rd[s] = (2 * (s >> 1) + (r16 >> 3)) * kStgStride + 128 * (r16 & 7) + 16 * ((4 * s + g - (r16 & 7)) & 7);
-  // rows past m repeat row m - 1 (not stored)
-  int64_t src = row0 + min(r16, m - 1);
-  if (a.pair) src = min((int64_t)((uint32_t)a.pair[src] / (uint32_t)a.topk), a.a_rows - 1);
-  const uint16_t* const ap = a.a + src * K + 32 * g;
+  // activations: a load covers 4 rows x 256 bytes (a step's 128 k); rows past m read as zero
+  const buf_rsrc ar = a.pair ? make_rsrc(a.a, (uint32_t)(a.a_rows * K * 2))
+                             : make_rsrc(a.a + row0 * K, (uint32_t)((int64_t)m * K * 2));
+  const bool few = m <= 4;
+  int pr[4];  // looked at after the first weight loads have gone out
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = 4 * i + g;
+    pr[i] = a.pair && r < m ? a.pair[row0 + r] : -1;
+  }
+  const int arow = min(r16, m - 1);
 
   v4f acc[4];
 #pragma unroll
   for (int f = 0; f < 4; ++f) acc[f] = v4f{0.f, 0.f, 0.f, 0.f};
   const int nss = (int)cdiv(K, 512);
   const int ss_begin = wave * nss / 4, ss_end = (wave + 1) * nss / 4;
+  constexpr int SH = kNV ? 2 : 1;  // 16-byte pieces of a row's scale bytes per super-step
   for (int ss = ss_begin; ss < ss_end; ++ss) {
     const int steps = min(4, (int)(K / 128) - 4 * ss);  // 128-k steps of the super-step
-    v4i raw[4][4];
-    uint32_t sd[4][kNV ? 8 : 4];  // the row's scale bytes of the super-step, a dword per step (MXFP4) or half step
+    // every weight line and scale of the super-step is in flight before any wait (scale
+    // bytes past the last row's end read as zero, dword by dword: a step past K is not run)
+    v4i raw[4][4], sd[SH], ax[4];
 #pragma unroll
-    for (int f = 0; f < 4; ++f) {
-      constexpr int SD = kNV ? 8 : 4;
+    for (int h = 0; h < SH; ++h) sd[h] = buf_load16(sr, svoff, (uint32_t)(ss * 16 * SH + 16 * h));
 #pragma unroll
-      for (int h = 0; h < SD; ++h) sd[f][h] = (uint32_t)buf_load4(sr[f], svoff, (uint32_t)(ss * 4 * SD + 4 * h));
+    for (int f = 0; f < 4; ++f)
 #pragma unroll
       for (int s = 0; s < 4; ++s)
-        raw[f][s] = buf_load16_nt(wr[f], wvoff + 128 * (s >> 1), (uint32_t)(8 * (s & 1) * wrow + ss * 256));
+        raw[f][s] = buf_load16_nt(wr, wvoff + 128 * (s >> 1),
+                                  (uint32_t)((frag_row(f) + 8 * (s & 1)) * wrow + ss * 256));
+    __builtin_amdgcn_sched_barrier(0);
+    auto avoff = [&](int i) -> uint32_t {
+      const uint32_t src = a.pair ? min((uint32_t)pr[i] / (uint32_t)a.topk, (uint32_t)a.a_rows) : (uint32_t)(4 * i + g);
+      return src * (uint32_t)(2 * K) + 16 * r16;
+    };
+    // at most 4 rows: a load per step, all of them now; else the rows of step 0
+    if (few) {
+#pragma unroll
+      for (int s = 0; s < 4; ++s) ax[s] = buf_load16(ar, avoff(0), (uint32_t)(ss * 1024 + 256 * s));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) ax[i] = buf_load16(ar, avoff(i), (uint32_t)(ss * 1024));
     }
     __builtin_amdgcn_sched_barrier(0);
+    // a wave's LDS operations run in order: one area serves the fragments in turn
+#pragma unroll
+    for (int h = 0; h < SH; ++h) *reinterpret_cast<v4i*>(sts + 16 * (SH * lane + h)) = sd[h];
     v4i b[4][4];
 #pragma unroll
     for (int f = 0; f < 4; ++f) {
-      uint8_t* const area = stg + f * kStgBytes;
 #pragma unroll
-      for (int s = 0; s < 4; ++s) *reinterpret_cast<v4i*>(area + s * kStgStride + 16 * lane) = raw[f][s];
+      for (int s = 0; s < 4; ++s) *reinterpret_cast<v4i*>(stg + s * kStgStride + 16 * lane) = raw[f][s];
 #pragma unroll
-      for (int s = 0; s < 4; ++s) b[f][s] = *reinterpret_cast<const v4i*>(area + rd[s]);
+      for (int s = 0; s < 4; ++s) b[f][s] = *reinterpret_cast<const v4i*>(stg + rd[s]);
     }
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
       if (s >= steps) break;
+      // row r's 16-byte chunk c sits at chunk c ^ r of its 256 bytes: no bank conflicts
+      if (few) {
+        *reinterpret_cast<v4i*>(sta + 256 * g + 16 * (r16 ^ g)) = ax[s];
+      } else {
+        if (s > 0) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) ax[i] = buf_load16(ar, avoff(i), (uint32_t)(ss * 1024 + 256 * s));
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          *reinterpret_cast<v4i*>(sta + 256 * (4 * i + g) + 16 * (r16 ^ (4 * i + g))) = ax[i];
+      }
       v4i av[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) av[j] = *reinterpret_cast<const v4i*>(ap + (int64_t)ss * 512 + 128 * s + 8 * j);
+      for (int j = 0; j < 4; ++j) av[j] = *reinterpret_cast<const v4i*>(sta + 256 * arow + 16 * ((4 * g + j) ^ arow));
 #pragma unroll
       for (int f = 0; f < 4; ++f) {
         float sc[2];
+        const uint32_t dw = *reinterpret_cast<const uint32_t*>(sts + 16 * SH * (16 * f + r16) + 4 * SH * s + (kNV ? 4 * (g >> 1) : 0));
         if constexpr (kNV) {
-          const uint32_t dw = sd[f][2 * s + (g >> 1)] >> (16 * (g & 1));
-          sc[0] = ue4m3_to_f32(dw & 0xFFu);
-          sc[1] = ue4m3_to_f32((dw >> 8) & 0xFFu);
+          sc[0] = ue4m3_to_f32((dw >> (16 * (g & 1))) & 0xFFu);
+          sc[1] = ue4m3_to_f32((dw >> (16 * (g & 1) + 8)) & 0xFFu);
         } else {
-          sc[0] = sc[1] = ue8m0_to_f32((sd[f][s] >> (8 * g)) & 0xFFu);
+          sc[0] = sc[1] = ue8m0_to_f32((dw >> (8 * g)) & 0xFFu);
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -115,13 +153,13 @@ __global__ void __launch_bounds__(256) w16_stream_kernel(W16TileArgs a) {
 #pragma unroll
   for (int f = 0; f < 4; ++f)
 #pragma unroll
-    for (int v = 0; v < 4; ++v) reinterpret_cast<float*>(&lds[wave][0])[(4 * v + f) * 64 + lane] = acc[f][v];
+    for (int v = 0; v < 4; ++v) reinterpret_cast<float*>(stg)[(4 * v + f) * 64 + lane] = acc[f][v];
   __syncthreads();
-  constexpr int kW = 4 * kStgBytes / 4;
+  constexpr int kW = sizeof(W16StreamLds<kNV>) / 4;
   float tot[4];
 #pragma unroll
   for (int f = 0; f < 4; ++f) {
-    const float* r = reinterpret_cast<const float*>(&lds[0][0]) + (4 * wave + f) * 64 + lane;
+    const float* r = reinterpret_cast<const float*>(lds[0].w) + (4 * wave + f) * 64 + lane;
     tot[f] = ((r[0] + r[kW]) + r[2 * kW]) + r[3 * kW];
   }
   const int lr = 4 * g + wave;
@@ -154,6 +192,10 @@ void launch_stream(W16TileArgs a, bool nv, bool swiglu, bool out_bf16, int64_t u
   else launch_stream_t<false, false>(a, out_bf16, grid, stream);
 }
 
+// calls of at most this many rows run in the streaming kernel alone (one launch), experts of
+// more than 16 rows in units of 16 that read the weights again from the cache
+constexpr int64_t kStreamRows = 128;
+
 // units that experts of lo < rows <= hi can make of R rows in all
 int64_t most_units(int64_t R, int E, int64_t lo, int bm) {
   const int64_t experts = R / (lo + 1) < E ? R / (lo + 1) : E;
@@ -166,18 +208,15 @@ int launch_w16_grouped(W16TileArgs a, bool nv, bool swiglu, bool out_bf16, hipSt
   constexpr int kAll = 0x7FFFFFFF;
   const int64_t R = a.R;
   a.min_rows = 0;
-  a.max_rows = 16;
-  launch_stream(a, nv, swiglu, out_bf16, most_units(R, a.E, 0, 0), stream);
-  if (R > 16) {
-    a.min_rows = 16;
-    a.max_rows = 64;
-    launch_w16_tile_grouped(a, nv, swiglu, out_bf16, 64, most_units(R, a.E, 16, 0), stream);
-  }
-  if (R > 64) {
-    a.min_rows = 64;
-    a.max_rows = kAll;
-    launch_w16_tile_grouped(a, nv, swiglu, out_bf16, 256, most_units(R, a.E, 64, 256), stream);
-  }
+  a.max_rows = R <= kStreamRows ? kAll : 16;
+  launch_stream(a, nv, swiglu, out_bf16, most_units(R, a.E, 0, R <= kStreamRows ? 16 : 0), stream);
+  if (R <= kStreamRows) return hipGetLastError() == hipSuccess ? 0 : -1;
+  a.min_rows = 16;
+  a.max_rows = 64;
+  launch_w16_tile_grouped(a, nv, swiglu, out_bf16, 64, most_units(R, a.E, 16, 0), stream);
+  a.min_rows = 64;
+  a.max_rows = kAll;
+  launch_w16_tile_grouped(a, nv, swiglu, out_bf16, 128, most_units(R, a.E, 64, 128), stream);
   return hipGetLastError() == hipSuccess ? 0 : -1;
 }
 

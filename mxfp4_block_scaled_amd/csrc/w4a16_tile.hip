@@ -25,18 +25,17 @@ namespace mxf {
 
 namespace {
 
-template <int BM, int BN>
-struct alignas(16) W16Slot {
-  uint8_t A[BM * 128];
-  uint8_t B[BN * 32];
-  uint8_t Bs[BN * 4];
+// LDS: NA slots of one 64-k stage of activations, two of 128 k of weight codes, two of a
+// scale group (16 scale bytes per weight row: 512 k of UE8M0 or 256 k of UE4M3)
+template <int BM, int BN, int NA>
+struct alignas(16) W16Ring {
+  uint8_t A[NA][BM * 128];
+  uint8_t B[2][BN * 64];
+  uint8_t S[2][BN * 16];
 };
-constexpr int kSlots = 3;
 
 __device__ __forceinline__ int swz_a16(int r) { return (r & 7) ^ ((r >> 3) & 1); }  // 8 chunks per row
-__device__ __forceinline__ int swz_b16(int r) { return (r >> 3) & 1; }              // 2 chunks per row
-
-typedef short v8s __attribute__((ext_vector_type(8)));
+__device__ __forceinline__ int swz_b16(int r) { return (r >> 2) & 3; }              // 4 chunks per row
 
 __device__ __forceinline__ v16f mfma32x32x16(v8bf a, v8bf b, v16f c) {
 #if defined(__HIP_DEVICE_COMPILE__)
@@ -48,32 +47,14 @@ __device__ __forceinline__ v16f mfma32x32x16(v8bf a, v8bf b, v16f c) {
 #endif
 }
 
-// first segment s whose end seg_off[s + 1] lies past row t (S if none): 64 probes a step
-__device__ __forceinline__ int first_segment(const int32_t* __restrict__ seg_off, int S, int64_t t) {
-  const int lane = threadIdx.x & 63;
-  int lo = 0, hi = S;
-  while (lo < hi) {
-    const int step = (hi - lo + 63) / 64;
-    const int64_t idx = lo + (int64_t)lane * step;
-    const bool p = idx < hi && (int64_t)seg_off[idx < hi ? idx + 1 : 0] > t;
-    const unsigned long long m = __ballot(p);
-    const int probes = (hi - lo + step - 1) / step;
-    const int f = m ? __ffsll((long long)m) - 1 : probes;  // the first probe past t
-    const int nlo = f == 0 ? lo : lo + (f - 1) * step + 1;
-    hi = f == probes ? hi : lo + f * step;
-    lo = nlo;
-    if (step == 1) break;
-  }
-  return __builtin_amdgcn_readfirstlane(lo);
-}
-
 // BM x BN per workgroup of NW waves: BM / 64 waves over rows, the others over columns
-template <int BM, int BN, int NW, bool kNV, bool kSwiglu, bool kOutBF16, bool kLora>
-__global__ void __launch_bounds__(NW * 64) w16_tile_kernel(W16TileArgs a) {
+template <int BM, int BN, int NW, int NA, bool kNV, bool kSwiglu, bool kOutBF16, bool kLora>
+__global__ void __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(2))) w16_tile_kernel(W16TileArgs a) {
   constexpr int WMN = BM / 64, WNN = NW / WMN, FN = BN / WNN / 32;
-  constexpr int IA = BM * 8 / 64 / NW, IB = BN * 2 / 64 / NW;  // 16-byte copies per lane per stage
+  constexpr int IA = BM * 8 / 64 / NW, IB = BN * 4 / 64 / NW;  // 16-byte copies per lane per 64 / 128 k
+  constexpr int P = kNV ? 4 : 8;  // stages per scale group
   static_assert(IA >= 1 && IB >= 1 && BN / 64 <= NW && (!kSwiglu || FN % 2 == 0), "tile shape");
-  __shared__ W16Slot<BM, BN> ring[kSlots];
+  __shared__ W16Ring<BM, BN, NA> ring;
   static_assert(sizeof(ring) <= 160 * 1024 && sizeof(ring) >= NW * 8192, "the epilogue stages through the ring");
 
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, g = lane >> 5,
@@ -88,10 +69,11 @@ __global__ void __launch_bounds__(NW * 64) w16_tile_kernel(W16TileArgs a) {
     if (a.offsets) {
       if (!w16_item<BM>(a.offsets, a.E, a.R, a.min_rows, a.max_rows, a.ntiles, x, j, e, n_tile, row0, m)) return;
     } else {  // the items of an n-tile are its units; 8 contiguous ranges of items, one per XCD
-      const int64_t units = (a.R + BM - 1) / BM, total = units * a.ntiles, w = x * total / 8 + j;
-      if (w >= (x + 1) * total / 8) return;
+      const uint32_t units = (uint32_t)((a.R + BM - 1) / BM), total = units * (uint32_t)a.ntiles;
+      const uint32_t w = w16_eighths(total, x) + (uint32_t)j;
+      if (w >= w16_eighths(total, x + 1)) return;
       n_tile = (int)(w / units);
-      row0 = (w % units) * BM;
+      row0 = (int64_t)(w - (uint32_t)n_tile * units) * BM;
       m = (int)min((int64_t)BM, a.R - row0);
     }
   }
@@ -110,9 +92,30 @@ __global__ void __launch_bounds__(NW * 64) w16_tile_kernel(W16TileArgs a) {
   };
   uint32_t va[IA], vb[IB];
 #pragma unroll
+  for (int q = 0; q < IB; ++q) {
+    const int chunk = (wave * IB + q) * 64 + lane, r = chunk >> 2;
+    vb[q] = (uint32_t)(b_row(r) * wrow + 16 * ((chunk & 3) ^ swz_b16(r)));
+  }
+  const bool has_sc = wave < BN / 64;
+  const uint32_t vs = (uint32_t)(b_row(64 * (has_sc ? wave : 0) + lane) * srow);
+  auto issue_a = [&](uint8_t* slot, int st) {
+#pragma unroll
+    for (int q = 0; q < IA; ++q) buf_dma16(ra, slot + (wave * IA + q) * 1024, va[q], (uint32_t)st * 128);
+  };
+  auto issue_b = [&](uint8_t* slot, int h) {
+#pragma unroll
+    for (int q = 0; q < IB; ++q) buf_dma16(rb, slot + (wave * IB + q) * 1024, vb[q], (uint32_t)h * 64);
+  };
+  auto issue_s = [&](int grp) {
+    if (has_sc) buf_dma16(rbs, &ring.S[grp & 1][wave * 1024], vs, (uint32_t)grp * 16);
+  };
+  issue_s(0);
+  issue_b(ring.B[0], 0);
+  // rows past m are past the resource
+#pragma unroll
   for (int q = 0; q < IA; ++q) {
     const int chunk = (wave * IA + q) * 64 + lane, r = chunk >> 3;
-    int64_t src = r;  // relative to row0; rows past m are past the resource
+    int64_t src = r;  // relative to row0
     if (a.pair) {
       src = a.a_rows;
       if (r < m) src = min((int64_t)((uint32_t)a.pair[row0 + r] / (uint32_t)a.topk), a.a_rows);
@@ -120,20 +123,8 @@ __global__ void __launch_bounds__(NW * 64) w16_tile_kernel(W16TileArgs a) {
     va[q] = (uint32_t)(src * K * 2 + 16 * ((chunk & 7) ^ swz_a16(r)));
   }
 #pragma unroll
-  for (int q = 0; q < IB; ++q) {
-    const int chunk = (wave * IB + q) * 64 + lane, r = chunk >> 1;
-    vb[q] = (uint32_t)(b_row(r) * wrow + 16 * ((chunk & 1) ^ swz_b16(r)));
-  }
-  const bool has_sc = wave < BN / 64;
-  const uint32_t vs = (uint32_t)(b_row(64 * (has_sc ? wave : 0) + lane) * srow);
-
-  auto issue = [&](W16Slot<BM, BN>& sl, int st) {
-#pragma unroll
-    for (int q = 0; q < IB; ++q) buf_dma16(rb, &sl.B[(wave * IB + q) * 1024], vb[q], (uint32_t)st * 32);
-    if (has_sc) buf_dma4(rbs, &sl.Bs[wave * 256], vs, (uint32_t)(kNV ? 4 * st : 4 * (st >> 1)));
-#pragma unroll
-    for (int q = 0; q < IA; ++q) buf_dma16(ra, &sl.A[(wave * IA + q) * 1024], va[q], (uint32_t)st * 128);
-  };
+  for (int st = 0; st < NA - 1; ++st)
+    if (st < nst) issue_a(ring.A[st], st);
 
   v16f acc[2][FN];
 #pragma unroll
@@ -145,7 +136,7 @@ __global__ void __launch_bounds__(NW * 64) w16_tile_kernel(W16TileArgs a) {
   for (int f = 0; f < FN; ++f) {
     if (kSwiglu) brow_l[f] = (f < FN / 2 ? 0 : BN / 2) + FN * 16 * wn + 32 * (f % (FN > 1 ? FN / 2 : 1)) + r32;
     else brow_l[f] = 32 * (FN * wn + f) + r32;
-    boff[f] = brow_l[f] * 32 + 16 * (g ^ swz_b16(brow_l[f]));
+    boff[f] = brow_l[f] * 64 + 16 * (g ^ swz_b16(brow_l[f]));
   }
 #pragma unroll
   for (int f = 0; f < 2; ++f) {
@@ -153,13 +144,17 @@ __global__ void __launch_bounds__(NW * 64) w16_tile_kernel(W16TileArgs a) {
     aoff[f] = r * 128 + 16 * ((4 * g) ^ swz_a16(r));
   }
 
-  auto compute = [&](const W16Slot<BM, BN>& sl, int st) {
+  auto compute = [&](const uint8_t* As, const uint8_t* Bs, auto Odd, int st) {
+    constexpr int odd = decltype(Odd)::value;  // stages of 128 k: blocks 0, 1 then 2, 3 of a row's codes
+    const uint8_t* const Ss = &ring.S[(st / P) & 1][4 * (kNV ? st & 3 : (st & 7) >> 1)];
     v4i b[FN], av[2][4];
     uint32_t sd[FN];
 #pragma unroll
     for (int f = 0; f < FN; ++f) {
-      sd[f] = *reinterpret_cast<const uint32_t*>(&sl.Bs[4 * brow_l[f]]);
-      b[f] = *reinterpret_cast<const v4i*>(&sl.B[boff[f]]);
+      int o = boff[f];
+      asm volatile("" : "+v"(o));
+      sd[f] = *reinterpret_cast<const uint32_t*>(Ss + 16 * brow_l[f]);
+      b[f] = *reinterpret_cast<const v4i*>(Bs + (o ^ (32 * odd)));
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j)
@@ -167,7 +162,7 @@ __global__ void __launch_bounds__(NW * 64) w16_tile_kernel(W16TileArgs a) {
       for (int f = 0; f < 2; ++f) {
         int o = aoff[f];
         asm volatile("" : "+v"(o));
-        av[f][j] = *reinterpret_cast<const v4i*>(&sl.A[o ^ (16 * j)]);
+        av[f][j] = *reinterpret_cast<const v4i*>(As + (o ^ (16 * j)));
       }
     float sc[FN][2];
 #pragma unroll
@@ -176,7 +171,7 @@ __global__ void __launch_bounds__(NW * 64) w16_tile_kernel(W16TileArgs a) {
         sc[f][0] = ue4m3_to_f32((sd[f] >> (16 * g)) & 0xFFu);
         sc[f][1] = ue4m3_to_f32((sd[f] >> (16 * g + 8)) & 0xFFu);
       } else {
-        sc[f][0] = sc[f][1] = ue8m0_to_f32((sd[f] >> (8 * (2 * (st & 1) + g))) & 0xFFu);
+        sc[f][0] = sc[f][1] = ue8m0_to_f32((sd[f] >> (8 * (2 * odd + g))) & 0xFFu);
       }
     }
 #pragma unroll
@@ -189,79 +184,112 @@ __global__ void __launch_bounds__(NW * 64) w16_tile_kernel(W16TileArgs a) {
       }
   };
   const bool active = 64 * wm < m;
-  // stage st: wait for this wave's copies of st (those of st + 1 may stay in flight), meet
-  // the others (their parts have landed too, and everyone is done with st - 1, whose slot
-  // the copies of st + 2 overwrite), issue st + 2, compute st
+  // stage st: wait for the copies it needs, meet the other waves (their parts have landed
+  // too, and everyone is done with stage st - 1), issue into what stage st - 1 freed, compute.
+  // Issue order at stage t: on even t the codes of stages t + 2, t + 3 and, every P stages,
+  // the next scale group, then the activations of t + NA - 1. So with NA == 3 only the last
+  // stage's issues may stay in flight: A, and after an even stage B (and S) before it.
   auto step = [&](auto I, int st) {
     constexpr int i = decltype(I)::value;
-    if (st + 1 < nst) {
-      if (has_sc) wait_vmcnt<IA + IB + 1>();
-      else wait_vmcnt<IA + IB>();
-    } else {
+    if (NA == 2 || st + 1 >= nst) {
       wait_vmcnt<0>();
+    } else if (i % 2 == 0) {
+      wait_vmcnt<IA>();
+    } else if (has_sc && (st - 1) % P == 0 && st - 1 + P < nst) {
+      wait_vmcnt<IA + IB + 1>();
+    } else {
+      wait_vmcnt<IA + IB>();
     }
     lds_barrier();
-    if (st + 2 < nst) issue(ring[(i + 2) % kSlots], st + 2);
+    if (i % 2 == 0 && st + 2 < nst) issue_b(ring.B[(i / 2 + 1) % 2], st / 2 + 1);
+    if (i % 2 == 0 && st % P == 0 && st + P < nst) issue_s(st / P + 1);
+    if (st + NA - 1 < nst) issue_a(ring.A[(i + NA - 1) % NA], st + NA - 1);
     __builtin_amdgcn_sched_barrier(0);
-    if (active) compute(ring[i], st);
+    if (active) compute(ring.A[i % NA], ring.B[(i / 2) % 2], std::integral_constant<int, i % 2>{}, st);
   };
-  issue(ring[0], 0);
-  if (nst > 1) issue(ring[1], 1);
-  for (int st = 0; st < nst; st += kSlots) {
-    step(std::integral_constant<int, 0>{}, st);
-    if (st + 1 < nst) step(std::integral_constant<int, 1>{}, st + 1);
-    if (st + 2 < nst) step(std::integral_constant<int, 2>{}, st + 2);
-  }
+  constexpr int U = NA == 3 ? 12 : 4;  // whole turns of the A and B slots
+  for (int st = 0; st < nst; st += U)  // nst is even
+    static_for<0, U / 2>([&](auto X_) {
+      constexpr int X = 2 * decltype(X_)::value;
+      if (st + X < nst) {
+        step(std::integral_constant<int, X>{}, st + X);
+        step(std::integral_constant<int, X + 1>{}, st + X + 1);
+      }
+    });
 
   // adapters: for each segment with rows here, acc += low . lora_b^T over the rank, low
-  // (scaled, fp32) split into two bf16 terms (16 significant bits: the adapter's share
-  // keeps an error of 2^-17 of itself)
+  // (scaled, fp32) held as two bf16 terms (16 significant bits: the adapter's share keeps an
+  // error of 2^-16 of itself). 64 segments' bounds and adapters are read at once, and the
+  // operands of the next 16 ranks are loaded before the current ones are multiplied, so that
+  // many short segments cost their loads and not their latency.
   if (kLora && active) {
     const int64_t rlo = row0 + 64 * wm, rhi = min(rlo + 64, row0 + m);
-    for (int s = first_segment(a.seg_off, a.S, rlo); s < a.S; ++s) {
-      const int64_t lo = a.seg_off[s], hi = a.seg_off[s + 1];
-      if (lo >= rhi) break;
-      const int l = a.seg_adapter[s];
-      if (l < 0 || l >= a.L || hi <= rlo) continue;
-      for (int k0 = 0; k0 < a.rank; k0 += 16) {
-        const int k = k0 + 8 * g;
-        v8bf xh[2], xl[2], bw[FN];
+    int s0 = first_segment(a.seg_off, a.S, rlo);
+    int lo_l = 0, hi_l = 0, l_l = 0, k_next = a.rank;
+    int lo = 0, hi = 0, l = 0;  // the segment of the operands to load, relative to rlo
+    unsigned long long mask = 0;
+    bool more = s0 < a.S;
+    auto advance = [&]() -> bool {  // the next 16 ranks: of the same segment, or the next one's first
+      k_next += 16;
+      if (k_next < a.rank) return true;
+      while (mask == 0) {
+        if (!more) return false;
+        const int s = s0 + lane;
+        const bool in = s < a.S;
+        const int64_t b0 = a.seg_off[in ? s : 0], b1 = a.seg_off[in ? s + 1 : 0];
+        l_l = in ? a.seg_adapter[s] : -1;
+        lo_l = (int)(max(b0, rlo) - rlo);
+        hi_l = (int)(min(b1, rhi) - rlo);
+        mask = __ballot(in && b0 < rhi && b1 > rlo && hi_l > lo_l && l_l >= 0 && l_l < a.L);
+        s0 += 64;
+        more = s0 < a.S && __ballot(in && b0 >= rhi) == 0;
+      }
+      const int i = __ffsll((long long)mask) - 1;
+      mask &= mask - 1;
+      lo = __builtin_amdgcn_readlane(lo_l, i);
+      hi = __builtin_amdgcn_readlane(hi_l, i);
+      l = __builtin_amdgcn_readlane(l_l, i);
+      k_next = 0;
+      return true;
+    };
+    struct Ops {
+      v4i h[2], lo[2], b[FN];
+    };
+    auto load = [&](Ops& o) {
+      const int k = k_next + 8 * g;
+      const bool kin = k < a.rank;
+#pragma unroll
+      for (int fm = 0; fm < 2; ++fm) {
+        const int t = 32 * fm + r32;
+        const bool ok = t >= lo && t < hi && kin;
+        const int64_t at = ok ? (rlo + t) * a.rank + k : 0;
+        o.h[fm] = *reinterpret_cast<const v4i*>(a.low_hi + at);
+        o.lo[fm] = *reinterpret_cast<const v4i*>(a.low_lo + at);
+        if (!ok) o.h[fm] = o.lo[fm] = v4i{};
+      }
+#pragma unroll
+      for (int f = 0; f < FN; ++f) {
+        const int64_t n = min((int64_t)n_tile * BN + brow_l[f], N - 1);
+        o.b[f] = *reinterpret_cast<const v4i*>(a.lora_b + ((int64_t)l * N + n) * a.rank + (kin ? k : 0));
+        if (!kin) o.b[f] = v4i{};
+      }
+    };
+    Ops cur, nxt;
+    bool have = advance();
+    if (have) load(cur);
+    while (have) {
+      const bool next = advance();
+      if (next) load(nxt);
+#pragma unroll
+      for (int f = 0; f < FN; ++f)
 #pragma unroll
         for (int fm = 0; fm < 2; ++fm) {
-          const int64_t t = rlo + 32 * fm + r32;
-          const bool ok = t >= lo && t < hi && t < rhi && k < a.rank;
-          float x[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) x[i] = 0.0f;
-          if (ok) {
-            for (int sl = 0; sl < a.nslice; ++sl) {
-              const float4* p = reinterpret_cast<const float4*>(a.low + ((int64_t)sl * a.R + t) * a.rank + k);
-              const float4 u = p[0], w = p[1];
-              x[0] += u.x, x[1] += u.y, x[2] += u.z, x[3] += u.w;
-              x[4] += w.x, x[5] += w.y, x[6] += w.z, x[7] += w.w;
-            }
-          }
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            xh[fm][i] = (__bf16)x[i];
-            xl[fm][i] = (__bf16)(x[i] - (float)xh[fm][i]);
-          }
+          const v8bf bw = __builtin_bit_cast(v8bf, cur.b[f]);
+          acc[fm][f] = mfma32x32x16(bw, __builtin_bit_cast(v8bf, cur.lo[fm]), acc[fm][f]);
+          acc[fm][f] = mfma32x32x16(bw, __builtin_bit_cast(v8bf, cur.h[fm]), acc[fm][f]);
         }
-#pragma unroll
-        for (int f = 0; f < FN; ++f) {
-          const int64_t n = min((int64_t)n_tile * BN + brow_l[f], N - 1);
-          v4i w = v4i{};
-          if (k < a.rank) w = *reinterpret_cast<const v4i*>(a.lora_b + ((int64_t)l * N + n) * a.rank + k);
-          bw[f] = __builtin_bit_cast(v8bf, w);
-        }
-#pragma unroll
-        for (int f = 0; f < FN; ++f)
-#pragma unroll
-          for (int fm = 0; fm < 2; ++fm) {
-            acc[fm][f] = mfma32x32x16(bw[f], xl[fm], acc[fm][f]);
-            acc[fm][f] = mfma32x32x16(bw[f], xh[fm], acc[fm][f]);
-          }
-      }
+      cur = nxt;
+      have = next;
     }
   }
 
@@ -273,7 +301,7 @@ __global__ void __launch_bounds__(NW * 64) w16_tile_kernel(W16TileArgs a) {
   constexpr int PF = OF * 32 * ES > 256 ? 256 / (32 * ES) : OF;  // fragments per pass
   constexpr int RB = PF * 32 * ES, NCH = RB / 16;
   static_assert(OF % PF == 0, "passes");
-  uint8_t* const stg = reinterpret_cast<uint8_t*>(&ring[0]) + wave * 8192;
+  uint8_t* const stg = reinterpret_cast<uint8_t*>(&ring) + wave * 8192;
   const int64_t ocols = kSwiglu ? half : N;
   const int64_t col0 = ((int64_t)n_tile * BN >> (kSwiglu ? 1 : 0)) + OF * 32 * wn;
 #pragma unroll
@@ -314,16 +342,16 @@ __global__ void __launch_bounds__(NW * 64) w16_tile_kernel(W16TileArgs a) {
     }
 }
 
-template <int BM, int BN, int NW, bool kSwiglu, bool kLora>
+template <int BM, int BN, int NW, int NA, bool kSwiglu, bool kLora>
 void launch_shape(W16TileArgs a, bool nv, bool out_bf16, int64_t units, hipStream_t stream) {
   a.ntiles = (int)cdiv(a.N, BN);
   const dim3 grid((unsigned)(8 * cdiv(units * a.ntiles, 8))), block(NW * 64);
   if (nv) {
-    if (out_bf16) w16_tile_kernel<BM, BN, NW, true, kSwiglu, true, kLora><<<grid, block, 0, stream>>>(a);
-    else w16_tile_kernel<BM, BN, NW, true, kSwiglu, false, kLora><<<grid, block, 0, stream>>>(a);
+    if (out_bf16) w16_tile_kernel<BM, BN, NW, NA, true, kSwiglu, true, kLora><<<grid, block, 0, stream>>>(a);
+    else w16_tile_kernel<BM, BN, NW, NA, true, kSwiglu, false, kLora><<<grid, block, 0, stream>>>(a);
   } else {
-    if (out_bf16) w16_tile_kernel<BM, BN, NW, false, kSwiglu, true, kLora><<<grid, block, 0, stream>>>(a);
-    else w16_tile_kernel<BM, BN, NW, false, kSwiglu, false, kLora><<<grid, block, 0, stream>>>(a);
+    if (out_bf16) w16_tile_kernel<BM, BN, NW, NA, false, kSwiglu, true, kLora><<<grid, block, 0, stream>>>(a);
+    else w16_tile_kernel<BM, BN, NW, NA, false, kSwiglu, false, kLora><<<grid, block, 0, stream>>>(a);
   }
 }
 
@@ -332,11 +360,14 @@ void launch_shape(W16TileArgs a, bool nv, bool out_bf16, int64_t units, hipStrea
 void launch_w16_tile_grouped(const W16TileArgs& a, bool nv, bool swiglu, bool out_bf16, int bm, int64_t units,
                              hipStream_t stream) {
   if (bm == 256) {
-    if (swiglu) launch_shape<256, 256, 8, true, false>(a, nv, out_bf16, units, stream);
-    else launch_shape<256, 256, 8, false, false>(a, nv, out_bf16, units, stream);
+    if (swiglu) launch_shape<256, 256, 8, 3, true, false>(a, nv, out_bf16, units, stream);
+    else launch_shape<256, 256, 8, 3, false, false>(a, nv, out_bf16, units, stream);
+  } else if (bm == 128) {
+    if (swiglu) launch_shape<128, 256, 4, 2, true, false>(a, nv, out_bf16, units, stream);
+    else launch_shape<128, 256, 4, 2, false, false>(a, nv, out_bf16, units, stream);
   } else {
-    if (swiglu) launch_shape<64, 256, 4, true, false>(a, nv, out_bf16, units, stream);
-    else launch_shape<64, 256, 4, false, false>(a, nv, out_bf16, units, stream);
+    if (swiglu) launch_shape<64, 256, 4, 3, true, false>(a, nv, out_bf16, units, stream);
+    else launch_shape<64, 256, 4, 3, false, false>(a, nv, out_bf16, units, stream);
   }
 }
 
@@ -344,8 +375,8 @@ void launch_w16_tile_lora(const W16TileArgs& a, bool nv, bool out_bf16, hipStrea
   // 256 x 256 tiles once they fill the chip's 256 compute units; below that the small
   // tile's four times as many workgroups finish sooner
   if (cdiv(a.R, 256) * cdiv(a.N, 256) >= 256)
-    launch_shape<256, 256, 8, false, true>(a, nv, out_bf16, cdiv(a.R, 256), stream);
-  else launch_shape<64, 128, 4, false, true>(a, nv, out_bf16, cdiv(a.R, 64), stream);
+    launch_shape<256, 256, 8, 3, false, true>(a, nv, out_bf16, cdiv(a.R, 256), stream);
+  else launch_shape<64, 128, 4, 3, false, true>(a, nv, out_bf16, cdiv(a.R, 64), stream);
 }
 
 }  // namespace mxf

@@ -20,8 +20,8 @@ struct W16TileArgs {
   void* out;               // [R][N] or, with SwiGLU, [R][N/2]
   int ntiles;
   // adapters (w4a16_lora.hip)
-  const float* low;        // [nslice][R][rank] fp32, the slices' sum is scaling * a . lora_a^T
-  int nslice, rank, L, S;
+  const uint16_t *low_hi, *low_lo;  // [R][rank] bf16 each: scaling * a . lora_a^T as the sum of two terms
+  int rank, L, S;
   const int32_t* seg_off;      // [S+1]
   const int32_t* seg_adapter;  // [S]
   const uint16_t* lora_b;      // [L][N][rank] bf16
@@ -35,27 +35,45 @@ __device__ __forceinline__ int w16_rows(const int32_t* __restrict__ off, int64_t
   return (int)(hi - lo);
 }
 
-// Units of an expert of c rows in a launch for experts of lo_rows < c <= hi_rows:
-// ceil(c / BM), or one when BM == 0.
+// Units of an expert of c rows in a launch for experts of lo_rows < c <= hi_rows
 template <int BM>
 __device__ __forceinline__ int w16_units(int c, int lo_rows, int hi_rows) {
-  if (c <= lo_rows || c > hi_rows) return 0;
-  if constexpr (BM == 0) return 1;
-  else return (c + BM - 1) / BM;
+  return c <= lo_rows || c > hi_rows ? 0 : (c + BM - 1) / BM;
+}
+
+// x n / 8 without leaving 32 bits
+__device__ __forceinline__ uint32_t w16_eighths(uint32_t n, int x) {
+  return (n >> 3) * (uint32_t)x + (((n & 7u) * (uint32_t)x) >> 3);
 }
 
 // Item j of XCD x: the units' items (n-tile by n-tile inside an expert, unit by unit inside
 // an n-tile) are split into 8 contiguous ranges, one per XCD, so that the workgroups of an
 // XCD share activation rows and weight tiles in its L2. Called by whole waves; false: none.
-template <int BM>
-__device__ __forceinline__ bool w16_item(const int32_t* __restrict__ off, int E, int64_t R, int lo_rows, int hi_rows,
-                                         int ntiles, int x, int j, int& e_out, int& n_out, int64_t& row0, int& m) {
+// Every workgroup starts with this, so its latency counts: with CE > 0 (E <= 64 CE) each
+// lane takes its experts' offsets in one batch of loads and keeps them.
+template <int BM, int CE>
+__device__ __forceinline__ bool w16_item_of(const int32_t* __restrict__ off, int E, int64_t R, int lo_rows, int hi_rows,
+                                            int ntiles, int x, int j, int& e_out, int& n_out, int64_t& row0, int& m) {
   const int lane = threadIdx.x & 63;
-  const int C = (E + 63) >> 6, first = lane * C;
+  const int C = CE > 0 ? CE : (E + 63) >> 6, first = lane * C;
+  int64_t r0 = 0;
   int units = 0;
-  int64_t r0;
-  for (int i = 0; i < C; ++i)
-    if (first + i < E) units += w16_units<BM>(w16_rows(off, R, first + i, r0), lo_rows, hi_rows);
+  int o[CE + 1];  // CE > 0: the lane's row bounds (experts past E are empty)
+  if constexpr (CE > 0) {
+#pragma unroll
+    for (int i = 0; i <= CE; ++i) o[i] = off[min(first + i, E)];
+#pragma unroll
+    for (int i = 0; i <= CE; ++i) {
+      o[i] = min(max(o[i], 0), (int)R);
+      if (i > 0) {
+        o[i] = max(o[i], o[i - 1]);
+        units += w16_units<BM>(o[i] - o[i - 1], lo_rows, hi_rows);
+      }
+    }
+  } else {
+    for (int i = 0; i < C; ++i)
+      if (first + i < E) units += w16_units<BM>(w16_rows(off, R, first + i, r0), lo_rows, hi_rows);
+  }
   int incl = units;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
@@ -63,40 +81,78 @@ __device__ __forceinline__ bool w16_item(const int32_t* __restrict__ off, int E,
     if (lane >= d) incl += y;
   }
   const int excl = incl - units;
-  const int64_t total = (int64_t)__shfl(incl, 63) * ntiles;
-  const int64_t w = x * total / 8 + j;
-  if (w >= (x + 1) * total / 8) return false;
-  const int p = (int)(w / ntiles);
+  // the host keeps units x ntiles below 2^31; x total / 8 in 32 bits
+  const uint32_t total = (uint32_t)__builtin_amdgcn_readlane(incl, 63) * (uint32_t)ntiles;
+  const uint32_t w = w16_eighths(total, x) + (uint32_t)j;
+  if (w >= w16_eighths(total, x + 1)) return false;
+  const int p = (int)(w / (uint32_t)ntiles);
   const bool mine = p >= excl && p < incl;
   const unsigned long long msk = __ballot(mine);
   if (msk == 0) return false;
   const int src = __ffsll((long long)msk) - 1;
-  int ee = 0, ue = 0, ke = 1;
+  int ee = 0, ue = 0, ke = 1, c = 0, lo = 0;
   if (mine) {
     int acc = excl;
-    for (int i = 0; i < C && first + i < E; ++i) {
-      const int n = w16_units<BM>(w16_rows(off, R, first + i, r0), lo_rows, hi_rows);
-      if (p < acc + n) {
+#pragma unroll
+    for (int i = 0; i < (CE > 0 ? CE : 1024); ++i) {
+      if (CE == 0 && (i >= C || first + i >= E)) break;
+      int ci;
+      if constexpr (CE > 0) {
+        r0 = o[i];
+        ci = o[i + 1] - o[i];
+      } else {
+        ci = w16_rows(off, R, first + i, r0);
+      }
+      const int n = w16_units<BM>(ci, lo_rows, hi_rows);
+      if (p >= acc && p < acc + n) {
         ee = first + i;
         ue = acc;
         ke = n;
-        break;
+        c = ci;
+        lo = (int)r0;
       }
       acc += n;
     }
   }
-  ee = __builtin_amdgcn_readfirstlane(__shfl(ee, src));
-  ue = __shfl(ue, src);
-  ke = __shfl(ke, src);
-  const int64_t local = w - (int64_t)ue * ntiles;
-  n_out = __builtin_amdgcn_readfirstlane((int)(local / ke));
-  const int loc = __builtin_amdgcn_readfirstlane((int)(local % ke));
+  e_out = __builtin_amdgcn_readlane(ee, src);
+  ue = __builtin_amdgcn_readlane(ue, src);
+  ke = __builtin_amdgcn_readlane(ke, src);
+  c = __builtin_amdgcn_readlane(c, src);
+  lo = __builtin_amdgcn_readlane(lo, src);
+  const uint32_t local = w - (uint32_t)ue * (uint32_t)ntiles;
+  n_out = (int)(local / (uint32_t)ke);
+  const int loc = (int)(local - (uint32_t)n_out * (uint32_t)ke);
   if (n_out < 0 || n_out >= ntiles || loc < 0) return false;
-  e_out = ee;
-  const int c = w16_rows(off, R, ee, r0);
-  row0 = r0 + (int64_t)loc * BM;
-  m = BM == 0 ? c : min(BM, c - loc * BM);
+  row0 = lo + (int64_t)loc * BM;
+  m = min(BM, c - loc * BM);
   return m > 0;
+}
+
+template <int BM>
+__device__ __forceinline__ bool w16_item(const int32_t* __restrict__ off, int E, int64_t R, int lo_rows, int hi_rows,
+                                         int ntiles, int x, int j, int& e_out, int& n_out, int64_t& row0, int& m) {
+  if (E <= 64) return w16_item_of<BM, 1>(off, E, R, lo_rows, hi_rows, ntiles, x, j, e_out, n_out, row0, m);
+  if (E <= 256) return w16_item_of<BM, 4>(off, E, R, lo_rows, hi_rows, ntiles, x, j, e_out, n_out, row0, m);
+  return w16_item_of<BM, 0>(off, E, R, lo_rows, hi_rows, ntiles, x, j, e_out, n_out, row0, m);
+}
+
+// first segment s whose end seg_off[s + 1] lies past row t (S if none): 64 probes a step
+__device__ __forceinline__ int first_segment(const int32_t* __restrict__ seg_off, int S, int64_t t) {
+  const int lane = threadIdx.x & 63;
+  int lo = 0, hi = S;
+  while (lo < hi) {
+    const int step = (hi - lo + 63) / 64;
+    const int64_t idx = lo + (int64_t)lane * step;
+    const bool p = idx < hi && (int64_t)seg_off[idx < hi ? idx + 1 : 0] > t;
+    const unsigned long long m = __ballot(p);
+    const int probes = (hi - lo + step - 1) / step;
+    const int f = m ? __ffsll((long long)m) - 1 : probes;  // the first probe past t
+    const int nlo = f == 0 ? lo : lo + (f - 1) * step + 1;
+    hi = f == probes ? hi : lo + f * step;
+    lo = nlo;
+    if (step == 1) break;
+  }
+  return __builtin_amdgcn_readfirstlane(lo);
 }
 
 void launch_w16_tile_grouped(const W16TileArgs& a, bool nv, bool swiglu, bool out_bf16, int bm, int64_t units,

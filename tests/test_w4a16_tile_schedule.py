@@ -5,7 +5,8 @@ hand-over of the three slots."""
 
 import pytest
 
-SHAPES = [(256, 256, 8, False), (256, 256, 8, True), (64, 256, 4, False), (64, 256, 4, True), (64, 128, 4, False)]
+SHAPES = [(256, 256, 8, False), (128, 256, 4, False), (128, 256, 4, True), (64, 256, 4, False), (64, 256, 4, True),
+          (64, 128, 4, False)]
 
 
 def swz_a(r):
@@ -13,18 +14,18 @@ def swz_a(r):
 
 
 def swz_b(r):
-    return (r >> 3) & 1
+    return (r >> 2) & 3
 
 
 def copies(BM, BN, NW):
     """(operand, wave, lane) -> LDS byte offset and (row, 16-byte chunk of the row's stage bytes)."""
-    IA, IB = BM * 8 // 64 // NW, BN * 2 // 64 // NW
+    IA, IB = BM * 8 // 64 // NW, BN * 4 // 64 // NW
     for wave in range(NW):
         for q in range(IB):
             for lane in range(64):
                 chunk = (wave * IB + q) * 64 + lane
-                r = chunk >> 1
-                yield "B", (wave * IB + q) * 1024 + 16 * lane, (r, (chunk & 1) ^ swz_b(r))
+                r = chunk >> 2
+                yield "B", (wave * IB + q) * 1024 + 16 * lane, (r, (chunk & 3) ^ swz_b(r))
         for q in range(IA):
             for lane in range(64):
                 chunk = (wave * IA + q) * 64 + lane
@@ -32,7 +33,7 @@ def copies(BM, BN, NW):
                 yield "A", (wave * IA + q) * 1024 + 16 * lane, (r, (chunk & 7) ^ swz_a(r))
         if wave < BN // 64:
             for lane in range(64):
-                yield "S", wave * 256 + 4 * lane, (64 * wave + lane, 0)
+                yield "S", wave * 1024 + 16 * lane, (64 * wave + lane, 0)
 
 
 @pytest.mark.parametrize("BM,BN,NW,swiglu", SHAPES)
@@ -45,9 +46,9 @@ def test_slot_is_filled_and_read_in_one_layout(BM, BN, NW, swiglu):
         assert at not in slot[op]
         slot[op][at] = what
     assert sorted(slot["A"]) == list(range(0, BM * 128, 16))
-    assert sorted(slot["B"]) == list(range(0, BN * 32, 16))
-    assert sorted(slot["S"]) == list(range(0, BN * 4, 4))
-    for name, per in (("A", 8), ("B", 2)):
+    assert sorted(slot["B"]) == list(range(0, BN * 64, 16))
+    assert sorted(slot["S"]) == list(range(0, BN * 16, 16))
+    for name, per in (("A", 8), ("B", 4)):
         assert sorted(slot[name].values()) == [(r, c) for r in range(len(slot[name]) // per) for c in range(per)]
     rows_seen, cols_seen = [], []
     for wave in range(NW):
@@ -58,9 +59,11 @@ def test_slot_is_filled_and_read_in_one_layout(BM, BN, NW, swiglu):
                     row = (0 if f < FN // 2 else BN // 2) + FN * 16 * wn + 32 * (f % (FN // 2)) + r32
                 else:
                     row = 32 * (FN * wn + f) + r32
-                assert slot["S"][4 * row] == (row, 0)
+                assert slot["S"][16 * row] == (row, 0)
                 for g in range(2):
-                    assert slot["B"][row * 32 + 16 * (g ^ swz_b(row))] == (row, g)  # the 32 codes k = 32 g + ...
+                    for odd in range(2):  # the 32 codes k = 32 (2 odd + g) + ... of the 128-k slot
+                        at = (row * 64 + 16 * (g ^ swz_b(row))) ^ (32 * odd)
+                        assert slot["B"][at] == (row, 2 * odd + g)
                 if wm == 0:
                     cols_seen.append(row)
         for f in range(2):
@@ -130,45 +133,71 @@ def test_epilogue_staging_round_trip(OF, es):
     assert 64 * (NCH // 2) == 32 * NCH
 
 
-@pytest.mark.parametrize("nst", [2, 4, 6, 32, 112])
-@pytest.mark.parametrize("per", [6, 7, 9])  # copies of a wave per stage
-def test_slots_are_handed_over(nst, per):
-    """A slot is computed only after its stage's copies landed and refilled only after every wave is done with it."""
-    issued, holds = 0, {}
-    outstanding = []  # stages in issue order, `per` copies each
+@pytest.mark.parametrize("nst", [2, 4, 6, 8, 10, 32, 112])
+@pytest.mark.parametrize("NA", [2, 3])
+@pytest.mark.parametrize("P", [4, 8])
+@pytest.mark.parametrize("IA,IB,has_sc", [(4, 2, True), (4, 2, False), (4, 4, True), (2, 4, True), (2, 2, False)])
+def test_slots_are_handed_over(nst, NA, P, IA, IB, has_sc):
+    """A stage is computed only after its copies landed, and a slot refilled only after every wave is done with it."""
+    outstanding, A, B, S = [], {}, {}, {}
 
-    def issue(st):
-        nonlocal issued
-        assert st == issued
-        issued += 1
-        holds[st % 3] = st
-        outstanding.extend([st] * per)
+    def issue_a(slot, st):
+        A[slot] = st
+        outstanding.extend([("A", st)] * IA)
 
-    issue(0)
-    if nst > 1:
-        issue(1)
+    def issue_b(slot, h):
+        B[slot] = h
+        outstanding.extend([("B", h)] * IB)
+
+    def issue_s(grp):
+        S[grp & 1] = grp
+        if has_sc:
+            outstanding.append(("S", grp))
+
+    issue_s(0)
+    issue_b(0, 0)
+    for st in range(min(NA - 1, nst)):
+        issue_a(st, st)
+    U = 12 if NA == 3 else 4
     for st in range(nst):
-        allowed = per if st + 1 < nst else 0
+        i = st % U
+        if NA == 2 or st + 1 >= nst:
+            allowed = 0
+        elif i % 2 == 0:
+            allowed = IA
+        elif has_sc and (st - 1) % P == 0 and st - 1 + P < nst:
+            allowed = IA + IB + 1
+        else:
+            allowed = IA + IB
         del outstanding[:max(0, len(outstanding) - allowed)]
-        assert st not in outstanding  # this wave's copies of the stage have landed before the barrier
-        # after the barrier every wave is past stage st - 1: its slot may be refilled
-        if st + 2 < nst:
-            assert (st + 2) % 3 == (st - 1) % 3
-            issue(st + 2)
-        assert holds[st % 3] == st
-    assert issued == nst and not outstanding
+        needed = {("A", st), ("B", st // 2), ("S", st // P)}
+        assert not needed & set(outstanding)
+        # after the barrier every wave is done with stage st - 1: what it and older stages read may be refilled
+        if i % 2 == 0 and st + 2 < nst:
+            slot = (i // 2 + 1) % 2
+            assert B.get(slot, -1) < (st // 2)
+            issue_b(slot, st // 2 + 1)
+        if i % 2 == 0 and st % P == 0 and st + P < nst:
+            assert S.get((st // P + 1) & 1, -1) < st // P
+            issue_s(st // P + 1)
+        if st + NA - 1 < nst:
+            slot = (i + NA - 1) % NA
+            assert A.get(slot, -1) < st
+            issue_a(slot, st + NA - 1)
+        assert A[i % NA] == st and B[(i // 2) % 2] == st // 2 and S[(st // P) & 1] == st // P
+    assert not outstanding
 
 
 @pytest.mark.parametrize("nv", [False, True])
 def test_scale_bytes(nv):
-    """Stage st of 64 k copies the row's scale dword that holds the scales of its two 32-k groups."""
-    for st in range(8):
-        dword = st if nv else st >> 1
+    """A scale group is 16 bytes of a row: stage st finds the scales of its two 32-k groups in one dword of it."""
+    P, per = (4, 16) if nv else (8, 32)
+    for st in range(40):
+        dword = st & 3 if nv else (st & 7) >> 1
         for g in range(2):
             for k in range(0, 32, 8):
-                byte = 16 * g // 8 + (k // 16) if nv else 2 * (st & 1) + g
-                per = 16 if nv else 32
-                assert 4 * dword + byte == (64 * st + 32 * g + k) // per
+                byte = 2 * g + k // 16 if nv else 2 * (st & 1) + g
+                assert 16 * (st // P) + 4 * dword + byte == (64 * st + 32 * g + k) // per
 
 
 def first_segment(ends, S, t):
