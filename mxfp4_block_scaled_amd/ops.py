@@ -120,29 +120,28 @@ def _need(t, name, dtypes, shape):
             raise RuntimeError(f"{name}: shape {tuple(t.shape)}, expected {shape} (dimension {i})")
 
 
-def _dev_all(*tensors):
-    """The one GPU that all the given tensors (None skipped) are on; they must be contiguous."""
-    dev = None
-    for t in tensors:
-        if t is None:
-            continue
-        if not t.is_cuda or not t.is_contiguous():
-            _dev(t)
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise RuntimeError(f"tensors are on {dev} and {t.device}, expected one GPU")
-    return dev
+# The current stream's handle without the Stream object around it (2 us of a 10 us call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda i: torch.cuda.current_stream(i).cuda_stream)
+
+
+def _is(t, name, dtype, shape, dev):
+    """_dev and _need in one: t is on `dev`, contiguous, of `dtype` (or one of a tuple) and `shape`."""
+    if t.dtype != dtype or t.shape != shape or t.device != dev or not t.is_contiguous():
+        _dev(t)
+        _need(t, name, dtype, shape)
+        if t.device != dev:
+            raise RuntimeError(f"{name} is on {t.device}, expected {dev}")
 
 
 def _call(name, dev, *args):
     """The C function `name` with the tensors' GPU current and its current stream as the last argument."""
-    fn = getattr(load(), name)
-    if torch.cuda.current_device() == dev.index:
-        rc = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    fn = getattr(_lib or load(), name)
+    i = dev.index
+    if torch.cuda.current_device() == i:
+        rc = fn(*args, _raw_stream(i))
     else:
         with torch.cuda.device(dev):
-            rc = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+            rc = fn(*args, _raw_stream(i))
     if rc:
         _check(rc, name)
 
@@ -442,25 +441,25 @@ def moe_grouped_gemm_w4a16(a, expert_offsets, w, w_scale, fmt="mxfp4", sorted_pa
     moe_route_permute) a [R/topk][K] and row r reads a[sorted_pair[r] // topk]. swiglu: the first N/2 weight rows
     are gate rows and the result is silu(gate) * up. Returns y [R][N] or [R][N/2]; with `out` given, rows outside
     every expert keep what it holds (in a new tensor they are uninitialised)."""
-    dev = _dev_all(a, expert_offsets, w, w_scale, sorted_pair, out)
+    dev = _dev(a)
     if a.dim() != 2 or w.dim() != 3:
         raise RuntimeError("a must be [rows][K] and w [E][N][K/2]")
     rows, K = a.shape
     E, N, _ = w.shape
     f = _one_of(fmt, WEIGHT_FMTS, "fmt")
     R = rows * topk if sorted_pair is not None else rows
-    _need(a, "a", torch.bfloat16, (rows, K))
-    _need(expert_offsets, "expert_offsets", torch.int32, (E + 1,))
-    _need(w, "w", torch.uint8, (E, N, K // 2))
-    _need(w_scale, "w_scale", torch.uint8, (E, N, K // (16 if f else 32)))
+    _is(a, "a", torch.bfloat16, (rows, K), dev)
+    _is(expert_offsets, "expert_offsets", torch.int32, (E + 1,), dev)
+    _is(w, "w", torch.uint8, (E, N, K // 2), dev)
+    _is(w_scale, "w_scale", torch.uint8, (E, N, K // (16 if f else 32)), dev)
     if sorted_pair is not None:
-        _need(sorted_pair, "sorted_pair", torch.int32, (R,))
+        _is(sorted_pair, "sorted_pair", torch.int32, (R,), dev)
     shape = (R, N // 2 if swiglu else N)
     if out is None:
         _one_of(out_dtype, DTYPES, "out_dtype")
         out = torch.empty(shape, dtype=out_dtype, device=dev)
     else:
-        _need(out, "out", (torch.float32, torch.bfloat16), shape)
+        _is(out, "out", (torch.float32, torch.bfloat16), shape, dev)
     _call("moe_grouped_gemm_w4a16", dev, a.data_ptr(), rows, R, _at(sorted_pair), topk, expert_offsets.data_ptr(), E, N,
           K, f, w.data_ptr(), w_scale.data_ptr(), int(swiglu), out.data_ptr(), DTYPES[out.dtype])
     return out
@@ -473,7 +472,7 @@ def fp4_gemm_w4a16_lora(a, w, w_scale, seg_offsets, seg_adapter, lora_a, lora_b,
     scaling[l] * (a lora_a[l]^T) lora_b[l]^T of its adapter l = seg_adapter[s]; a negative l, and rows in no
     segment, get the projection alone. seg_offsets [S+1], seg_adapter [S] int32; lora_a [L][rank][K], lora_b
     [L][N][rank] bf16; scaling [L] fp32. Returns c [M][N] in out_dtype (fp32 or bf16)."""
-    dev = _dev_all(a, w, w_scale, seg_offsets, seg_adapter, lora_a, lora_b, scaling, out, workspace)
+    dev = _dev(a)
     if a.dim() != 2 or w.dim() != 2 or lora_a.dim() != 3 or seg_adapter.dim() != 1:
         raise RuntimeError("a must be [M][K], w [N][K/2], lora_a [L][rank][K] and seg_adapter [S]")
     M, K = a.shape
@@ -481,22 +480,24 @@ def fp4_gemm_w4a16_lora(a, w, w_scale, seg_offsets, seg_adapter, lora_a, lora_b,
     L, rank, _ = lora_a.shape
     S = seg_adapter.shape[0]
     f = _one_of(fmt, WEIGHT_FMTS, "fmt")
-    _need(a, "a", torch.bfloat16, (M, K))
-    _need(w, "w", torch.uint8, (N, K // 2))
-    _need(w_scale, "w_scale", torch.uint8, (N, K // (16 if f else 32)))
-    _need(seg_offsets, "seg_offsets", torch.int32, (S + 1,))
-    _need(seg_adapter, "seg_adapter", torch.int32, (S,))
-    _need(lora_a, "lora_a", torch.bfloat16, (L, rank, K))
-    _need(lora_b, "lora_b", torch.bfloat16, (L, N, rank))
-    _need(scaling, "scaling", torch.float32, (L,))
+    _is(a, "a", torch.bfloat16, (M, K), dev)
+    _is(w, "w", torch.uint8, (N, K // 2), dev)
+    _is(w_scale, "w_scale", torch.uint8, (N, K // (16 if f else 32)), dev)
+    _is(seg_offsets, "seg_offsets", torch.int32, (S + 1,), dev)
+    _is(seg_adapter, "seg_adapter", torch.int32, (S,), dev)
+    _is(lora_a, "lora_a", torch.bfloat16, (L, rank, K), dev)
+    _is(lora_b, "lora_b", torch.bfloat16, (L, N, rank), dev)
+    _is(scaling, "scaling", torch.float32, (L,), dev)
     if out is None:
         _one_of(out_dtype, DTYPES, "out_dtype")
         out = torch.empty((M, N), dtype=out_dtype, device=dev)
     else:
-        _need(out, "out", (torch.float32, torch.bfloat16), (M, N))
+        _is(out, "out", (torch.float32, torch.bfloat16), (M, N), dev)
     need = load().fp4_w4a16_lora_workspace_bytes(M, N, K, rank)
     if workspace is None:
         workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+    elif _dev(workspace) != dev:
+        raise RuntimeError(f"workspace is on {workspace.device}, expected {dev}")
     else:
         _need(workspace, "workspace", torch.uint8, ((">=", need),))
     _call("fp4_gemm_w4a16_lora", dev, a.data_ptr(), M, N, K, f, w.data_ptr(), w_scale.data_ptr(), _at(seg_offsets),
@@ -516,12 +517,11 @@ def moe_block_norm(y, x=None, post_weight=None, gate=None, residual_scale=1.0, p
     act_fmt "e4m3" / "e2m1" also quantises n (from fp32) as mxfp4_quantize_act. `r` may be given as the output
     (x itself: updated in place). Returns a dict of r (x's dtype, without x r_dtype or y's), n (n_dtype), q and
     q_scale; what is not wanted is None."""
-    dev = _dev_all(y, x, post_weight, gate, pre_weight, expert_gates, pair_row, r)
+    dev = _dev(y)
     if y.dim() != 2:
         raise RuntimeError("y must be 2-d [rows][H]")
-    floats = (torch.bfloat16, torch.float32)
     y_rows, H = y.shape
-    _need(y, "y", floats, (y_rows, H))
+    _one_of(y.dtype, DTYPES, "y")
     topk = 0
     T = y_rows
     if (expert_gates is None) != (pair_row is None):
@@ -530,34 +530,31 @@ def moe_block_norm(y, x=None, post_weight=None, gate=None, residual_scale=1.0, p
         if expert_gates.dim() != 2 or expert_gates.shape[1] < 1:
             raise RuntimeError("expert_gates must be [T][topk]")
         T, topk = expert_gates.shape
-        _need(expert_gates, "expert_gates", torch.float32, (T, topk))
-        _need(pair_row, "pair_row", torch.int32, (T * topk,))
+        _is(expert_gates, "expert_gates", torch.float32, (T, topk), dev)
+        _is(pair_row, "pair_row", torch.int32, (T * topk,), dev)
     if x is not None:
-        _need(x, "x", floats, (T, H))
         r_dtype = x.dtype
+        _is(x, "x", r_dtype, (T, H), dev)
     elif r_dtype is None:
         r_dtype = y.dtype if r is None else r.dtype
-    x_dtype = _one_of(r_dtype, DTYPES, "r_dtype")
+    x_dtype = _one_of(r_dtype, DTYPES, "the residual's dtype")
     w_dtype = torch.float32
     for name, t in (("post_weight", post_weight), ("pre_weight", pre_weight)):
         if t is not None:
-            _need(t, name, floats, (H,))
             w_dtype = t.dtype
+            _one_of(w_dtype, DTYPES, name)
+            _is(t, name, w_dtype, (H,), dev)
     if post_weight is not None and post_weight.dtype != w_dtype:
         raise RuntimeError(f"post_weight is {post_weight.dtype} and pre_weight {w_dtype}, expected one dtype")
     mode, g_dtype = 0, torch.float32
     if gate is not None:
         g_dtype = gate.dtype
-        if gate.dim() == 1:
-            mode = 1
-        elif gate.dim() == 2 and gate.shape[1] == 1 and H != 1:
-            mode = 2
-        else:
-            mode = 3
-        _need(gate, "gate", floats, {1: (H,), 2: (T, 1), 3: (T, H)}[mode])
+        mode = 1 if gate.dim() == 1 else 2 if gate.dim() == 2 and gate.shape[1] == 1 else 3
+        _one_of(g_dtype, DTYPES, "gate")
+        _is(gate, "gate", g_dtype, {1: (H,), 2: (T, 1), 3: (T, H)}[mode], dev)
     fmt = None if act_fmt is None else _one_of(act_fmt, FMTS, "act_fmt")
     if r is not None:
-        _need(r, "r", r_dtype, (T, H))
+        _is(r, "r", r_dtype, (T, H), dev)
     elif want_r:
         r = torch.empty((T, H), dtype=r_dtype, device=dev)
     n_code = _one_of(n_dtype, DTYPES, "n_dtype")
