@@ -311,6 +311,7 @@ int fp4_gemm_w4a16_lora(const uint16_t* a, int64_t M, int64_t N, int64_t K, int 
   if (S < 0 || L < 0 || rank < 8 || rank > 128 || rank % 8 != 0) return MXF_ERR_SHAPE;
   if (K >= (int64_t(1) << 22) || N > kMaxRows || (N + 257) * (K / 2) >= kMaxOffset) return MXF_ERR_UNSUPPORTED;
   if (mxf::cdiv(M, 64) * mxf::cdiv(N, 128) > kMaxRows - 8) return MXF_ERR_UNSUPPORTED;
+  if ((N + 256) * rank * 2 >= kMaxOffset) return MXF_ERR_UNSUPPORTED;  // an adapter's second factor
   if (M == 0) return MXF_OK;
   if (!a || !w || !w_scale || !c) return MXF_ERR_NULL;
   if (S > 0 && (!seg_offsets || !seg_adapter)) return MXF_ERR_NULL;

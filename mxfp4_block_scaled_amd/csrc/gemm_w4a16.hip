@@ -203,13 +203,4 @@ int launch_w4a16_gemm(bool nvfp4, const uint16_t* a, int64_t M, int64_t N, int64
   return hipGetLastError() == hipSuccess ? 0 : -1;
 }
 
-void launch_w4a16_slices(bool nvfp4, const uint16_t* a, int64_t M, int64_t N, int64_t K, const uint8_t* w,
-                         const uint8_t* ws, float* partials, hipStream_t stream) {
-  const int S = w4a16_ksplit(M, N, K);
-  W16Args args{a, w, ws, partials, M, N, K, S > 1 ? 4 : (int)(K / 512)};
-  const dim3 grid((unsigned)cdiv(N, 64), (unsigned)S);
-  if (nvfp4) launch_w4a16_mt<1>(args, (int)cdiv(M, 16), grid, stream);
-  else launch_w4a16_mt<0>(args, (int)cdiv(M, 16), grid, stream);
-}
-
 }  // namespace mxf

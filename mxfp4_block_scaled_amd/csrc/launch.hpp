@@ -54,10 +54,6 @@ int w4a16_ksplit(int64_t M, int64_t N, int64_t K);
 int launch_w4a16_gemm(bool nvfp4, const uint16_t* a, int64_t M, int64_t N, int64_t K, const uint8_t* w,
                       const uint8_t* ws, float* c, float* partials, hipStream_t stream);
 
-// the same for at most 64 rows, leaving its w4a16_ksplit K slices [S][M][N] in partials
-void launch_w4a16_slices(bool nvfp4, const uint16_t* a, int64_t M, int64_t N, int64_t K, const uint8_t* w,
-                         const uint8_t* ws, float* partials, hipStream_t stream);
-
 // ragged grouped products of bf16 activations and FP4 expert weights (w4a16_grouped.hip)
 struct W16TileArgs;
 int launch_w16_grouped(W16TileArgs a, bool nvfp4, bool swiglu, bool out_bf16, hipStream_t stream);

@@ -1,5 +1,5 @@
 // FP4 weights as bf16 matrix operands: the register decoders shared by the kernels that
-// multiply FP4 weights with bf16 activations (gemm_w4a16.hip, w4a16_tile.hip,
+// multiply FP4 weights with bf16 activations (gemm_w4a16.hip, w4a16_tile_body.hpp,
 // w4a16_grouped.hip).
 #pragma once
 

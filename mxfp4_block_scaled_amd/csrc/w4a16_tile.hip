@@ -1,345 +1,15 @@
-// Tiled products of bf16 activations with FP4 weights: y = A . W_hat^T for many rows per
-// weight matrix, either grouped by expert with ragged row ranges (moe_grouped_gemm_w4a16)
-// or over one matrix with low-rank adapters beside it (fp4_gemm_w4a16_lora).
-//
-// A workgroup computes BM rows x BN weight rows with waves of 64 rows x 32 FN weight rows
-// on the 32x32x16 bf16 MFMA (weights as the first operand, so a lane ends up with runs of
-// 4 consecutive columns of one row). A stage is 64 k: BM x 128 bytes of activations,
-// BN x 32 bytes of codes and one scale dword per weight row, all copied HBM -> LDS
-// directly; three slots, the copies of stage st + 2 go out while st is computed. The
-// weights stay 4 bits wide up to the registers: a lane reads the 16 bytes that hold 32
-// codes of its weight row and converts 8 of them (exactly: a code times its scale has at
-// most 5 significant bits) in front of each MFMA.
-//
-// K order: inside a stage MFMA j takes, in lane group g (lane / 32), k = 32 g + 8 j +
-// [0, 8), for both operands: a weight lane's 16 bytes are 16-byte chunk g of its 32-byte
-// stage row, one 32-element block, and an activation lane reads chunk 4 g + j of its
-// 128-byte stage row. Chunks are XOR-swizzled per row so that the 16 lanes of an LDS
-// cycle hit different banks.
-//
-// Rows past a unit's end and weight rows past N read as zero through the range-checked
-// buffer resources and are not stored.
-#include "w4a16_tile.hpp"
+// Launches of the tiled FP4-weight x bf16-activation product (w4a16_tile_body.hpp).
+#include "w4a16_tile_body.hpp"
 
 namespace mxf {
 
 namespace {
 
-// LDS: NA slots of one 64-k stage of activations, two of 128 k of weight codes, two of a
-// scale group (16 scale bytes per weight row: 512 k of UE8M0 or 256 k of UE4M3)
-template <int BM, int BN, int NA>
-struct alignas(16) W16Ring {
-  uint8_t A[NA][BM * 128];
-  uint8_t B[2][BN * 64];
-  uint8_t S[2][BN * 16];
-};
-
-__device__ __forceinline__ int swz_a16(int r) { return (r & 7) ^ ((r >> 3) & 1); }  // 8 chunks per row
-__device__ __forceinline__ int swz_b16(int r) { return (r >> 2) & 3; }              // 4 chunks per row
-
-__device__ __forceinline__ v16f mfma32x32x16(v8bf a, v8bf b, v16f c) {
-#if defined(__HIP_DEVICE_COMPILE__)
-  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
-#else
-  (void)a;
-  (void)b;
-  return c;
-#endif
-}
-
-// BM x BN per workgroup of NW waves: BM / 64 waves over rows, the others over columns
 template <int BM, int BN, int NW, int NA, bool kNV, bool kSwiglu, bool kOutBF16, bool kLora>
 __global__ void __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(2))) w16_tile_kernel(W16TileArgs a) {
-  constexpr int WMN = BM / 64, WNN = NW / WMN, FN = BN / WNN / 32;
-  constexpr int IA = BM * 8 / 64 / NW, IB = BN * 4 / 64 / NW;  // 16-byte copies per lane per 64 / 128 k
-  constexpr int P = kNV ? 4 : 8;  // stages per scale group
-  static_assert(IA >= 1 && IB >= 1 && BN / 64 <= NW && (!kSwiglu || FN % 2 == 0), "tile shape");
   __shared__ W16Ring<BM, BN, NA> ring;
-  static_assert(sizeof(ring) <= 160 * 1024 && sizeof(ring) >= NW * 8192, "the epilogue stages through the ring");
-
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, g = lane >> 5,
-            r32 = lane & 31;
-  const int wm = wave / WNN, wn = wave % WNN;
-  const int64_t K = a.K, N = a.N;
-
-  int e = 0, n_tile, m;
-  int64_t row0;
-  {
-    const int x = (int)(blockIdx.x & 7u), j = (int)(blockIdx.x >> 3);
-    if (a.offsets) {
-      if (!w16_item<BM>(a.offsets, a.E, a.R, a.min_rows, a.max_rows, a.ntiles, x, j, e, n_tile, row0, m)) return;
-    } else {  // the items of an n-tile are its units; 8 contiguous ranges of items, one per XCD
-      const uint32_t units = (uint32_t)((a.R + BM - 1) / BM), total = units * (uint32_t)a.ntiles;
-      const uint32_t w = w16_eighths(total, x) + (uint32_t)j;
-      if (w >= w16_eighths(total, x + 1)) return;
-      n_tile = (int)(w / units);
-      row0 = (int64_t)(w - (uint32_t)n_tile * units) * BM;
-      m = (int)min((int64_t)BM, a.R - row0);
-    }
-  }
-  const int64_t wrow = K / 2, srow = kNV ? K / 16 : K / 32, half = N / 2;
-  const int nst = (int)(K / 64);
-
-  const buf_rsrc ra = a.pair ? make_rsrc(a.a, (uint32_t)(a.a_rows * K * 2))
-                             : make_rsrc(a.a + row0 * K, (uint32_t)((int64_t)m * K * 2));
-  const buf_rsrc rb = make_rsrc(a.w + (int64_t)e * N * wrow, (uint32_t)(N * wrow));
-  const buf_rsrc rbs = make_rsrc(a.ws + (int64_t)e * N * srow, (uint32_t)(N * srow));
-
-  // the weight row that tile row r holds (N and beyond: reads as zero)
-  auto b_row = [&](int r) -> int64_t {
-    if (kSwiglu) return (r < BN / 2 ? 0 : half - BN / 2) + (int64_t)n_tile * (BN / 2) + r;
-    return (int64_t)n_tile * BN + r;
-  };
-  uint32_t va[IA], vb[IB];
-#pragma unroll
-  for (int q = 0; q < IB; ++q) {
-    const int chunk = (wave * IB + q) * 64 + lane, r = chunk >> 2;
-    vb[q] = (uint32_t)(b_row(r) * wrow + 16 * ((chunk & 3) ^ swz_b16(r)));
-  }
-  const bool has_sc = wave < BN / 64;
-  const uint32_t vs = (uint32_t)(b_row(64 * (has_sc ? wave : 0) + lane) * srow);
-  auto issue_a = [&](uint8_t* slot, int st) {
-#pragma unroll
-    for (int q = 0; q < IA; ++q) buf_dma16(ra, slot + (wave * IA + q) * 1024, va[q], (uint32_t)st * 128);
-  };
-  auto issue_b = [&](uint8_t* slot, int h) {
-#pragma unroll
-    for (int q = 0; q < IB; ++q) buf_dma16(rb, slot + (wave * IB + q) * 1024, vb[q], (uint32_t)h * 64);
-  };
-  auto issue_s = [&](int grp) {
-    if (has_sc) buf_dma16(rbs, &ring.S[grp & 1][wave * 1024], vs, (uint32_t)grp * 16);
-  };
-  issue_s(0);
-  issue_b(ring.B[0], 0);
-  // rows past m are past the resource
-#pragma unroll
-  for (int q = 0; q < IA; ++q) {
-    const int chunk = (wave * IA + q) * 64 + lane, r = chunk >> 3;
-    int64_t src = r;  // relative to row0
-    if (a.pair) {
-      src = a.a_rows;
-      if (r < m) src = min((int64_t)((uint32_t)a.pair[row0 + r] / (uint32_t)a.topk), a.a_rows);
-    }
-    va[q] = (uint32_t)(src * K * 2 + 16 * ((chunk & 7) ^ swz_a16(r)));
-  }
-#pragma unroll
-  for (int st = 0; st < NA - 1; ++st)
-    if (st < nst) issue_a(ring.A[st], st);
-
-  v16f acc[2][FN];
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int f = 0; f < FN; ++f) acc[i][f] = v16f{};
-  int brow_l[FN], aoff[2], boff[FN];
-#pragma unroll
-  for (int f = 0; f < FN; ++f) {
-    if (kSwiglu) brow_l[f] = (f < FN / 2 ? 0 : BN / 2) + FN * 16 * wn + 32 * (f % (FN > 1 ? FN / 2 : 1)) + r32;
-    else brow_l[f] = 32 * (FN * wn + f) + r32;
-    boff[f] = brow_l[f] * 64 + 16 * (g ^ swz_b16(brow_l[f]));
-  }
-#pragma unroll
-  for (int f = 0; f < 2; ++f) {
-    const int r = 64 * wm + 32 * f + r32;
-    aoff[f] = r * 128 + 16 * ((4 * g) ^ swz_a16(r));
-  }
-
-  auto compute = [&](const uint8_t* As, const uint8_t* Bs, auto Odd, int st) {
-    constexpr int odd = decltype(Odd)::value;  // stages of 128 k: blocks 0, 1 then 2, 3 of a row's codes
-    const uint8_t* const Ss = &ring.S[(st / P) & 1][4 * (kNV ? st & 3 : (st & 7) >> 1)];
-    v4i b[FN], av[2][4];
-    uint32_t sd[FN];
-#pragma unroll
-    for (int f = 0; f < FN; ++f) {
-      int o = boff[f];
-      asm volatile("" : "+v"(o));
-      sd[f] = *reinterpret_cast<const uint32_t*>(Ss + 16 * brow_l[f]);
-      b[f] = *reinterpret_cast<const v4i*>(Bs + (o ^ (32 * odd)));
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int f = 0; f < 2; ++f) {
-        int o = aoff[f];
-        asm volatile("" : "+v"(o));
-        av[f][j] = *reinterpret_cast<const v4i*>(As + (o ^ (16 * j)));
-      }
-    float sc[FN][2];
-#pragma unroll
-    for (int f = 0; f < FN; ++f) {
-      if (kNV) {
-        sc[f][0] = ue4m3_to_f32((sd[f] >> (16 * g)) & 0xFFu);
-        sc[f][1] = ue4m3_to_f32((sd[f] >> (16 * g + 8)) & 0xFFu);
-      } else {
-        sc[f][0] = sc[f][1] = ue8m0_to_f32((sd[f] >> (8 * (2 * odd + g))) & 0xFFu);
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int f = 0; f < FN; ++f) {
-        const v8bf wv = kNV ? decode8_nv((uint32_t)b[f][j], sc[f][j >> 1]) : decode8((uint32_t)b[f][j], sc[f][0]);
-#pragma unroll
-        for (int fm = 0; fm < 2; ++fm) acc[fm][f] = mfma32x32x16(wv, __builtin_bit_cast(v8bf, av[fm][j]), acc[fm][f]);
-      }
-  };
-  const bool active = 64 * wm < m;
-  // stage st: wait for the copies it needs, meet the other waves (their parts have landed
-  // too, and everyone is done with stage st - 1), issue into what stage st - 1 freed, compute.
-  // Issue order at stage t: on even t the codes of stages t + 2, t + 3 and, every P stages,
-  // the next scale group, then the activations of t + NA - 1. So with NA == 3 only the last
-  // stage's issues may stay in flight: A, and after an even stage B (and S) before it.
-  auto step = [&](auto I, int st) {
-    constexpr int i = decltype(I)::value;
-    if (NA == 2 || st + 1 >= nst) {
-      wait_vmcnt<0>();
-    } else if (i % 2 == 0) {
-      wait_vmcnt<IA>();
-    } else if (has_sc && (st - 1) % P == 0 && st - 1 + P < nst) {
-      wait_vmcnt<IA + IB + 1>();
-    } else {
-      wait_vmcnt<IA + IB>();
-    }
-    lds_barrier();
-    if (i % 2 == 0 && st + 2 < nst) issue_b(ring.B[(i / 2 + 1) % 2], st / 2 + 1);
-    if (i % 2 == 0 && st % P == 0 && st + P < nst) issue_s(st / P + 1);
-    if (st + NA - 1 < nst) issue_a(ring.A[(i + NA - 1) % NA], st + NA - 1);
-    __builtin_amdgcn_sched_barrier(0);
-    if (active) compute(ring.A[i % NA], ring.B[(i / 2) % 2], std::integral_constant<int, i % 2>{}, st);
-  };
-  constexpr int U = NA == 3 ? 12 : 4;  // whole turns of the A and B slots
-  for (int st = 0; st < nst; st += U)  // nst is even
-    static_for<0, U / 2>([&](auto X_) {
-      constexpr int X = 2 * decltype(X_)::value;
-      if (st + X < nst) {
-        step(std::integral_constant<int, X>{}, st + X);
-        step(std::integral_constant<int, X + 1>{}, st + X + 1);
-      }
-    });
-
-  // adapters: for each segment with rows here, acc += low . lora_b^T over the rank, low
-  // (scaled, fp32) held as two bf16 terms (16 significant bits: the adapter's share keeps an
-  // error of 2^-16 of itself). 64 segments' bounds and adapters are read at once, and the
-  // operands of the next 16 ranks are loaded before the current ones are multiplied, so that
-  // many short segments cost their loads and not their latency.
-  if (kLora && active) {
-    const int64_t rlo = row0 + 64 * wm, rhi = min(rlo + 64, row0 + m);
-    int s0 = first_segment(a.seg_off, a.S, rlo);
-    int lo_l = 0, hi_l = 0, l_l = 0, k_next = a.rank;
-    int lo = 0, hi = 0, l = 0;  // the segment of the operands to load, relative to rlo
-    unsigned long long mask = 0;
-    bool more = s0 < a.S;
-    auto advance = [&]() -> bool {  // the next 16 ranks: of the same segment, or the next one's first
-      k_next += 16;
-      if (k_next < a.rank) return true;
-      while (mask == 0) {
-        if (!more) return false;
-        const int s = s0 + lane;
-        const bool in = s < a.S;
-        const int64_t b0 = a.seg_off[in ? s : 0], b1 = a.seg_off[in ? s + 1 : 0];
-        l_l = in ? a.seg_adapter[s] : -1;
-        lo_l = (int)(max(b0, rlo) - rlo);
-        hi_l = (int)(min(b1, rhi) - rlo);
-        mask = __ballot(in && b0 < rhi && b1 > rlo && hi_l > lo_l && l_l >= 0 && l_l < a.L);
-        s0 += 64;
-        more = s0 < a.S && __ballot(in && b0 >= rhi) == 0;
-      }
-      const int i = __ffsll((long long)mask) - 1;
-      mask &= mask - 1;
-      lo = __builtin_amdgcn_readlane(lo_l, i);
-      hi = __builtin_amdgcn_readlane(hi_l, i);
-      l = __builtin_amdgcn_readlane(l_l, i);
-      k_next = 0;
-      return true;
-    };
-    struct Ops {
-      v4i h[2], lo[2], b[FN];
-    };
-    auto load = [&](Ops& o) {
-      const int k = k_next + 8 * g;
-      const bool kin = k < a.rank;
-#pragma unroll
-      for (int fm = 0; fm < 2; ++fm) {
-        const int t = 32 * fm + r32;
-        const bool ok = t >= lo && t < hi && kin;
-        const int64_t at = ok ? (rlo + t) * a.rank + k : 0;
-        o.h[fm] = *reinterpret_cast<const v4i*>(a.low_hi + at);
-        o.lo[fm] = *reinterpret_cast<const v4i*>(a.low_lo + at);
-        if (!ok) o.h[fm] = o.lo[fm] = v4i{};
-      }
-#pragma unroll
-      for (int f = 0; f < FN; ++f) {
-        const int64_t n = min((int64_t)n_tile * BN + brow_l[f], N - 1);
-        o.b[f] = *reinterpret_cast<const v4i*>(a.lora_b + ((int64_t)l * N + n) * a.rank + (kin ? k : 0));
-        if (!kin) o.b[f] = v4i{};
-      }
-    };
-    Ops cur, nxt;
-    bool have = advance();
-    if (have) load(cur);
-    while (have) {
-      const bool next = advance();
-      if (next) load(nxt);
-#pragma unroll
-      for (int f = 0; f < FN; ++f)
-#pragma unroll
-        for (int fm = 0; fm < 2; ++fm) {
-          const v8bf bw = __builtin_bit_cast(v8bf, cur.b[f]);
-          acc[fm][f] = mfma32x32x16(bw, __builtin_bit_cast(v8bf, cur.lo[fm]), acc[fm][f]);
-          acc[fm][f] = mfma32x32x16(bw, __builtin_bit_cast(v8bf, cur.h[fm]), acc[fm][f]);
-        }
-      cur = nxt;
-      have = next;
-    }
-  }
-
-  // epilogue: 32 rows x CP columns at a time through the wave's 8 KB of the ring (runs of
-  // 4 columns in, 16-byte pieces of whole row segments out)
-  lds_barrier();  // every wave is done with the ring
-  if (!active) return;
-  constexpr int ES = kOutBF16 ? 2 : 4, OF = kSwiglu ? FN / 2 : FN;
-  constexpr int PF = OF * 32 * ES > 256 ? 256 / (32 * ES) : OF;  // fragments per pass
-  constexpr int RB = PF * 32 * ES, NCH = RB / 16;
-  static_assert(OF % PF == 0, "passes");
-  uint8_t* const stg = reinterpret_cast<uint8_t*>(&ring) + wave * 8192;
-  const int64_t ocols = kSwiglu ? half : N;
-  const int64_t col0 = ((int64_t)n_tile * BN >> (kSwiglu ? 1 : 0)) + OF * 32 * wn;
-#pragma unroll
-  for (int fm = 0; fm < 2; ++fm)
-#pragma unroll
-    for (int p = 0; p < OF / PF; ++p) {
-#pragma unroll
-      for (int f = 0; f < PF; ++f)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          float v[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float x = acc[fm][p * PF + f][4 * j + i];
-            if constexpr (kSwiglu) v[i] = silu_mul(x, acc[fm][p * PF + f + FN / 2][4 * j + i]);
-            else v[i] = x;
-          }
-          if (kOutBF16) {
-            const int c = (4 * f + j) ^ (r32 & (NCH - 1));
-            *reinterpret_cast<uint2*>(stg + RB * r32 + 16 * c + 8 * g) =
-                make_uint2(bf16x2_bits(v[0], v[1]), bf16x2_bits(v[2], v[3]));
-          } else {
-            const int c = (8 * f + 2 * j + g) ^ (r32 & (NCH - 1));
-            *reinterpret_cast<float4*>(stg + RB * r32 + 16 * c) = make_float4(v[0], v[1], v[2], v[3]);
-          }
-        }
-      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-#pragma unroll
-      for (int k = 0; k < NCH / 2; ++k) {
-        const int idx = lane + 64 * k, rr = idx / NCH, c = idx % NCH;
-        const v4i v = *reinterpret_cast<const v4i*>(stg + RB * rr + 16 * (c ^ (rr & (NCH - 1))));
-        const int lrow = 64 * wm + 32 * fm + rr;
-        const int64_t col = col0 + p * PF * 32 + c * (16 / ES);
-        if (lrow < m && col < ocols)
-          *reinterpret_cast<v4i*>(static_cast<uint8_t*>(a.out) + ((row0 + lrow) * ocols + col) * ES) = v;
-      }
-      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    }
+  w16_tile<BM, BN, NW, NA, kNV, kSwiglu, kOutBF16, kLora, false>(a, ring, (int)(blockIdx.x & 7u), (int)(blockIdx.x >> 3),
+                                                                 0);
 }
 
 template <int BM, int BN, int NW, int NA, bool kSwiglu, bool kLora>

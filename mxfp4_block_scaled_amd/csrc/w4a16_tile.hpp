@@ -1,5 +1,5 @@
 // Arguments and work lookup of the FP4-weight x bf16-activation kernels over ragged rows
-// (w4a16_tile.hip, w4a16_grouped.hip, w4a16_lora.hip).
+// (w4a16_tile_body.hpp, w4a16_tile.hip, w4a16_grouped.hip, w4a16_lora.hip).
 #pragma once
 
 #include "w4a16_common.hpp"
@@ -21,7 +21,8 @@ struct W16TileArgs {
   int ntiles;
   // adapters (w4a16_lora.hip)
   const uint16_t *low_hi, *low_lo;  // [R][rank] bf16 each: scaling * a . lora_a^T as the sum of two terms
-  int rank, L, S;
+  int rank, L, S, lslices;  // low: lslices K slices [lslices][R][rank], each as its two terms
+  int kslices;              // K slices of a sliced product
   const int32_t* seg_off;      // [S+1]
   const int32_t* seg_adapter;  // [S]
   const uint16_t* lora_b;      // [L][N][rank] bf16
@@ -40,6 +41,9 @@ template <int BM>
 __device__ __forceinline__ int w16_units(int c, int lo_rows, int hi_rows) {
   return c <= lo_rows || c > hi_rows ? 0 : (c + BM - 1) / BM;
 }
+
+// the first of n items that belongs to share i of s
+__device__ __forceinline__ uint32_t w16_share(uint32_t n, int i, int s) { return n * (uint32_t)i / (uint32_t)s; }
 
 // x n / 8 without leaving 32 bits
 __device__ __forceinline__ uint32_t w16_eighths(uint32_t n, int x) {

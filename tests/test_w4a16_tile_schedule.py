@@ -1,4 +1,4 @@
-"""Host replay of the tiled FP4 x bf16 kernel's copy schedule and lane layout (csrc/w4a16_tile.hip), for each tile
+"""Host replay of the tiled FP4 x bf16 kernel's copy schedule and lane layout (csrc/w4a16_tile_body.hpp), for each tile
 shape it is built in: every copy's source and LDS bytes, coverage of a slot, what each fragment read returns (every
 row's k of the stage exactly once, the same k for both operands), the scale byte it is multiplied with, and the
 hand-over of the three slots."""
@@ -136,8 +136,9 @@ def test_epilogue_staging_round_trip(OF, es):
 @pytest.mark.parametrize("nst", [2, 4, 6, 8, 10, 32, 112])
 @pytest.mark.parametrize("NA", [2, 3])
 @pytest.mark.parametrize("P", [4, 8])
+@pytest.mark.parametrize("st0", [0, 2, 4, 6, 14])  # a K slice's first stage
 @pytest.mark.parametrize("IA,IB,has_sc", [(4, 2, True), (4, 2, False), (4, 4, True), (2, 4, True), (2, 2, False)])
-def test_slots_are_handed_over(nst, NA, P, IA, IB, has_sc):
+def test_slots_are_handed_over(nst, NA, P, st0, IA, IB, has_sc):
     """A stage is computed only after its copies landed, and a slot refilled only after every wave is done with it."""
     outstanding, A, B, S = [], {}, {}, {}
 
@@ -154,18 +155,23 @@ def test_slots_are_handed_over(nst, NA, P, IA, IB, has_sc):
         if has_sc:
             outstanding.append(("S", grp))
 
-    issue_s(0)
-    issue_b(0, 0)
-    for st in range(min(NA - 1, nst)):
-        issue_a(st, st)
+    end = st0 + nst
+
+    def next_s(st):
+        return (st % P == 0 or st == st0) and (st // P + 1) * P < end
+
+    issue_s(st0 // P)
+    issue_b(0, st0 // 2)
+    for i in range(min(NA - 1, nst)):
+        issue_a(i, st0 + i)
     U = 12 if NA == 3 else 4
-    for st in range(nst):
-        i = st % U
-        if NA == 2 or st + 1 >= nst:
+    for st in range(st0, end):
+        i = (st - st0) % U
+        if NA == 2 or st + 1 >= end:
             allowed = 0
         elif i % 2 == 0:
             allowed = IA
-        elif has_sc and (st - 1) % P == 0 and st - 1 + P < nst:
+        elif has_sc and next_s(st - 1):
             allowed = IA + IB + 1
         else:
             allowed = IA + IB
@@ -173,18 +179,18 @@ def test_slots_are_handed_over(nst, NA, P, IA, IB, has_sc):
         needed = {("A", st), ("B", st // 2), ("S", st // P)}
         assert not needed & set(outstanding)
         # after the barrier every wave is done with stage st - 1: what it and older stages read may be refilled
-        if i % 2 == 0 and st + 2 < nst:
+        if i % 2 == 0 and st + 2 < end:
             slot = (i // 2 + 1) % 2
             assert B.get(slot, -1) < (st // 2)
             issue_b(slot, st // 2 + 1)
-        if i % 2 == 0 and st % P == 0 and st + P < nst:
+        if i % 2 == 0 and next_s(st):
             assert S.get((st // P + 1) & 1, -1) < st // P
             issue_s(st // P + 1)
-        if st + NA - 1 < nst:
+        if st + NA - 1 < end:
             slot = (i + NA - 1) % NA
             assert A.get(slot, -1) < st
             issue_a(slot, st + NA - 1)
-        assert A[i % NA] == st and B[(i // 2) % 2] == st // 2 and S[(st // P) & 1] == st // P
+        assert A[i % NA] == st and B[(i // 2) % 2] == st // 2 and S[(st // P) & 1] == st // P and i % 2 == st % 2
     assert not outstanding
 
 
