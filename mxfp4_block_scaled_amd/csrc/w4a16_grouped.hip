@@ -192,9 +192,14 @@ void launch_stream(W16TileArgs a, bool nv, bool swiglu, bool out_bf16, int64_t u
   else launch_stream_t<false, false>(a, out_bf16, grid, stream);
 }
 
-// calls of at most this many rows run in the streaming kernel alone (one launch), experts of
-// more than 16 rows in units of 16 that read the weights again from the cache
-constexpr int64_t kStreamRows = 128;
+// Small calls run in the streaming kernel alone (one launch), experts of more than 16 rows in
+// units of 16 that read the weights again from the cache: calls of at most kStreamRows rows,
+// and those of at most kStreamItems workgroups. Its time grows with items x K (5 us a million),
+// that of the tiled launches with the longest chain, 0.9 us for each 64 k. Measured (streamed /
+// tiled, us): 8 experts x 2048 x 2048, 1024 rows (2304 items) 26 / 33, 2048 rows (4352) 48 / 35;
+// 4 x 4096 x 7168, 512 rows (2304) 86 / 93, 1024 rows (4352) 154 / 95; 64 x 512 x 512, 2048 rows
+// (1536) 10.9 / 11.2.
+constexpr int64_t kStreamRows = 128, kStreamItems = 2560;
 
 // units that experts of lo < rows <= hi can make of R rows in all
 int64_t most_units(int64_t R, int E, int64_t lo, int bm) {
@@ -207,10 +212,11 @@ int64_t most_units(int64_t R, int E, int64_t lo, int bm) {
 int launch_w16_grouped(W16TileArgs a, bool nv, bool swiglu, bool out_bf16, hipStream_t stream) {
   constexpr int kAll = 0x7FFFFFFF;
   const int64_t R = a.R;
+  const bool small = R <= kStreamRows || most_units(R, a.E, 0, 16) * cdiv(a.N, 64) <= kStreamItems;
   a.min_rows = 0;
-  a.max_rows = R <= kStreamRows ? kAll : 16;
-  launch_stream(a, nv, swiglu, out_bf16, most_units(R, a.E, 0, R <= kStreamRows ? 16 : 0), stream);
-  if (R <= kStreamRows) return hipGetLastError() == hipSuccess ? 0 : -1;
+  a.max_rows = small ? kAll : 16;
+  launch_stream(a, nv, swiglu, out_bf16, most_units(R, a.E, 0, small ? 16 : 0), stream);
+  if (small) return hipGetLastError() == hipSuccess ? 0 : -1;
   a.min_rows = 16;
   a.max_rows = 64;
   launch_w16_tile_grouped(a, nv, swiglu, out_bf16, 64, most_units(R, a.E, 16, 0), stream);

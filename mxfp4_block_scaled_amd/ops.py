@@ -570,19 +570,22 @@ def moe_block_norm(y, x=None, post_weight=None, gate=None, residual_scale=1.0, p
 
 
 def moe_layer(x, logits, w1, w1_scale, w2, w2_scale, topk, act_fmt="e4m3", y_dtype=torch.bfloat16,
-              out_dtype=torch.bfloat16, fused=False):
+              out_dtype=torch.bfloat16, fused=False, w_fmt="mxfp4"):
     """The whole expert layer through the C-ABI calls (one stream, no host sync).
     fused=True (T <= 64): quantisation and routing in one launch (E <= 256), FC2 and
     the combine in one kernel; y is not formed (None).
     act_fmt="bf16": the activations enter the expert products as they are (no
-    quantisation: q, q_scale and h_scale are None, h is bf16)."""
+    quantisation: q, q_scale and h_scale are None, h is bf16); then the weights may be
+    NVFP4 (w_fmt="nvfp4") too."""
     T = x.shape[0]
+    if act_fmt != "bf16" and w_fmt != "mxfp4":
+        raise RuntimeError("w_fmt: NVFP4 weights need act_fmt=\"bf16\"")
     if act_fmt == "bf16":
         if fused:
             raise RuntimeError("fused: the bf16 layer has no fused form")
         ids, gates, offs, sp, pr = moe_route_permute(logits, topk)
-        h = moe_grouped_gemm_w4a16(x, offs, w1, w1_scale, sorted_pair=sp, topk=topk, swiglu=True)
-        y = moe_grouped_gemm_w4a16(h, offs, w2, w2_scale, out_dtype=y_dtype)
+        h = moe_grouped_gemm_w4a16(x, offs, w1, w1_scale, w_fmt, sorted_pair=sp, topk=topk, swiglu=True)
+        y = moe_grouped_gemm_w4a16(h, offs, w2, w2_scale, w_fmt, out_dtype=y_dtype)
         out = moe_unpermute_combine(y, gates, pr, T, topk, out_dtype)
         return dict(q=None, q_scale=None, topk_ids=ids, gates=gates, expert_offsets=offs, sorted_pair=sp, pair_row=pr,
                     h=h, h_scale=None, y=y, out=out)

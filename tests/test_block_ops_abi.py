@@ -103,3 +103,5 @@ def test_bf16_layer_has_no_fused_form():
     x = torch.zeros(2, 512, dtype=torch.bfloat16)
     with pytest.raises(RuntimeError, match="fused"):
         ops.moe_layer(x, None, None, None, None, None, 2, act_fmt="bf16", fused=True)
+    with pytest.raises(RuntimeError, match="w_fmt"):
+        ops.moe_layer(x, None, None, None, None, None, 2, act_fmt="e4m3", w_fmt="nvfp4")

@@ -77,6 +77,12 @@ CASES = [
     ([130, 70], 0, 0, 48, 2048, "nvfp4", False, torch.bfloat16),
     ([200, 90, 513], 0, 0, 576, 320 * 2, "nvfp4", True, torch.float32),
     ([8] * 70, 0, 0, 80, 256, "mxfp4", False, torch.float32),  # more experts than lanes
+    # wide enough for the tiled kernels beside the streaming one (more than 2560 streamed workgroups)
+    ([300, 1, 20, 64, 65, 0, 16, 17, 257], 3, 5, 4112, 128, "mxfp4", False, torch.float32),
+    ([130, 63, 500, 40], 0, 0, 4128, 384, "nvfp4", True, torch.bfloat16),
+    ([90, 33, 128, 5, 700], 1, 0, 3616, 640, "mxfp4", True, torch.float32),
+    ([256, 129, 18, 2, 0, 260], 0, 7, 4368, 1152, "nvfp4", False, torch.bfloat16),
+    ([3] * 260 + [40, 70], 0, 0, 1040, 256, "mxfp4", False, torch.float32),  # more experts than a lane batch holds
 ]
 
 
@@ -106,9 +112,9 @@ def test_against_64_bits(case, gather):
 def test_one_row_is_its_own():
     """A row does not depend on what else its expert or the others hold: NaN and infinite rows beside it change
     nothing, and each row alone gives the bits that it gives among others of the same class."""
-    E, N, K = 3, 320, 512
+    E, N, K = 3, 4096, 256
     w, s, _ = weights(E, N, K, "mxfp4", 5)
-    for counts in ([4, 9, 2], [40, 20, 61], [100, 300, 80]):
+    for counts in ([4, 9, 2], [40, 20, 61], [100, 500, 80], [50, 60, 600]):
         R = sum(counts)
         offs = torch.tensor(np.cumsum([0] + counts), dtype=torch.int32).cuda()
         a = torch.randn(R, K, generator=torch.Generator().manual_seed(R)).to(torch.bfloat16).cuda()
@@ -125,7 +131,12 @@ def test_one_row_is_its_own():
 
 def test_offsets_are_held_to_the_rows():
     """Offsets outside [0, R] are taken as 0 and R; every write stays inside y."""
-    E, N, K, R = 3, 64, 256, 40
+    for R, N in ((40, 64), (700, 4096)):
+        check_offsets(R, N)
+
+
+def check_offsets(R, N):
+    E, K = 3, 128
     w, s, hat = weights(E, N, K, "mxfp4", 9)
     a = torch.randn(R, K).to(torch.bfloat16)
     raw = torch.full((3 * R, N), 3.0, device="cuda")
@@ -136,10 +147,10 @@ def test_offsets_are_held_to_the_rows():
     assert (raw[:R] == 3).all() and (raw[2 * R:] == 3).all()
 
 
-@pytest.mark.parametrize("R", [40, 300])
-def test_pairs_outside_the_rows_stay_inside_a(R):
+@pytest.mark.parametrize("R,N", [(40, 64), (800, 4096)])
+def test_pairs_outside_the_rows_stay_inside_a(R, N):
     """Entries of sorted_pair outside their range spoil their own rows only."""
-    E, N, K, topk = 2, 64, 256, 2
+    E, K, topk = 2, 256, 2
     w, s, _ = weights(E, N, K, "mxfp4", 10)
     a = torch.randn(R // topk, K).to(torch.bfloat16).cuda()
     offs = torch.tensor([0, 12, R], dtype=torch.int32).cuda()
@@ -155,9 +166,8 @@ def test_pairs_outside_the_rows_stay_inside_a(R):
 
 def test_extreme_scale_bytes():
     """UE8M0 bytes at both ends of 2..252 in the streamed and the tiled kernel."""
-    N, K = 64, 256
     g = np.random.default_rng(3)
-    for counts in ([3], [30], [90]):
+    for counts, N, K in (([3], 64, 256), ([30], 64, 256), ([700], 4096, 128)):
         for lo, hi, shift in ((2, 6, 60), (248, 252, -60)):
             w = g.integers(0, 256, (1, N, K // 2), dtype=np.uint8)
             s = g.integers(lo, hi + 1, (1, N, K // 32), dtype=np.uint8)
@@ -171,17 +181,20 @@ def test_extreme_scale_bytes():
 
 
 def test_every_ue4m3_scale():
-    N, K = 128, 1024
+    for R, N, K in ((2, 128, 1024), (33, 128, 1024), (700, 4096, 256)):
+        check_ue4m3(R, N, K)
+
+
+def check_ue4m3(R, N, K):
     w = np.random.default_rng(4).integers(0, 256, (1, N, K // 2), dtype=np.uint8)
     s = (np.arange(N * K // 16) % 0x7F).astype(np.uint8).reshape(1, N, K // 16)
     hat = torch.from_numpy(oracle.dequant_nvfp4_weights(w[0], s[0]))[None].double()
-    for R in (2, 33, 129):
-        a = torch.randn(R, K).to(torch.bfloat16)
-        y = ops.moe_grouped_gemm_w4a16(a.cuda(), torch.tensor([0, R], dtype=torch.int32).cuda(),
-                                       torch.from_numpy(w).cuda(), torch.from_numpy(s).cuda(), "nvfp4",
-                                       out_dtype=torch.float32)
-        want, d = reference(a, torch.arange(R), [0, R], hat, False)
-        assert_close(y, want, d, "y")
+    a = torch.randn(R, K).to(torch.bfloat16)
+    y = ops.moe_grouped_gemm_w4a16(a.cuda(), torch.tensor([0, R], dtype=torch.int32).cuda(),
+                                   torch.from_numpy(w).cuda(), torch.from_numpy(s).cuda(), "nvfp4",
+                                   out_dtype=torch.float32)
+    want, d = reference(a, torch.arange(R), [0, R], hat, False)
+    assert_close(y, want, d, "y")
 
 
 def test_no_rows():
