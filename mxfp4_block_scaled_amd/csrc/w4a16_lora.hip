@@ -147,22 +147,20 @@ __global__ void __launch_bounds__(NW * 64) lora_shrink_kernel(ShrinkArgs p) {
   if (blk < w16_eighths(nb, x + 1)) lora_shrink<MF, RF, NW, false>(p, lds, blk, (int)blockIdx.y, (int)blockIdx.z);
 }
 
-// M <= 64: the first nshrink workgroups shrink (their row block slowest), the others each
-// take a tile of the projection over a K slice
+// M <= 64: the first workgroups each take a tile of the projection over a K slice, the others
+// shrink (their row block slowest)
 template <int RF, bool kNV>
-__global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) lora_decode_kernel(ShrinkArgs p, W16TileArgs a,
-                                                                                                int nshrink) {
+__global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) lora_decode_kernel(ShrinkArgs p, W16TileArgs a) {
   __shared__ union Lds {
     ShrinkLds<1, RF, 4> s;
     W16Ring<64, 128, 3> ring;
   } lds;
-  const int b = (int)blockIdx.x;
-  if (b < nshrink) {
-    const int per = p.slices * p.zsplit, i = b % per;
-    lora_shrink<1, RF, 4, true>(p, lds.s, (uint32_t)(b / per), i % p.slices, i / p.slices);
-  } else {  // slice by slice; within a slice the n-tiles are spread over the XCDs
-    const int i = b - nshrink;
-    w16_tile<64, 128, 4, 3, kNV, false, false, false, true>(a, lds.ring, 0, i % a.ntiles, i / a.ntiles);
+  const int nbase = a.ntiles * a.kslices, b = (int)blockIdx.x;
+  if (b < nbase) {  // slice by slice; within a slice the n-tiles are spread over the XCDs
+    w16_tile<64, 128, 4, 3, kNV, false, false, false, true>(a, lds.ring, 0, b % a.ntiles, b / a.ntiles);
+  } else {
+    const int per = p.slices * p.zsplit, i = (b - nbase) % per;
+    lora_shrink<1, RF, 4, true>(p, lds.s, (uint32_t)((b - nbase) / per), i % p.slices, i / p.slices);
   }
 }
 
@@ -186,8 +184,8 @@ template <int RF>
 void launch_decode(const ShrinkArgs& s, const W16TileArgs& a, bool nv, hipStream_t stream) {
   const int nshrink = s.S > 0 ? (int)cdiv(s.M, 16) * s.slices * s.zsplit : 0;
   const dim3 grid((unsigned)(nshrink + a.ntiles * a.kslices));
-  if (nv) lora_decode_kernel<RF, true><<<grid, 256, 0, stream>>>(s, a, nshrink);
-  else lora_decode_kernel<RF, false><<<grid, 256, 0, stream>>>(s, a, nshrink);
+  if (nv) lora_decode_kernel<RF, true><<<grid, 256, 0, stream>>>(s, a);
+  else lora_decode_kernel<RF, false><<<grid, 256, 0, stream>>>(s, a);
 }
 
 struct FinishArgs {
@@ -201,7 +199,7 @@ struct FinishArgs {
   int bslices, lslices, rank, L, S;
 };
 
-constexpr int kMaxBaseSlices = 8;
+constexpr int kMaxBaseSlices = 8, kMaxLowSlices = 16;
 
 // one row, 256 columns per workgroup of one wave: 4 columns per lane
 template <bool kOutBF16>
@@ -230,8 +228,12 @@ __global__ void __launch_bounds__(64) lora_finish_kernel(FinishArgs p) {
   }
   if (has)
     for (int r = threadIdx.x; r < p.rank; r += 64) {
-      float v = 0.0f;
-      for (int i = 0; i < p.lslices; ++i) v += p.low[((int64_t)i * p.M + t) * p.rank + r];
+      float w[kMaxLowSlices], v = 0.0f;
+#pragma unroll
+      for (int i = 0; i < kMaxLowSlices; ++i)  // all on their way before the first is added
+        w[i] = i < p.lslices ? p.low[((int64_t)i * p.M + t) * p.rank + r] : 0.0f;
+#pragma unroll
+      for (int i = 0; i < kMaxLowSlices; ++i) v += w[i];
       low[r] = v;
     }
   __syncthreads();
@@ -270,7 +272,7 @@ __global__ void __launch_bounds__(64) lora_finish_kernel(FinishArgs p) {
 int lora_shrink_slices(int64_t M, int64_t K) {
   // M <= 64: K slices of at least 256 (64 for each of a workgroup's 4 waves), up to 16. More
   // rows: with blocks of 32 rows about a workgroup a compute unit, each slice of at least 1024
-  if (M <= 64) return (int)(K / 256 < 16 ? K / 256 : 16);
+  if (M <= 64) return (int)(K / 256 < kMaxLowSlices ? K / 256 : kMaxLowSlices);
   const int64_t want = 256 / cdiv(M, 32), most = K / 1024 < 4 ? K / 1024 : 4;
   const int64_t n = want < most ? want : most;
   return (int)(n > 1 ? n : 1);
@@ -292,8 +294,10 @@ int launch_w16_lora(const W16LoraArgs& p, bool nv, bool out_bf16, hipStream_t st
   float* const low = base + (int64_t)bs * p.M * p.N;
   uint16_t* const low_hi = reinterpret_cast<uint16_t*>(low);  // M > 64: two bf16 terms in fp32's place
   uint16_t* const low_lo = low_hi + (int64_t)ls * p.M * p.rank;
-  const int64_t blocks = cdiv(p.M, 16);
-  const int z = (int)(cdiv(p.S, blocks) < 16 ? cdiv(p.S, blocks) : 16);
+  const int64_t blocks = cdiv(p.M, 16), per_block = cdiv(p.S, blocks);
+  const int z = (int)(per_block < 1 ? 1 : per_block < 16 ? per_block : 16);
+  // what fits the compute units beside the projection's tiles
+  if (p.M <= 64 && ls > 512 / (blocks * z)) ls = (int)(512 / (blocks * z) > 1 ? 512 / (blocks * z) : 1);
   const ShrinkArgs s{p.a, p.lora_a, p.scaling, p.seg_off, p.seg_adapter, low, low_hi, low_lo, p.M, p.K, p.rank, p.L, p.S,
                      z, ls};
   W16TileArgs a{};
