@@ -296,8 +296,8 @@ int moe_grouped_gemm_w4a16(const uint16_t* a, int64_t a_rows, int64_t R, const i
 
 size_t fp4_w4a16_lora_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t rank) {
   if (M <= 0 || N <= 0 || K <= 0 || rank <= 0) return 0;
-  const size_t base = (size_t)mxf::lora_base_slices(M, N, K) * (size_t)M * (size_t)N;
-  const size_t low = (size_t)mxf::lora_shrink_slices(M, K) * (size_t)M * (size_t)rank;
+  const size_t base = (size_t)mxf::lora_base_slices(M, N, K, rank) * (size_t)M * (size_t)N;
+  const size_t low = (size_t)mxf::lora_shrink_slices(M, N, K, rank) * (size_t)M * (size_t)rank;
   return round_up((base + low) * sizeof(float), 256);
 }
 

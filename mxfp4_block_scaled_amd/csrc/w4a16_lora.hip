@@ -2,12 +2,14 @@
 //   c[t] = a[t] . W_hat^T + scaling[l] * (a[t] . lora_a[l]^T) . lora_b[l]^T
 // with l = seg_adapter[s] of the segment s that holds row t (negative: no adapter).
 //   shrink:  low[t] = scaling[l] * a[t] . lora_a[l]^T in fp32
-//   M > 64:  the shrink, then the tiled product (w4a16_tile_body.hpp), which takes
-//            low . lora_b^T into its accumulators after the last stage, so c is written once.
-//   M <= 64: a launch in which some workgroups shrink and the others compute K slices of the
-//            projection (N alone gives too few tiles to fill the chip), then one pass that adds
-//            the slices and the fp32 expansion. Two launches, since a call of this size costs
-//            its launches and latencies.
+//   tiles enough to fill the chip: the shrink, then the tiled product (w4a16_tile_body.hpp),
+//            which takes low . lora_b^T into its accumulators after the last stage, so c is
+//            written once.
+//   fewer:   a launch in which some workgroups compute K slices of the projection's tiles and the
+//            others shrink, then one pass that adds the slices and the fp32 expansion: at these
+//            sizes a call costs its launches and the length of its K chain (256 requests of one
+//            row at 4096 x 7168, rank 16: 77 us with whole-K tiles, whose last stage walks 64
+//            segments, ... sliced).
 #include "w4a16_tile_body.hpp"
 
 namespace mxf {
@@ -137,7 +139,7 @@ __device__ __forceinline__ void lora_shrink(const ShrinkArgs& p, ShrinkLds<MF, R
   }
 }
 
-// M > 64: grid (8 x row blocks of an XCD, K slices, segments' share)
+// Not sliced: grid (8 x row blocks of an XCD, K slices, segments' share)
 template <int MF, int RF, int NW>
 __global__ void __launch_bounds__(NW * 64) lora_shrink_kernel(ShrinkArgs p) {
   __shared__ ShrinkLds<MF, RF, NW> lds;
@@ -147,7 +149,7 @@ __global__ void __launch_bounds__(NW * 64) lora_shrink_kernel(ShrinkArgs p) {
   if (blk < w16_eighths(nb, x + 1)) lora_shrink<MF, RF, NW, false>(p, lds, blk, (int)blockIdx.y, (int)blockIdx.z);
 }
 
-// M <= 64: the first workgroups each take a tile of the projection over a K slice, the others
+// Sliced: the first workgroups each take a tile of the projection over a K slice, the others
 // shrink (their row block slowest)
 template <int RF, bool kNV>
 __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) lora_decode_kernel(ShrinkArgs p, W16TileArgs a) {
@@ -155,16 +157,16 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) l
     ShrinkLds<1, RF, 4> s;
     W16Ring<64, 128, 3> ring;
   } lds;
-  const int nbase = a.ntiles * a.kslices, b = (int)blockIdx.x;
-  if (b < nbase) {  // slice by slice; within a slice the n-tiles are spread over the XCDs
-    w16_tile<64, 128, 4, 3, kNV, false, false, false, true>(a, lds.ring, 0, b % a.ntiles, b / a.ntiles);
+  const int items = a.ntiles * (int)((a.R + 63) / 64), nbase = items * a.kslices, b = (int)blockIdx.x;
+  if (b < nbase) {  // slice by slice; within a slice the tiles are spread over the XCDs
+    w16_tile<64, 128, 4, 3, kNV, false, false, false, true>(a, lds.ring, 0, b % items, b / items);
   } else {
     const int per = p.slices * p.zsplit, i = (b - nbase) % per;
     lora_shrink<1, RF, 4, true>(p, lds.s, (uint32_t)((b - nbase) / per), i % p.slices, i / p.slices);
   }
 }
 
-// Rows of a workgroup of the shrink (M > 64): 32 where segments are long, so that an adapter is
+// Rows of a workgroup of the shrink (not sliced): 32 where segments are long, so that an adapter is
 // read for twice the rows
 bool shrink_wide(int64_t M, int64_t S) { return M >= 32 * S; }
 
@@ -183,7 +185,7 @@ void launch_shrink(const ShrinkArgs& s, hipStream_t stream) {
 template <int RF>
 void launch_decode(const ShrinkArgs& s, const W16TileArgs& a, bool nv, hipStream_t stream) {
   const int nshrink = s.S > 0 ? (int)cdiv(s.M, 16) * s.slices * s.zsplit : 0;
-  const dim3 grid((unsigned)(nshrink + a.ntiles * a.kslices));
+  const dim3 grid((unsigned)(nshrink + a.ntiles * cdiv(a.R, 64) * a.kslices));
   if (nv) lora_decode_kernel<RF, true><<<grid, 256, 0, stream>>>(s, a);
   else lora_decode_kernel<RF, false><<<grid, 256, 0, stream>>>(s, a);
 }
@@ -269,35 +271,44 @@ __global__ void __launch_bounds__(64) lora_finish_kernel(FinishArgs p) {
 
 }  // namespace
 
-int lora_shrink_slices(int64_t M, int64_t K) {
-  // M <= 64: K slices of at least 256 (64 for each of a workgroup's 4 waves), up to 16. More
-  // rows: with blocks of 32 rows about a workgroup a compute unit, each slice of at least 1024
-  if (M <= 64) return (int)(K / 256 < kMaxLowSlices ? K / 256 : kMaxLowSlices);
-  const int64_t want = 256 / cdiv(M, 32), most = K / 1024 < 4 ? K / 1024 : 4;
-  const int64_t n = want < most ? want : most;
-  return (int)(n > 1 ? n : 1);
+namespace {
+
+// Fewer than 256 tiles of 64 x 128, where the pass over the rows does not read lora_b too often
+// (N x rank for each row, from the cache)
+bool sliced(int64_t M, int64_t N, int rank) {
+  return M <= 64 || (cdiv(M, 64) * cdiv(N, 128) < 256 && M * N * rank <= (int64_t(1) << 26));
 }
 
-int lora_base_slices(int64_t M, int64_t N, int64_t K) {
-  if (M > 64) return 0;
-  // tiles of 128 weight rows and K slices of at least 256 that fill 256 compute units
-  const int64_t want = 256 / cdiv(N, 128), most = K / 256 < kMaxBaseSlices ? K / 256 : kMaxBaseSlices;
-  const int64_t n = want < most ? want : most;
-  return (int)(n > 1 ? n : 1);
+int clamp_slices(int64_t want, int64_t most) { return (int)(want < most ? (want > 1 ? want : 1) : (most > 1 ? most : 1)); }
+
+}  // namespace
+
+int lora_shrink_slices(int64_t M, int64_t N, int64_t K, int rank) {
+  // sliced: K slices of at least 256 (64 for each of a workgroup's 4 waves), as many as fit the
+  // compute units beside the projection's tiles. Else, with blocks of 32 rows, about a workgroup
+  // a compute unit, each slice of at least 1024
+  if (sliced(M, N, rank)) return clamp_slices(512 / cdiv(M, 16), K / 256 < kMaxLowSlices ? K / 256 : kMaxLowSlices);
+  return clamp_slices(256 / cdiv(M, 32), K / 1024 < 4 ? K / 1024 : 4);
+}
+
+int lora_base_slices(int64_t M, int64_t N, int64_t K, int rank) {
+  // K slices of at least 256 for two workgroups a compute unit
+  if (!sliced(M, N, rank)) return 0;
+  return clamp_slices(512 / (cdiv(M, 64) * cdiv(N, 128)), K / 256 < kMaxBaseSlices ? K / 256 : kMaxBaseSlices);
 }
 
 int launch_w16_lora(const W16LoraArgs& p, bool nv, bool out_bf16, hipStream_t stream) {
-  const int bs = lora_base_slices(p.M, p.N, p.K);
-  int ls = lora_shrink_slices(p.M, p.K);
-  if (p.M > 64 && !shrink_wide(p.M, p.S)) ls = 1;  // short segments: every slice is another pass over their adapters
+  const int bs = lora_base_slices(p.M, p.N, p.K, p.rank);
+  int ls = lora_shrink_slices(p.M, p.N, p.K, p.rank);
+  if (bs == 0 && !shrink_wide(p.M, p.S)) ls = 1;  // short segments: every slice is another pass over their adapters
   float* const base = p.workspace;
   float* const low = base + (int64_t)bs * p.M * p.N;
-  uint16_t* const low_hi = reinterpret_cast<uint16_t*>(low);  // M > 64: two bf16 terms in fp32's place
+  uint16_t* const low_hi = reinterpret_cast<uint16_t*>(low);  // not sliced: two bf16 terms in fp32's place
   uint16_t* const low_lo = low_hi + (int64_t)ls * p.M * p.rank;
   const int64_t blocks = cdiv(p.M, 16), per_block = cdiv(p.S, blocks);
   const int z = (int)(per_block < 1 ? 1 : per_block < 16 ? per_block : 16);
   // what fits the compute units beside the projection's tiles
-  if (p.M <= 64 && ls > 512 / (blocks * z)) ls = (int)(512 / (blocks * z) > 1 ? 512 / (blocks * z) : 1);
+  if (bs > 0 && ls > 512 / (blocks * z)) ls = (int)(512 / (blocks * z) > 1 ? 512 / (blocks * z) : 1);
   const ShrinkArgs s{p.a, p.lora_a, p.scaling, p.seg_off, p.seg_adapter, low, low_hi, low_lo, p.M, p.K, p.rank, p.L, p.S,
                      z, ls};
   W16TileArgs a{};
@@ -319,7 +330,7 @@ int launch_w16_lora(const W16LoraArgs& p, bool nv, bool out_bf16, hipStream_t st
   a.seg_off = p.seg_off;
   a.seg_adapter = p.seg_adapter;
   a.lora_b = p.lora_b;
-  if (p.M > 64) {
+  if (bs == 0) {
     if (p.S > 0) {
       if (p.rank <= 16) launch_shrink<1>(s, stream);
       else if (p.rank <= 32) launch_shrink<2>(s, stream);

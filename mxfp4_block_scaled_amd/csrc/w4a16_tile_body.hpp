@@ -48,7 +48,7 @@ __device__ __forceinline__ v16f mfma32x32x16(v8bf a, v8bf b, v16f c) {
 }
 
 // One workgroup's tile: BM x BN by NW waves, BM / 64 of them over rows, the others over
-// columns; x, j: its XCD and item. kSlices (at most BM rows, j the n-tile): only the K slice `slice` of a.kslices, whose sums go
+// columns; x, j: its XCD and item. kSlices (one matrix, j = unit x ntiles + n-tile): only the K slice `slice` of a.kslices, whose sums go
 // to slice `slice` of out, [kslices][R][N] fp32.
 template <int BM, int BN, int NW, int NA, bool kNV, bool kSwiglu, bool kOutBF16, bool kLora, bool kSlices>
 __device__ __forceinline__ void w16_tile(const W16TileArgs& a, W16Ring<BM, BN, NA>& ring, int x, int j, int slice) {
@@ -65,10 +65,10 @@ __device__ __forceinline__ void w16_tile(const W16TileArgs& a, W16Ring<BM, BN, N
 
   int e = 0, n_tile, m;
   int64_t row0;
-  if constexpr (kSlices) {  // at most BM rows: item j is n-tile j
-    n_tile = j;
-    row0 = 0;
-    m = (int)a.R;
+  if constexpr (kSlices) {  // item j: the n-tiles of a unit of rows after each other
+    n_tile = j % a.ntiles;
+    row0 = (int64_t)(j / a.ntiles) * BM;
+    m = (int)min((int64_t)BM, a.R - row0);
   } else {
     if (a.offsets) {
       if (!w16_item<BM>(a.offsets, a.E, a.R, a.min_rows, a.max_rows, a.ntiles, x, j, e, n_tile, row0, m)) return;
