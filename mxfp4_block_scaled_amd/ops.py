@@ -124,26 +124,32 @@ def _need(t, name, dtypes, shape):
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda i: torch.cuda.current_stream(i).cuda_stream)
 
 
-def _is(t, name, dtype, shape, dev):
-    """_dev and _need in one: t is on `dev`, contiguous, of `dtype` (or one of a tuple) and `shape`."""
-    if t.dtype != dtype or t.shape != shape or t.device != dev or not t.is_contiguous():
+def _is(t, name, dtype, shape, i):
+    """_dev and _need in one: t is on GPU i, contiguous, of `dtype` (or one of a tuple) and `shape`."""
+    if t.dtype != dtype or t.shape != shape or t.get_device() != i or not t.is_contiguous():
         _dev(t)
         _need(t, name, dtype, shape)
-        if t.device != dev:
-            raise RuntimeError(f"{name} is on {t.device}, expected {dev}")
+        if t.get_device() != i:
+            raise RuntimeError(f"{name} is on {t.device}, expected GPU {i}")
 
 
-def _call(name, dev, *args):
-    """The C function `name` with the tensors' GPU current and its current stream as the last argument."""
+def _call(name, i, *args):
+    """The C function `name` with the tensors' GPU i current and its current stream as the last argument."""
     fn = getattr(_lib or load(), name)
-    i = dev.index
-    if torch.cuda.current_device() == i:
+    if torch._C._cuda_getDevice() == i:
         rc = fn(*args, _raw_stream(i))
     else:
-        with torch.cuda.device(dev):
+        with torch.cuda.device(i):
             rc = fn(*args, _raw_stream(i))
     if rc:
         _check(rc, name)
+
+
+def _new(like, dtype, shape):
+    """An uninitialised tensor beside `like`; of its own dtype and shape the quicker way."""
+    if like.dtype == dtype:
+        return torch.empty_like(like) if like.shape == shape else like.new_empty(shape)
+    return torch.empty(shape, dtype=dtype, device=like.device)
 
 
 def _at(t):
@@ -441,26 +447,27 @@ def moe_grouped_gemm_w4a16(a, expert_offsets, w, w_scale, fmt="mxfp4", sorted_pa
     moe_route_permute) a [R/topk][K] and row r reads a[sorted_pair[r] // topk]. swiglu: the first N/2 weight rows
     are gate rows and the result is silu(gate) * up. Returns y [R][N] or [R][N/2]; with `out` given, rows outside
     every expert keep what it holds (in a new tensor they are uninitialised)."""
-    dev = _dev(a)
+    _dev(a)
+    i = a.get_device()
     if a.dim() != 2 or w.dim() != 3:
         raise RuntimeError("a must be [rows][K] and w [E][N][K/2]")
     rows, K = a.shape
     E, N, _ = w.shape
     f = _one_of(fmt, WEIGHT_FMTS, "fmt")
     R = rows * topk if sorted_pair is not None else rows
-    _is(a, "a", torch.bfloat16, (rows, K), dev)
-    _is(expert_offsets, "expert_offsets", torch.int32, (E + 1,), dev)
-    _is(w, "w", torch.uint8, (E, N, K // 2), dev)
-    _is(w_scale, "w_scale", torch.uint8, (E, N, K // (16 if f else 32)), dev)
+    _is(a, "a", torch.bfloat16, (rows, K), i)
+    _is(expert_offsets, "expert_offsets", torch.int32, (E + 1,), i)
+    _is(w, "w", torch.uint8, (E, N, K // 2), i)
+    _is(w_scale, "w_scale", torch.uint8, (E, N, K // (16 if f else 32)), i)
     if sorted_pair is not None:
-        _is(sorted_pair, "sorted_pair", torch.int32, (R,), dev)
+        _is(sorted_pair, "sorted_pair", torch.int32, (R,), i)
     shape = (R, N // 2 if swiglu else N)
     if out is None:
         _one_of(out_dtype, DTYPES, "out_dtype")
-        out = torch.empty(shape, dtype=out_dtype, device=dev)
+        out = _new(a, out_dtype, shape)
     else:
-        _is(out, "out", (torch.float32, torch.bfloat16), shape, dev)
-    _call("moe_grouped_gemm_w4a16", dev, a.data_ptr(), rows, R, _at(sorted_pair), topk, expert_offsets.data_ptr(), E, N,
+        _is(out, "out", (torch.float32, torch.bfloat16), shape, i)
+    _call("moe_grouped_gemm_w4a16", i, a.data_ptr(), rows, R, _at(sorted_pair), topk, expert_offsets.data_ptr(), E, N,
           K, f, w.data_ptr(), w_scale.data_ptr(), int(swiglu), out.data_ptr(), DTYPES[out.dtype])
     return out
 
@@ -472,7 +479,8 @@ def fp4_gemm_w4a16_lora(a, w, w_scale, seg_offsets, seg_adapter, lora_a, lora_b,
     scaling[l] * (a lora_a[l]^T) lora_b[l]^T of its adapter l = seg_adapter[s]; a negative l, and rows in no
     segment, get the projection alone. seg_offsets [S+1], seg_adapter [S] int32; lora_a [L][rank][K], lora_b
     [L][N][rank] bf16; scaling [L] fp32. Returns c [M][N] in out_dtype (fp32 or bf16)."""
-    dev = _dev(a)
+    _dev(a)
+    i = a.get_device()
     if a.dim() != 2 or w.dim() != 2 or lora_a.dim() != 3 or seg_adapter.dim() != 1:
         raise RuntimeError("a must be [M][K], w [N][K/2], lora_a [L][rank][K] and seg_adapter [S]")
     M, K = a.shape
@@ -480,27 +488,27 @@ def fp4_gemm_w4a16_lora(a, w, w_scale, seg_offsets, seg_adapter, lora_a, lora_b,
     L, rank, _ = lora_a.shape
     S = seg_adapter.shape[0]
     f = _one_of(fmt, WEIGHT_FMTS, "fmt")
-    _is(a, "a", torch.bfloat16, (M, K), dev)
-    _is(w, "w", torch.uint8, (N, K // 2), dev)
-    _is(w_scale, "w_scale", torch.uint8, (N, K // (16 if f else 32)), dev)
-    _is(seg_offsets, "seg_offsets", torch.int32, (S + 1,), dev)
-    _is(seg_adapter, "seg_adapter", torch.int32, (S,), dev)
-    _is(lora_a, "lora_a", torch.bfloat16, (L, rank, K), dev)
-    _is(lora_b, "lora_b", torch.bfloat16, (L, N, rank), dev)
-    _is(scaling, "scaling", torch.float32, (L,), dev)
+    _is(a, "a", torch.bfloat16, (M, K), i)
+    _is(w, "w", torch.uint8, (N, K // 2), i)
+    _is(w_scale, "w_scale", torch.uint8, (N, K // (16 if f else 32)), i)
+    _is(seg_offsets, "seg_offsets", torch.int32, (S + 1,), i)
+    _is(seg_adapter, "seg_adapter", torch.int32, (S,), i)
+    _is(lora_a, "lora_a", torch.bfloat16, (L, rank, K), i)
+    _is(lora_b, "lora_b", torch.bfloat16, (L, N, rank), i)
+    _is(scaling, "scaling", torch.float32, (L,), i)
     if out is None:
         _one_of(out_dtype, DTYPES, "out_dtype")
-        out = torch.empty((M, N), dtype=out_dtype, device=dev)
+        out = _new(a, out_dtype, (M, N))
     else:
-        _is(out, "out", (torch.float32, torch.bfloat16), (M, N), dev)
+        _is(out, "out", (torch.float32, torch.bfloat16), (M, N), i)
     need = load().fp4_w4a16_lora_workspace_bytes(M, N, K, rank)
     if workspace is None:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
-    elif _dev(workspace) != dev:
-        raise RuntimeError(f"workspace is on {workspace.device}, expected {dev}")
+        workspace = w.new_empty(max(need, 1))
+    elif _dev(workspace) != a.device:
+        raise RuntimeError(f"workspace is on {workspace.device}, expected {a.device}")
     else:
         _need(workspace, "workspace", torch.uint8, ((">=", need),))
-    _call("fp4_gemm_w4a16_lora", dev, a.data_ptr(), M, N, K, f, w.data_ptr(), w_scale.data_ptr(), _at(seg_offsets),
+    _call("fp4_gemm_w4a16_lora", i, a.data_ptr(), M, N, K, f, w.data_ptr(), w_scale.data_ptr(), _at(seg_offsets),
           _at(seg_adapter), S, _at(lora_a), _at(lora_b), _at(scaling), L, rank, out.data_ptr(), DTYPES[out.dtype],
           workspace.data_ptr(), workspace.numel())
     return out
@@ -517,7 +525,8 @@ def moe_block_norm(y, x=None, post_weight=None, gate=None, residual_scale=1.0, p
     act_fmt "e4m3" / "e2m1" also quantises n (from fp32) as mxfp4_quantize_act. `r` may be given as the output
     (x itself: updated in place). Returns a dict of r (x's dtype, without x r_dtype or y's), n (n_dtype), q and
     q_scale; what is not wanted is None."""
-    dev = _dev(y)
+    _dev(y)
+    i = y.get_device()
     if y.dim() != 2:
         raise RuntimeError("y must be 2-d [rows][H]")
     y_rows, H = y.shape
@@ -530,11 +539,11 @@ def moe_block_norm(y, x=None, post_weight=None, gate=None, residual_scale=1.0, p
         if expert_gates.dim() != 2 or expert_gates.shape[1] < 1:
             raise RuntimeError("expert_gates must be [T][topk]")
         T, topk = expert_gates.shape
-        _is(expert_gates, "expert_gates", torch.float32, (T, topk), dev)
-        _is(pair_row, "pair_row", torch.int32, (T * topk,), dev)
+        _is(expert_gates, "expert_gates", torch.float32, (T, topk), i)
+        _is(pair_row, "pair_row", torch.int32, (T * topk,), i)
     if x is not None:
         r_dtype = x.dtype
-        _is(x, "x", r_dtype, (T, H), dev)
+        _is(x, "x", r_dtype, (T, H), i)
     elif r_dtype is None:
         r_dtype = y.dtype if r is None else r.dtype
     x_dtype = _one_of(r_dtype, DTYPES, "the residual's dtype")
@@ -543,7 +552,7 @@ def moe_block_norm(y, x=None, post_weight=None, gate=None, residual_scale=1.0, p
         if t is not None:
             w_dtype = t.dtype
             _one_of(w_dtype, DTYPES, name)
-            _is(t, name, w_dtype, (H,), dev)
+            _is(t, name, w_dtype, (H,), i)
     if post_weight is not None and post_weight.dtype != w_dtype:
         raise RuntimeError(f"post_weight is {post_weight.dtype} and pre_weight {w_dtype}, expected one dtype")
     mode, g_dtype = 0, torch.float32
@@ -551,19 +560,19 @@ def moe_block_norm(y, x=None, post_weight=None, gate=None, residual_scale=1.0, p
         g_dtype = gate.dtype
         mode = 1 if gate.dim() == 1 else 2 if gate.dim() == 2 and gate.shape[1] == 1 else 3
         _one_of(g_dtype, DTYPES, "gate")
-        _is(gate, "gate", g_dtype, {1: (H,), 2: (T, 1), 3: (T, H)}[mode], dev)
+        _is(gate, "gate", g_dtype, {1: (H,), 2: (T, 1), 3: (T, H)}[mode], i)
     fmt = None if act_fmt is None else _one_of(act_fmt, FMTS, "act_fmt")
     if r is not None:
-        _is(r, "r", r_dtype, (T, H), dev)
+        _is(r, "r", r_dtype, (T, H), i)
     elif want_r:
-        r = torch.empty((T, H), dtype=r_dtype, device=dev)
+        r = _new(y if x is None else x, r_dtype, (T, H))
     n_code = _one_of(n_dtype, DTYPES, "n_dtype")
-    n = torch.empty((T, H), dtype=n_dtype, device=dev) if want_n else None
+    n = _new(y if x is None else x, n_dtype, (T, H)) if want_n else None
     q = qs = None
     if fmt is not None:
-        q = torch.empty((T, H // 2 if fmt == MXF_E2M1 else H), dtype=torch.uint8, device=dev)
-        qs = torch.empty((T, H // 32), dtype=torch.uint8, device=dev)
-    _call("moe_block_norm", dev, y.data_ptr(), DTYPES[y.dtype], y_rows, _at(expert_gates), _at(pair_row), topk, T, H,
+        q = torch.empty((T, H // 2 if fmt == MXF_E2M1 else H), dtype=torch.uint8, device=y.device)
+        qs = q.new_empty((T, H // 32))
+    _call("moe_block_norm", i, y.data_ptr(), DTYPES[y.dtype], y_rows, _at(expert_gates), _at(pair_row), topk, T, H,
           _at(x), x_dtype, residual_scale, _at(post_weight), _at(pre_weight), DTYPES[w_dtype], eps, _at(gate),
           DTYPES[g_dtype], mode, _at(r), _at(n), n_code, fmt or 0, _at(q), _at(qs))
     return dict(r=r, n=n, q=q, q_scale=qs)

@@ -214,7 +214,7 @@ def test_block_norm_writes_stay_inside(T, H_, topk, fmt):
     qs = Guarded((T, H_ // 32), torch.uint8, 90) if fmt else None
     t = {k: bn.cu(v) for k, v in i.items()}
     at = ops._at
-    ops._call("moe_block_norm", r.t.device, at(t["y"]), 1, t["y"].shape[0], at(t["gates"]), at(t["pair"]), topk, T, H_,
+    ops._call("moe_block_norm", 0, at(t["y"]), 1, t["y"].shape[0], at(t["gates"]), at(t["pair"]), topk, T, H_,
               at(t["x"]), 1, 1.0, at(t["post"]), at(t["pre"]), 0, 1e-6, at(t["gate"]), 1, 3, at(r.t), at(n.t), 0,
               ops.FMTS[fmt] if fmt else 0, at(q.t) if q else None, at(qs.t) if qs else None)
     torch.cuda.synchronize()
