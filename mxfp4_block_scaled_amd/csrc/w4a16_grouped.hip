@@ -192,37 +192,48 @@ void launch_stream(W16TileArgs a, bool nv, bool swiglu, bool out_bf16, int64_t u
   else launch_stream_t<false, false>(a, out_bf16, grid, stream);
 }
 
-// Small calls run in the streaming kernel alone (one launch), experts of more than 16 rows in
-// units of 16 that read the weights again from the cache: calls of at most kStreamRows rows,
-// and those of at most kStreamItems workgroups. Its time grows with items x K (5 us a million),
-// that of the tiled launches with the longest chain, 0.9 us for each 64 k. Measured (streamed /
-// tiled, us): 8 experts x 2048 x 2048, 1024 rows (2304 items) 26 / 33, 2048 rows (4352) 48 / 35;
-// 4 x 4096 x 7168, 512 rows (2304) 86 / 93, 1024 rows (4352) 154 / 95; 64 x 512 x 512, 2048 rows
-// (1536) 10.9 / 11.2.
-constexpr int64_t kStreamRows = 128, kStreamItems = 2560;
-
 // units that experts of lo < rows <= hi can make of R rows in all
 int64_t most_units(int64_t R, int E, int64_t lo, int bm) {
   const int64_t experts = R / (lo + 1) < E ? R / (lo + 1) : E;
   return bm == 0 ? experts : experts + R / bm;
 }
 
+// Which kernels a call runs; what the experts hold is on the device, so by bounds on it.
+// Measured in us (8 experts: rows in all; streamed | 64 x 128 | 64 x 256 | 128 x 256 tiles):
+//   2048 x 2048, 512 rows   18 | 20 | 24 | 33     4 experts 4096 x 7168, 512 rows   90 | 59 | 65 | 96
+//                1024       28 | 23 | 25 | 34                            2048      351 | 144 | 155 | 154
+//                6000      139 | 60 | 56 | 57                            6000      977 | 411 | 354 | 308
+// The streaming kernel's time grows with workgroups x K (5 us a million) and needs one launch;
+// a tiled launch lasts at least its K chain (0.36 us for 64 k of 64 x 128 tiles).
+bool streams_all(int64_t R, int64_t workgroups, int64_t K) { return R <= 128 || workgroups <= 1100 + 600000 / K; }
+
 }  // namespace
 
 int launch_w16_grouped(W16TileArgs a, bool nv, bool swiglu, bool out_bf16, hipStream_t stream) {
   constexpr int kAll = 0x7FFFFFFF;
   const int64_t R = a.R;
-  const bool small = R <= kStreamRows || most_units(R, a.E, 0, 16) * cdiv(a.N, 64) <= kStreamItems;
+  const bool all = streams_all(R, most_units(R, a.E, 0, 16) * cdiv(a.N, 64), a.K);
   a.min_rows = 0;
-  a.max_rows = small ? kAll : 16;
-  launch_stream(a, nv, swiglu, out_bf16, most_units(R, a.E, 0, small ? 16 : 0), stream);
-  if (small) return hipGetLastError() == hipSuccess ? 0 : -1;
-  a.min_rows = 16;
-  a.max_rows = 64;
-  launch_w16_tile_grouped(a, nv, swiglu, out_bf16, 64, most_units(R, a.E, 16, 0), stream);
-  a.min_rows = 64;
-  a.max_rows = kAll;
-  launch_w16_tile_grouped(a, nv, swiglu, out_bf16, 128, most_units(R, a.E, 64, 128), stream);
+  a.max_rows = all ? kAll : 16;  // units of 16 rows read an expert's weights again from the cache
+  launch_stream(a, nv, swiglu, out_bf16, most_units(R, a.E, 0, all ? 16 : 0), stream);
+  if (!all) {
+    const int64_t nt = cdiv(a.N, 256), w128 = most_units(R, a.E, 16, 128) * nt;
+    a.min_rows = 16;
+    if (w128 < 1024) {  // few tiles: one tiled launch, of the shape that keeps the chip busy
+      const W16Shape shape = R >= 96 * (int64_t)a.E && w128 >= 384              ? W16Shape::k128x256
+                             : !swiglu && most_units(R, a.E, 16, 64) * nt < 600 ? W16Shape::k64x128
+                                                                                : W16Shape::k64x256;
+      a.max_rows = kAll;
+      launch_w16_tile_grouped(a, nv, swiglu, out_bf16, shape, most_units(R, a.E, 16, shape == W16Shape::k128x256 ? 128 : 64),
+                              stream);
+    } else {  // a large call, perhaps a skewed one: by the expert's own rows
+      a.max_rows = 64;
+      launch_w16_tile_grouped(a, nv, swiglu, out_bf16, W16Shape::k64x256, most_units(R, a.E, 16, 0), stream);
+      a.min_rows = 64;
+      a.max_rows = kAll;
+      launch_w16_tile_grouped(a, nv, swiglu, out_bf16, W16Shape::k128x256, most_units(R, a.E, 64, 128), stream);
+    }
+  }
   return hipGetLastError() == hipSuccess ? 0 : -1;
 }
 

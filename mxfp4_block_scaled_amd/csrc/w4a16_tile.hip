@@ -27,14 +27,13 @@ void launch_shape(W16TileArgs a, bool nv, bool out_bf16, int64_t units, hipStrea
 
 }  // namespace
 
-void launch_w16_tile_grouped(const W16TileArgs& a, bool nv, bool swiglu, bool out_bf16, int bm, int64_t units,
+void launch_w16_tile_grouped(const W16TileArgs& a, bool nv, bool swiglu, bool out_bf16, W16Shape shape, int64_t units,
                              hipStream_t stream) {
-  if (bm == 256) {
-    if (swiglu) launch_shape<256, 256, 8, 3, true, false>(a, nv, out_bf16, units, stream);
-    else launch_shape<256, 256, 8, 3, false, false>(a, nv, out_bf16, units, stream);
-  } else if (bm == 128) {
+  if (shape == W16Shape::k128x256) {
     if (swiglu) launch_shape<128, 256, 4, 2, true, false>(a, nv, out_bf16, units, stream);
     else launch_shape<128, 256, 4, 2, false, false>(a, nv, out_bf16, units, stream);
+  } else if (shape == W16Shape::k64x128 && !swiglu) {
+    launch_shape<64, 128, 4, 3, false, false>(a, nv, out_bf16, units, stream);
   } else {
     if (swiglu) launch_shape<64, 256, 4, 3, true, false>(a, nv, out_bf16, units, stream);
     else launch_shape<64, 256, 4, 3, false, false>(a, nv, out_bf16, units, stream);

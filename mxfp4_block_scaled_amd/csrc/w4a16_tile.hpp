@@ -159,7 +159,9 @@ __device__ __forceinline__ int first_segment(const int32_t* __restrict__ seg_off
   return __builtin_amdgcn_readfirstlane(lo);
 }
 
-void launch_w16_tile_grouped(const W16TileArgs& a, bool nv, bool swiglu, bool out_bf16, int bm, int64_t units,
+// tiles of rows x weight rows (64 x 128 without SwiGLU only)
+enum class W16Shape { k64x128, k64x256, k128x256 };
+void launch_w16_tile_grouped(const W16TileArgs& a, bool nv, bool swiglu, bool out_bf16, W16Shape shape, int64_t units,
                              hipStream_t stream);
 void launch_w16_tile_lora(const W16TileArgs& a, bool nv, bool out_bf16, hipStream_t stream);
 

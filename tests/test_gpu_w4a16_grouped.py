@@ -82,6 +82,10 @@ CASES = [
     ([130, 63, 500, 40], 0, 0, 4128, 384, "nvfp4", True, torch.bfloat16),
     ([90, 33, 128, 5, 700], 1, 0, 3616, 640, "mxfp4", True, torch.float32),
     ([256, 129, 18, 2, 0, 260], 0, 7, 4368, 1152, "nvfp4", False, torch.bfloat16),
+    # large enough for a tiled launch per class of experts (1024 and more 128 x 256 tiles)
+    ([500, 300, 200, 130, 100, 90, 65, 64, 40, 33, 20, 17, 16, 10, 5, 3, 1, 0, 0, 2, 1, 1, 1, 1], 2, 1, 7440, 128,
+     "mxfp4", False, torch.bfloat16),
+    ([1, 300, 200, 0, 100, 90, 65, 64, 40, 33, 700, 17, 16, 10, 5], 0, 0, 11296, 128, "nvfp4", True, torch.float32),
     ([3] * 260 + [40, 70], 0, 0, 1040, 256, "mxfp4", False, torch.float32),  # more experts than a lane batch holds
 ]
 
