@@ -41,10 +41,12 @@ void launch_w16_tile_grouped(const W16TileArgs& a, bool nv, bool swiglu, bool ou
 }
 
 void launch_w16_tile_lora(const W16TileArgs& a, bool nv, bool out_bf16, hipStream_t stream) {
-  // 256 x 256 tiles once they fill the chip's 256 compute units; below that the small
-  // tile's four times as many workgroups finish sooner
-  if (cdiv(a.R, 256) * cdiv(a.N, 256) >= 256)
-    launch_shape<256, 256, 8, 3, false, true>(a, nv, out_bf16, cdiv(a.R, 256), stream);
+  // 128 x 256 tiles once there is about one for each of the 256 compute units (two fit one);
+  // below that the small tile's four times as many workgroups finish sooner. Measured, us (64 x
+  // 128 | 128 x 256): 4096 x 7168, 1500 rows 123 | 136, 2048 rows (256 tiles) 179 | 147, 8192 rows
+  // 571 | 435; 2048 x 4096, 3000 rows (192 tiles) 75 | 83, 4096 rows 103 | 85. 256 x 256 tiles, one a
+  // compute unit: 227 instead of 234 at 4096 x 4096 x 7168, where they fill the chip once, else slower.
+  if (cdiv(a.R, 128) * cdiv(a.N, 256) >= 240) launch_shape<128, 256, 4, 2, false, true>(a, nv, out_bf16, cdiv(a.R, 128), stream);
   else launch_shape<64, 128, 4, 3, false, true>(a, nv, out_bf16, cdiv(a.R, 64), stream);
 }
 

@@ -63,7 +63,11 @@ CASES = [
     ([1] * 70, 1, 3, 256, 512, 40, 9, "mxfp4", torch.bfloat16),
     ([100, 0, 0, 31, 200, 1, 7], 0, 20, 528, 1536, 72, 5, "nvfp4", torch.float32),
     ([5, 700, 60], 0, 0, 1040, 512, 64, 2, "mxfp4", torch.bfloat16),
-    ([900, 3200], 0, 4, 4352, 512, 16, 2, "mxfp4", torch.float32),  # large tiles
+    ([1] * 300, 5, 0, 272, 1024, 16, 7, "nvfp4", torch.float32),  # single rows, sliced
+    ([100, 0, 1900, 3, 97], 0, 0, 1040, 512, 24, 3, "mxfp4", torch.bfloat16),  # 64 x 128 tiles, low in K slices
+    ([7] * 300, 1, 2, 1040, 1536, 8, 5, "mxfp4", torch.float32),  # the same with short segments
+    ([150, 50], 0, 0, 4112, 2048, 128, 2, "nvfp4", torch.float32),  # a wide adapter: few tiles, not sliced
+    ([900, 3200], 0, 4, 4352, 512, 16, 2, "mxfp4", torch.float32),  # 128 x 256 tiles
     ([2049, 1, 2046], 0, 0, 4096, 512, 120, 3, "nvfp4", torch.bfloat16),
 ]
 

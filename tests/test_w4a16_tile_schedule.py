@@ -5,7 +5,7 @@ hand-over of the three slots."""
 
 import pytest
 
-SHAPES = [(256, 256, 8, False), (128, 256, 4, False), (128, 256, 4, True), (64, 256, 4, False), (64, 256, 4, True),
+SHAPES = [(128, 256, 4, False), (128, 256, 4, True), (64, 256, 4, False), (64, 256, 4, True),
           (64, 128, 4, False)]
 
 
