@@ -349,8 +349,9 @@ typedef enum { MXF_W_MXFP4 = 0, MXF_W_NVFP4 = 1 } mxf_weight;
  *                and y [R][N/2] = silu(gate) * up, in fp32 before the one rounding to y_dtype
  *   y            fp32 or bf16 (y_dtype; round to nearest even). Rows of y outside
  *                [expert_offsets[0], expert_offsets[E]) are left as they were.
- * Deterministic: no atomics, a fixed summation order; a row's result does not depend on
- * the other experts' rows. Requires K % 128 == 0, N % 16 == 0 (swiglu: N % 32 == 0),
+ * Deterministic: no atomics, and the same call sums in the same order (which kernel an expert
+ * runs in, and with it the order, follows from R, E, N, K and its own rows); a row's result does
+ * not depend on what other rows hold. Requires K % 128 == 0, N % 16 == 0 (swiglu: N % 32 == 0),
  * E <= 1024, and the bytes of one expert's codes below 4 GiB with a margin of 257 rows;
  * with sorted_pair also a below 4 GiB. R == 0 is a no-op.
  * Errors: NULL, SHAPE, ALIGN, FORMAT, UNSUPPORTED.
@@ -374,7 +375,8 @@ int moe_grouped_gemm_w4a16(const uint16_t* a, int64_t a_rows, int64_t R, const i
  *                product is kept in fp32 between its two factors
  *   workspace    fp4_w4a16_lora_workspace_bytes() bytes, 16-byte aligned, contents
  *                irrelevant; calls that may overlap need one each
- * Requires K % 512 == 0, N % 16 == 0, rank % 8 == 0, 8 <= rank <= 128. S == 0 (with L == 0
+ * Requires K % 512 == 0, N % 16 == 0, rank % 8 == 0, 8 <= rank <= 128, and the codes and one
+ * adapter's lora_b below 4 GiB (with a margin of 257 rows). S == 0 (with L == 0
  * or not): the projection alone. M == 0 is a no-op.
  * Errors: NULL, SHAPE, ALIGN, FORMAT, UNSUPPORTED, WORKSPACE.
  */

@@ -59,7 +59,8 @@ def test_lora_errors():
         (dict(fmt=-1), FORMAT), (dict(cd=3), FORMAT), (dict(M=-1), SHAPE), (dict(N=40), SHAPE), (dict(K=4096 + 128), SHAPE),
         (dict(S=-1), SHAPE), (dict(L=-1), SHAPE), (dict(rank=0), SHAPE), (dict(rank=12), SHAPE), (dict(rank=136), SHAPE),
         (dict(K=2 ** 22), UNSUPPORTED), (dict(N=2 ** 17, K=2 ** 16), UNSUPPORTED),
-        (dict(M=2 ** 31 - 1, N=2 ** 13), UNSUPPORTED), (dict(a=None), NULL), (dict(w=None), NULL), (dict(ws=None), NULL),
+        (dict(M=2 ** 31 - 1, N=2 ** 13), UNSUPPORTED), (dict(N=2 ** 24, K=512, rank=128), UNSUPPORTED),
+        (dict(a=None), NULL), (dict(w=None), NULL), (dict(ws=None), NULL),
         (dict(c=None), NULL), (dict(so=None), NULL), (dict(sa=None), NULL), (dict(la=None), NULL), (dict(lb=None), NULL),
         (dict(sc=None), NULL), (dict(a=U), ALIGN), (dict(so=U), ALIGN), (dict(sa=U), ALIGN), (dict(la=U), ALIGN),
         (dict(lb=U), ALIGN), (dict(sc=U), ALIGN), (dict(c=U), ALIGN), (dict(wk=U), ALIGN),

@@ -158,6 +158,43 @@ def test_in_place_and_bad_rows_stay_apart():
     assert torch.equal(bad["n"][keep], want["n"][keep]) and torch.isnan(bad["n"][3]).all()
 
 
+@pytest.mark.parametrize("topk,xd,fmt", [(0, F32, None), (6, BF, "e4m3"), (2, BF, "e2m1")])
+def test_large_batches_are_their_parts(topk, xd, fmt):
+    """A batch that passes the caches by gives each of its rows the bits that it has in a smaller one."""
+    T, H, part = 4224, 8064, 528
+    i = inputs(T, H, topk, True, "full", xd, BF, BF, 21)
+    t = {k: cu(v) for k, v in i.items()}
+    want_fmt = dict(act_fmt=fmt, eps=EPS, residual_scale=0.75)
+    whole = ops.moe_block_norm(t["y"], x=t["x"], post_weight=t["post"], gate=t["gate"], pre_weight=t["pre"],
+                               expert_gates=t["gates"], pair_row=t["pair"], **want_fmt)
+    for at in range(0, T, part):
+        rows = slice(at, at + part)
+        got = ops.moe_block_norm(t["y"] if topk else t["y"][rows], x=t["x"][rows], post_weight=t["post"],
+                                 gate=t["gate"][rows], pre_weight=t["pre"],
+                                 expert_gates=t["gates"][rows].contiguous() if topk else None,
+                                 pair_row=t["pair"][at * topk:(at + part) * topk] if topk else None, **want_fmt)
+        for k, v in got.items():
+            assert v is None or torch.equal(v, whole[k][rows]), k
+    few = slice(100, 140)
+    pairs = i["pair"][100 * topk:140 * topk] if topk else None
+    r, dr, n, dn = reference(i["y"] if topk else i["y"][few], i["x"][few], i["post"], i["gate"][few], 0.75, i["pre"],
+                             i["gates"][few] if topk else None, pairs)
+    close(whole["r"][few], r, dr, "r")
+    close(whole["n"][few], n, dn, "n")
+
+
+def test_without_weights():
+    """No pre-norm weight is a weight of ones; without x and post-norm r is the gated block output."""
+    i = inputs(7, 264, 0, False, "channel", None, BF, BF, 22)
+    got = ops.moe_block_norm(cu(i["y"]), gate=cu(i["gate"]), eps=EPS, r_dtype=F32, n_dtype=F32)
+    ones = ops.moe_block_norm(cu(i["y"]), gate=cu(i["gate"]), eps=EPS, r_dtype=F32, n_dtype=F32,
+                              pre_weight=torch.ones(264, device="cuda"))
+    r, dr, n, dn = reference(i["y"], None, None, i["gate"], 1.0, None, None, None)
+    close(got["r"], r, dr, "r")
+    close(got["n"], n, dn, "n")
+    assert torch.equal(got["n"], ones["n"])
+
+
 def test_no_rows():
     got = ops.moe_block_norm(torch.empty(0, 64, dtype=BF, device="cuda"))
     assert got["r"].shape == (0, 64) and got["n"].shape == (0, 64)
