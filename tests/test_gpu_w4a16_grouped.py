@@ -113,6 +113,37 @@ def test_against_64_bits(case, gather):
     assert (y.cpu()[outside] == 7.0).all(), "rows outside every expert were written"
 
 
+@pytest.mark.parametrize("fmt,swiglu,N,dtype", [("mxfp4", False, 4240, torch.float32), ("nvfp4", True, 4256, torch.bfloat16)])
+@pytest.mark.parametrize("rows", ["few", "mixed"])
+def test_many_experts_of_a_short_k(fmt, swiglu, N, dtype, rows):
+    """128 experts of wide matrices with a short K, where a workgroup streams several runs of weight rows."""
+    E, K = 128, 256
+    g = np.random.default_rng(N)
+    counts = np.zeros(E, int)
+    if rows == "few":
+        counts[g.permutation(E)[:100]] = 1
+        counts[3], counts[77] = 9, 18
+    else:
+        counts = g.integers(0, 6, E)
+        counts[5], counts[90], counts[127] = 30, 80, 17
+    R = int(counts.sum())
+    offs = np.concatenate([[0], np.cumsum(counts)])
+    w = torch.from_numpy(g.integers(0, 256, (E, N, K // 2), dtype=np.uint8))
+    lo, hi = (0, 0x50) if fmt == "nvfp4" else (118, 131)
+    s = torch.from_numpy(g.integers(lo, hi, (E, N, K // (16 if fmt == "nvfp4" else 32)), dtype=np.uint8))
+    a = torch.randn(R, K).to(torch.bfloat16)
+    y = ops.moe_grouped_gemm_w4a16(a.cuda(), torch.from_numpy(offs.astype(np.int32)).cuda(), w.cuda(), s.cuda(), fmt,
+                                   swiglu=swiglu, out_dtype=dtype)
+    decode = oracle.dequant_nvfp4_weights if fmt == "nvfp4" else oracle.dequant_weights
+    for e in (0, 3, 5, 41, 77, 90, 127):
+        rows_e = slice(offs[e], offs[e + 1])
+        if counts[e]:
+            hat = torch.from_numpy(decode(w[e].numpy(), s[e].numpy()))[None].double()
+            x = a[rows_e]
+            want, d = reference(x, torch.arange(len(x)), [0, len(x)], hat, swiglu)
+            assert_close(y[rows_e], want, d, f"expert {e}")
+
+
 def test_one_row_is_its_own():
     """A row does not depend on what else its expert or the others hold: NaN and infinite rows beside it change
     nothing, and each row alone gives the bits that it gives among others of the same class."""
