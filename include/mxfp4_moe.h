@@ -368,6 +368,7 @@ int moe_grouped_gemm_w4a16(const uint16_t* a, int64_t a_rows, int64_t R, const i
  * A segment whose adapter is outside [0, L) (say -1), and rows in no segment, get the
  * projection alone.
  *   a            [M][K] bf16;  w, w_scale as for mxfp4_gemm_w4a16 / nvfp4_gemm_w4a16
+ * Infinities and NaN of an adapter reach the rows of its segments only.
  *   seg_offsets  [S+1] int32, ascending (a request's rows are consecutive); seg_adapter [S]
  *   lora_a       [L][rank][K] bf16;  lora_b [L][N][rank] bf16;  scaling [L] fp32. An adapter
  *                of a smaller rank is padded with zero rows of lora_a.

@@ -129,7 +129,7 @@ __device__ __forceinline__ void lora_shrink(const ShrinkArgs& p, ShrinkLds<MF, R
       if (kSplit) {
         p.low[((int64_t)slice * p.M + row) * p.rank + r] = t;
       } else {
-        const __bf16 h = (__bf16)t, d = (__bf16)(t - (float)h);
+        const __bf16 h = (__bf16)t, d = (__bf16)(isfinite((float)h) ? t - (float)h : 0.0f);  // an infinity stays one
         const int64_t at = ((int64_t)slice * p.M + row) * p.rank + r;
         p.low_hi[at] = __builtin_bit_cast(uint16_t, h);
         p.low_lo[at] = __builtin_bit_cast(uint16_t, d);

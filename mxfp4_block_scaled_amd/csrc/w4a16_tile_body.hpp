@@ -224,12 +224,16 @@ __device__ __forceinline__ void w16_tile(const W16TileArgs& a, W16Ring<BM, BN, N
       }
     });
 
+  lds_barrier();  // every wave is done with the ring
+  if (!active) return;
+  uint8_t* const stg = reinterpret_cast<uint8_t*>(&ring) + wave * 8192;
+
   // adapters: for each segment with rows here, acc += low . lora_b^T over the rank, low
   // (scaled, fp32) held as two bf16 terms (16 significant bits: the adapter's share keeps an
   // error of 2^-16 of itself). 64 segments' bounds and adapters are read at once, and the
   // operands of the next 16 ranks are loaded before the current ones are multiplied, so that
   // many short segments cost their loads and not their latency.
-  if (kLora && active) {
+  if (kLora) {
     const int64_t rlo = row0 + 64 * wm, rhi = min(rlo + 64, row0 + m);
     int s0 = first_segment(a.seg_off, a.S, rlo);
     int lo_l = 0, hi_l = 0, l_l = 0, k_next = a.rank;
@@ -265,6 +269,7 @@ __device__ __forceinline__ void w16_tile(const W16TileArgs& a, W16Ring<BM, BN, N
     };
     struct Ops {
       v4i h[2], lo[2], b[FN];
+      int first, end;  // the segment's rows
     };
     // per-lane byte offsets; the item adds scalars only (rows past N of lora_b read as zero)
     uint32_t loff[2], boff_l[FN];
@@ -279,6 +284,8 @@ __device__ __forceinline__ void w16_tile(const W16TileArgs& a, W16Ring<BM, BN, N
       const buf_rsrc rw = make_rsrc(a.lora_b + (int64_t)l * N * a.rank, nrank);
       const uint32_t k2 = 2 * (uint32_t)k_next;
       const bool kin = k_next + 8 * g < a.rank;  // the last 8 of a rank that is no multiple of 16
+      o.first = lo;
+      o.end = hi;
 #pragma unroll
       for (int fm = 0; fm < 2; ++fm) {
         const int t = 32 * fm + r32;
@@ -294,6 +301,18 @@ __device__ __forceinline__ void w16_tile(const W16TileArgs& a, W16Ring<BM, BN, N
         if (kin) o.b[f] = buf_load16(rw, boff_l[f], k2);
       }
     };
+    // an infinity or NaN of the adapter would reach the rows beside the segment (0 times it is NaN):
+    // those rows' sums wait in LDS meanwhile
+    auto spills = [&](const Ops& o) -> bool {
+      if (o.first <= 0 && o.end >= 64) return false;
+      uint32_t any = 0;  // exponents of all ones carry into the sign
+#pragma unroll
+      for (int f = 0; f < FN; ++f)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) any |= ((uint32_t)o.b[f][i] & 0x7FFF7FFFu) + 0x00800080u;
+      return __ballot((any & 0x80008000u) != 0) != 0;
+    };
+    float* const kept = reinterpret_cast<float*>(stg) + lane;
     constexpr int D = FN == 1 ? 4 : 2;  // operands in flight
     Ops o[D];
     bool have[D];
@@ -306,14 +325,32 @@ __device__ __forceinline__ void w16_tile(const W16TileArgs& a, W16Ring<BM, BN, N
 #pragma unroll
       for (int d = 0; d < D; ++d) {
         if (!have[d]) break;
+        const bool apart = __builtin_expect(spills(o[d]), 0);
 #pragma unroll
-        for (int f = 0; f < FN; ++f)
+        for (int f = 0; f < FN; ++f) {
+          if (apart) {
 #pragma unroll
-          for (int fm = 0; fm < 2; ++fm) {
-            const v8bf bw = __builtin_bit_cast(v8bf, o[d].b[f]);
-            acc[fm][f] = mfma32x32x16(bw, __builtin_bit_cast(v8bf, o[d].lo[fm]), acc[fm][f]);
-            acc[fm][f] = mfma32x32x16(bw, __builtin_bit_cast(v8bf, o[d].h[fm]), acc[fm][f]);
+            for (int i = 0; i < 32; ++i) kept[64 * i] = acc[i / 16][f][i % 16];
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
           }
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int fm = 0; fm < 2; ++fm)
+              acc[fm][f] = mfma32x32x16(__builtin_bit_cast(v8bf, o[d].b[f]),
+                                        __builtin_bit_cast(v8bf, h ? o[d].h[fm] : o[d].lo[fm]), acc[fm][f]);
+          if (apart) {
+#pragma unroll
+            for (int fm = 0; fm < 2; ++fm) {
+              const int t = 32 * fm + r32;
+              if (t < o[d].first || t >= o[d].end) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) acc[fm][f][i] = kept[64 * (16 * fm + i)];
+              }
+            }
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+          }
+        }
         have[d] = advance();
         if (have[d]) load(o[d]);
       }
@@ -322,13 +359,10 @@ __device__ __forceinline__ void w16_tile(const W16TileArgs& a, W16Ring<BM, BN, N
 
   // epilogue: 32 rows x CP columns at a time through the wave's 8 KB of the ring (runs of
   // 4 columns in, 16-byte pieces of whole row segments out)
-  lds_barrier();  // every wave is done with the ring
-  if (!active) return;
   constexpr int ES = kOutBF16 ? 2 : 4, OF = kSwiglu ? FN / 2 : FN;
   constexpr int PF = OF * 32 * ES > 256 ? 256 / (32 * ES) : OF;  // fragments per pass
   constexpr int RB = PF * 32 * ES, NCH = RB / 16;
   static_assert(OF % PF == 0, "passes");
-  uint8_t* const stg = reinterpret_cast<uint8_t*>(&ring) + wave * 8192;
   const int64_t ocols = kSwiglu ? half : N;
   uint8_t* const out = static_cast<uint8_t*>(a.out) + (kSlices ? (int64_t)slice * a.R * N * 4 : 0);
   const int64_t col0 = ((int64_t)n_tile * BN >> (kSwiglu ? 1 : 0)) + OF * 32 * wn;

@@ -128,6 +128,43 @@ def test_rows_and_adapters_stay_apart(M):
     assert torch.equal(got[keep], want[keep]) and torch.isnan(got[cut + 1]).all()
 
 
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("M,N,K,rank", [(9, 272, 512, 24), (200, 4112, 512, 128), (4100, 4352, 512, 16)])
+def test_an_adapter_that_is_not_finite_reaches_its_own_rows_only(M, N, K, rank, bad):
+    """One of the adapters in use holds a NaN or an infinity: the requests beside it keep their results bit for
+    bit, and its own rows show it (one row per workgroup pass, 64 x 128 tiles, 128 x 256 tiles)."""
+    L = 3
+    w, s, _ = weights(1, N, K, "mxfp4", 6)
+    la, lb, scaling = (t.cuda() for t in adapters(L, rank, N, K, 7))
+    a = bf16(2, M, K).cuda()
+    lo, hi = M // 2 - 3, M // 2 + 2  # inside one tile, with rows of others (and of none) before and behind
+    offs = torch.tensor([0, lo - 1, lo, hi, M - 1, M], dtype=torch.int32).cuda()
+    ad = torch.tensor([1, -1, 2, 0, 2], dtype=torch.int32).cuda()
+    want = ops.fp4_gemm_w4a16_lora(a, w[0], s[0], offs, ad, la, lb, scaling)
+    lb[2, 5, 3] = lb[2, N - 1, rank - 1] = bad
+    got = ops.fp4_gemm_w4a16_lora(a, w[0], s[0], offs, ad, la, lb, scaling)
+    own = torch.zeros(M, dtype=torch.bool, device="cuda")
+    own[lo:hi] = own[M - 1] = True
+    assert torch.equal(got[~own], want[~own])
+    cols = torch.zeros(N, dtype=torch.bool, device="cuda")
+    cols[5] = cols[N - 1] = True
+    assert not torch.isfinite(got[own][:, cols]).any() and torch.equal(got[own][:, ~cols], want[own][:, ~cols])
+
+
+@pytest.mark.parametrize("M,N,K,rank", [(9, 272, 512, 24), (200, 4112, 512, 128), (4100, 4352, 512, 16)])
+def test_an_infinite_first_product_stays_infinite(M, N, K, rank):
+    w, s, _ = weights(1, N, K, "mxfp4", 6)
+    la, lb, scaling = adapters(1, rank, N, K, 7)
+    la[0, rank - 1, 17] = float("inf")
+    a = bf16(2, M, K)
+    assert (a[:, 17] != 0).all() and (lb[0, :, rank - 1] != 0).all()
+    got = ops.fp4_gemm_w4a16_lora(a.cuda(), w[0], s[0], torch.tensor([0, M], dtype=torch.int32).cuda(),
+                                  torch.zeros(1, dtype=torch.int32).cuda(), la.cuda(), lb.cuda(), scaling.cuda(),
+                                  out_dtype=torch.float32)
+    want = float("inf") * a[:, 17, None].float().sign() * lb[0, None, :, rank - 1].float().sign()
+    assert torch.equal(got.cpu(), want)
+
+
 def test_no_rows():
     w, s, _ = weights(1, 32, 512, "mxfp4", 1)
     la, lb, scaling = (t.cuda() for t in adapters(1, 8, 32, 512, 1))
