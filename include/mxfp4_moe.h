@@ -366,14 +366,14 @@ int moe_grouped_gemm_w4a16(const uint16_t* a, int64_t a_rows, int64_t R, const i
  *   c[t] = a[t] * W_hat^T + scaling[l] * (a[t] * lora_a[l]^T) * lora_b[l]^T
  * where l = seg_adapter[s] for the segment s with seg_offsets[s] <= t < seg_offsets[s+1].
  * A segment whose adapter is outside [0, L) (say -1), and rows in no segment, get the
- * projection alone.
+ * projection alone. Infinities and NaN of an adapter reach the rows of its segments only.
  *   a            [M][K] bf16;  w, w_scale as for mxfp4_gemm_w4a16 / nvfp4_gemm_w4a16
- * Infinities and NaN of an adapter reach the rows of its segments only.
  *   seg_offsets  [S+1] int32, ascending (a request's rows are consecutive); seg_adapter [S]
  *   lora_a       [L][rank][K] bf16;  lora_b [L][N][rank] bf16;  scaling [L] fp32. An adapter
  *                of a smaller rank is padded with zero rows of lora_a.
- *   c            [M][N] fp32 or bf16 (c_dtype), one rounding at the end; the low-rank
- *                product is kept in fp32 between its two factors
+ *   c            [M][N] fp32 or bf16 (c_dtype), one rounding at the end; between its
+ *                two factors the low-rank product is held in fp32 (few rows) or as two bf16
+ *                terms (16 significant bits)
  *   workspace    fp4_w4a16_lora_workspace_bytes() bytes, 16-byte aligned, contents
  *                irrelevant; calls that may overlap need one each
  * Requires K % 512 == 0, N % 16 == 0, rank % 8 == 0, 8 <= rank <= 128, and the codes and one
@@ -405,7 +405,8 @@ int fp4_gemm_w4a16_lora(const uint16_t* a, int64_t M, int64_t N, int64_t K, int 
  *   r, n, q      any may be NULL (not wanted), not all; n [T][H] (n_dtype); q [T][H] (E4M3)
  *                or [T][H/2] (E2M1) by fmt, with q_scale [T][H/32]
  * Requires H % 8 == 0 (H % 32 == 0 with q), H <= 65536, eps > 0, topk <= 8; with topk == 0
- * y_rows must be T. T == 0 is a no-op. Errors: NULL, SHAPE, ALIGN, FORMAT, UNSUPPORTED.
+ * y_rows must be T, with topk > 0 at least 1. T == 0 is a no-op.
+ * Errors: NULL, SHAPE, ALIGN, FORMAT, UNSUPPORTED.
  */
 int moe_block_norm(const void* y, int y_dtype, int64_t y_rows, const float* expert_gates, const int32_t* pair_row,
                    int32_t topk, int64_t T, int64_t H, const void* x, int x_dtype, float residual_scale,

@@ -336,7 +336,7 @@ int moe_block_norm(const void* y, int y_dtype, int64_t y_rows, const float* expe
       !valid_dtype(n_dtype) || !valid_elem(fmt) || gate_mode < 0 || gate_mode > 3)
     return MXF_ERR_FORMAT;
   if (T < 0 || H <= 0 || H % (q ? 32 : 8) != 0 || topk < 0 || topk > 8 || y_rows < 0) return MXF_ERR_SHAPE;
-  if (!(eps > 0.0f) || (topk == 0 && y_rows != T)) return MXF_ERR_SHAPE;
+  if (!(eps > 0.0f) || (topk == 0 ? y_rows != T : T > 0 && y_rows < 1)) return MXF_ERR_SHAPE;
   if (H > 65536 || T > kMaxRows || y_rows > kMaxRows || T * topk > kMaxRows) return MXF_ERR_UNSUPPORTED;
   if (T == 0) return MXF_OK;
   if (!y || (topk > 0 && (!expert_gates || !pair_row)) || (gate_mode > 0 && !gate)) return MXF_ERR_NULL;

@@ -88,6 +88,15 @@ def test_block_norm_errors():
         assert call(fn, good, **change) == want, change
 
 
+def test_block_norm_combine_needs_rows():
+    """The combine of dropped pairs only still reads a row of y beside them: there has to be one."""
+    fn = _lib().moe_block_norm
+    good = dict(y=A, yd=1, rows=0, eg=A, pr=A, topk=2, T=0, H=64, x=None, xd=1, alpha=1.0, post=None, pre=None, wd=0,
+                eps=1e-6, gate=None, gd=1, gm=0, r=A, n=A, nd=1, fmt=0, q=None, qs=None, stream=None)
+    assert call(fn, good) == OK
+    assert call(fn, good, T=5) == SHAPE
+
+
 def test_binding_refuses_host_tensors():
     z = torch.zeros
     a, off = z(4, 128, dtype=torch.bfloat16), z(3, dtype=torch.int32)
