@@ -1,14 +1,20 @@
 // Grouped products of bf16 activations with FP4 expert weights over ragged row ranges.
 // Experts of at most 16 rows (decode, the tail of a skewed routing) stream their weights
-// here; the others run in the tiled kernel (w4a16_tile.hip).
+// here, and so does all of a small call; the others run in the tiled kernel
+// (w4a16_tile_body.hpp, launched from w4a16_tile.hip).
 //
-// The streaming kernel: a workgroup owns one expert and kSub runs, one after the other, of 64 of
-// its weight rows (SwiGLU: 32 gate rows and the 32 matching up rows), its 4 waves split K and meet in LDS in a fixed
-// order. HBM bound: every weight byte is read once, as whole 128-byte lines with
-// non-temporal loads, and passed through a per-wave LDS area into the lane layout of the
-// 16x16x32 bf16 MFMA: lane (g, r16) holds the 32 codes of row r16, block 4 s + g of a
-// 512-k super-step at step s, and instruction j takes their codes 8 j + [0, 8) against
-// activations k = 128 s + 32 g + 8 j + [0, 8).
+// The streaming kernel: a workgroup owns one expert and kSub runs, one after the other, of 64
+// of its weight rows (SwiGLU: 32 gate rows and the 32 matching up rows); its 4 waves split K
+// and meet in LDS in a fixed order. HBM bound: every weight byte is read once, as whole
+// 128-byte lines with non-temporal loads, and passed through a per-wave LDS area into the
+// lane layout of the 16x16x32 bf16 MFMA: lane (g, r16) holds the 32 codes of row r16, block
+// 4 s + g of a 512-k super-step at step s, and instruction j takes their codes 8 j + [0, 8)
+// against activations k = 128 s + 32 g + 8 j + [0, 8). Activations and scales pass through
+// LDS too: loaded by the lane that needs them, 16 rows in 16 neighbouring lanes, they cost the
+// address unit 64 accesses an instruction, and that was the bound (48 rows over 48 of 256
+// experts of 4096 x 7168, SwiGLU, 0.67 GB: 158 us with both, 123 with the scales, 111 with
+// both through LDS = 6.1 TB/s). A launch that stays on the chip and walks the experts was
+// slower (143 us), and so were a super-step's activations loaded one super-step ahead (115).
 #include "w4a16_tile.hpp"
 
 namespace mxf {
@@ -173,16 +179,16 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(kNV ? 
     const int lr = 4 * g + wave;
     if (lr < m) {
 #pragma unroll
-    for (int f = 0; f < (kSwiglu ? 2 : 4); ++f) {
-      float v;
-      if constexpr (kSwiglu) v = silu_mul(tot[f], tot[f + 2]);
-      else v = tot[f];
-      const int64_t c = i0 + 16 * f;
-      if (c >= ocols) continue;
-      const int64_t at = (row0 + lr) * ocols + c + r16;
-      if (kOutBF16) static_cast<uint16_t*>(a.out)[at] = (uint16_t)bf16x2_bits(v, 0.0f);
-      else static_cast<float*>(a.out)[at] = v;
-    }
+      for (int f = 0; f < (kSwiglu ? 2 : 4); ++f) {
+        float v;
+        if constexpr (kSwiglu) v = silu_mul(tot[f], tot[f + 2]);
+        else v = tot[f];
+        const int64_t c = i0 + 16 * f;
+        if (c >= ocols) continue;
+        const int64_t at = (row0 + lr) * ocols + c + r16;
+        if (kOutBF16) static_cast<uint16_t*>(a.out)[at] = (uint16_t)bf16x2_bits(v, 0.0f);
+        else static_cast<float*>(a.out)[at] = v;
+      }
     }
   }
 }

@@ -9,7 +9,11 @@
 //            others shrink, then one pass that adds the slices and the fp32 expansion: at these
 //            sizes a call costs its launches and the length of its K chain (256 requests of one
 //            row at 4096 x 7168, rank 16: 77 us with whole-K tiles, whose last stage walks 64
-//            segments, ... sliced).
+//            segments, 35 us sliced).
+// Measured: 4096 x 4096 x 7168, rank 64, 8 requests (0.25 TFLOP) 240 us, of which the shrink 28
+// and the tiles 205 = 1.17 PFLOP/s, bound as the tiled product is; 64 requests of one row at
+// 4096 x 7168, rank 16 (26 MB) 18 us, one row at rank 32 10 us, two launches of which one lasts at least
+// 3.4 us.
 #include "w4a16_tile_body.hpp"
 
 namespace mxf {
@@ -29,15 +33,16 @@ struct ShrinkArgs {
 };
 
 // A workgroup's shrink: row block blk of 16 MF rows, K slice `slice` of p.slices, every
-// zsplit-th segment of those rows from the z-th on. NW waves split the slice's K and meet in LDS in wave order. MF x RF
-// fragments of 16 rows x 16 ranks on the 16x16x32 MFMA. Bound by the loads: a workgroup
-// reads its rows' share of a once and the adapters of their segments; the launches deal
-// row blocks to the XCDs in contiguous ranges, so that an adapter is fetched into the L2 of
-// the XCDs that use it only. A load instruction takes whole 128-byte lines of 8 rows (lanes that follow
-// each other read what follows: the matrix lane layout, 16 rows in 16 neighbouring lanes,
-// costs the address unit 64 accesses an instruction: 73 us instead of 37 for 4096 x 7168
-// activations and rank 64);
-// each fragment then passes through 2 KB of the wave's LDS into the lane layout.
+// zsplit-th segment of those rows from the z-th on. NW waves split the slice's K and meet in
+// LDS in wave order. MF x RF fragments of 16 rows x 16 ranks on the 16x16x32 MFMA. Bound by
+// the loads: a workgroup reads its rows' share of a once and the adapters of their segments;
+// the launches deal row blocks to the XCDs in contiguous ranges, so that an adapter is
+// fetched into the L2 of the XCDs that use it only. A load instruction takes whole 128-byte
+// lines of 8 rows, and each fragment then passes through 2 KB of the wave's LDS into the lane
+// layout (loaded in that layout, 16 rows in 16 neighbouring lanes, it costs the address unit
+// 64 accesses an instruction: 73 us instead of 37 for 4096 x 7168 activations and rank 64).
+// With K slices, so that there is a workgroup for each compute unit, 28 us = 2.1 TB/s of
+// activations.
 template <int MF, int RF, int NW>
 struct ShrinkLds {
   v4i part[NW][(MF * RF * 1024 > 2048 ? MF * RF * 1024 : 2048) / 16];  // per wave: a fragment, then its partial sums
@@ -203,7 +208,9 @@ struct FinishArgs {
 
 constexpr int kMaxBaseSlices = 8, kMaxLowSlices = 16;
 
-// one row, 256 columns per workgroup of one wave: 4 columns per lane
+// One row, 256 columns per workgroup of one wave: 4 columns per lane. Latency bound (a chain of
+// segment lookup, low, sum over the rank): about 5 of the 18 us of 64 requests at 4096 x 7168.
+// lora_b through LDS in whole lines instead of a lane's own rows: 18.6 us.
 template <bool kOutBF16>
 __global__ void __launch_bounds__(64) lora_finish_kernel(FinishArgs p) {
   __shared__ float low[128];

@@ -4,18 +4,30 @@
 //
 // A workgroup computes BM rows x BN weight rows with waves of 64 rows x 32 FN weight rows
 // on the 32x32x16 bf16 MFMA (weights as the first operand, so a lane ends up with runs of
-// 4 consecutive columns of one row). A stage is 64 k: BM x 128 bytes of activations,
-// BN x 32 bytes of codes and one scale dword per weight row, all copied HBM -> LDS
-// directly; three slots, the copies of stage st + 2 go out while st is computed. The
-// weights stay 4 bits wide up to the registers: a lane reads the 16 bytes that hold 32
-// codes of its weight row and converts 8 of them (exactly: a code times its scale has at
-// most 5 significant bits) in front of each MFMA.
+// 4 consecutive columns of one row). A stage is 64 k. Everything is copied HBM -> LDS
+// directly: NA slots of BM x 128 bytes of activations, one stage each; two of BN x 64 bytes
+// of codes, 128 k each; two of 16 scale bytes per weight row (512 k of MXFP4, 256 k of
+// NVFP4). The wider pieces of codes and scales halve and quarter the number of cache lines
+// that a copy asks for (a 7168-long K over one share of 64 experts: the copies alone 473 us
+// with 32 bytes and one scale dword a stage, 357 so). The copies of stage st + NA - 1 go out
+// while st is computed. The weights stay 4 bits wide up to the registers: a lane reads the 16
+// bytes that hold 32 codes of its weight row and converts 8 of them (exactly: a code times
+// its scale has at most 5 significant bits) in front of each MFMA.
 //
 // K order: inside a stage MFMA j takes, in lane group g (lane / 32), k = 32 g + 8 j +
-// [0, 8), for both operands: a weight lane's 16 bytes are 16-byte chunk g of its 32-byte
-// stage row, one 32-element block, and an activation lane reads chunk 4 g + j of its
+// [0, 8), for both operands: a weight lane's 16 bytes are chunk 2 (st & 1) + g of its
+// 64-byte code row, one 32-element block, and an activation lane reads chunk 4 g + j of its
 // 128-byte stage row. Chunks are XOR-swizzled per row so that the 16 lanes of an LDS
 // cycle hit different banks.
+//
+// Many rows are bound by the MFMA at the clock that the power allows: 64 experts x 4096 x
+// 7168, 12288 rows, SwiGLU (0.72 TFLOP) 605 us = 1.19 PFLOP/s, the MFMA busy 65 % of the time
+// at 1.8 GHz; a plain bf16 product of the same size from the library 552 us. There the 128 x
+// 256 tile has two slots (73 KB: two workgroups a compute unit, whose stages interleave); 256
+// x 256 and 128 x 512, one workgroup a compute unit, were slower (742 us). Few tiles are
+// bound by the length of a stage, 0.36 us with 64 x 128 tiles: copy, barrier, decode and MFMA
+// of one wave after each other. Three slots there; four or five take the room of a workgroup
+// (256 rows x 4096 x 7168 in K slices 35 -> 38 us).
 //
 // Rows past a unit's end and weight rows past N read as zero through the range-checked
 // buffer resources and are not stored.
@@ -48,8 +60,8 @@ __device__ __forceinline__ v16f mfma32x32x16(v8bf a, v8bf b, v16f c) {
 }
 
 // One workgroup's tile: BM x BN by NW waves, BM / 64 of them over rows, the others over
-// columns; x, j: its XCD and item. kSlices (one matrix, j = unit x ntiles + n-tile): only the K slice `slice` of a.kslices, whose sums go
-// to slice `slice` of out, [kslices][R][N] fp32.
+// columns; x, j: its XCD and item. kSlices (one matrix, j = unit x ntiles + n-tile): only the
+// K slice `slice` of a.kslices, whose sums go to slice `slice` of out, [kslices][R][N] fp32.
 template <int BM, int BN, int NW, int NA, bool kNV, bool kSwiglu, bool kOutBF16, bool kLora, bool kSlices>
 __device__ __forceinline__ void w16_tile(const W16TileArgs& a, W16Ring<BM, BN, NA>& ring, int x, int j, int slice) {
   constexpr int WMN = BM / 64, WNN = NW / WMN, FN = BN / WNN / 32;
