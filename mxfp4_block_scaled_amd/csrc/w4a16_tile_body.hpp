@@ -8,7 +8,7 @@
 // directly: NA slots of BM x 128 bytes of activations, one stage each; two of BN x 64 bytes
 // of codes, 128 k each; two of 16 scale bytes per weight row (512 k of MXFP4, 256 k of
 // NVFP4). The wider pieces of codes and scales halve and quarter the number of cache lines
-// that a copy asks for (a 7168-long K over one share of 64 experts: the copies alone 473 us
+// that a copy asks for (12288 rows over 32 experts of 4096 x 7168: the copies alone 473 us
 // with 32 bytes and one scale dword a stage, 357 so). The copies of stage st + NA - 1 go out
 // while st is computed. The weights stay 4 bits wide up to the registers: a lane reads the 16
 // bytes that hold 32 codes of its weight row and converts 8 of them (exactly: a code times
@@ -20,7 +20,7 @@
 // 128-byte stage row. Chunks are XOR-swizzled per row so that the 16 lanes of an LDS
 // cycle hit different banks.
 //
-// Many rows are bound by the MFMA at the clock that the power allows: 64 experts x 4096 x
+// Many rows are bound by the MFMA at the clock that the power allows: 32 experts x 4096 x
 // 7168, 12288 rows, SwiGLU (0.72 TFLOP) 605 us = 1.19 PFLOP/s, the MFMA busy 65 % of the time
 // at 1.8 GHz; a plain bf16 product of the same size from the library 552 us. There the 128 x
 // 256 tile has two slots (73 KB: two workgroups a compute unit, whose stages interleave); 256

@@ -66,6 +66,9 @@ CASES = [
     ([1] * 300, 5, 0, 272, 1024, 16, 7, "nvfp4", torch.float32),  # single rows, sliced
     ([100, 0, 1900, 3, 97], 0, 0, 1040, 512, 24, 3, "mxfp4", torch.bfloat16),  # 64 x 128 tiles, low in K slices
     ([7] * 300, 1, 2, 1040, 1536, 8, 5, "mxfp4", torch.float32),  # the same with short segments
+    ([100, 3, 0, 90, 1, 200, 2, 371], 4, 6, 1520, 1024, 24, 5, "nvfp4", torch.bfloat16),  # sliced, long segments
+    ([3] * 10 + [0] * 80 + [6] * 100 + [1], 0, 1, 1520, 512, 40, 6, "mxfp4", torch.float32),  # empty ones between
+    ([1, 2] * 200 + [400], 2, 0, 1296, 512, 8, 3, "mxfp4", torch.float32),
     ([150, 50], 0, 0, 4112, 2048, 128, 2, "nvfp4", torch.float32),  # a wide adapter: few tiles, not sliced
     ([900, 3200], 0, 4, 4352, 512, 16, 2, "mxfp4", torch.float32),  # 128 x 256 tiles
     ([2049, 1, 2046], 0, 0, 4096, 512, 120, 3, "nvfp4", torch.bfloat16),
@@ -129,10 +132,11 @@ def test_rows_and_adapters_stay_apart(M):
 
 
 @pytest.mark.parametrize("bad", [float("nan"), float("inf")])
-@pytest.mark.parametrize("M,N,K,rank", [(9, 272, 512, 24), (200, 4112, 512, 128), (4100, 4352, 512, 16)])
+@pytest.mark.parametrize("M,N,K,rank", [(9, 272, 512, 24), (777, 1520, 512, 24), (200, 4112, 512, 128),
+                                        (4100, 4352, 512, 16)])
 def test_an_adapter_that_is_not_finite_reaches_its_own_rows_only(M, N, K, rank, bad):
     """One of the adapters in use holds a NaN or an infinity: the requests beside it keep their results bit for
-    bit, and its own rows show it (one row per workgroup pass, 64 x 128 tiles, 128 x 256 tiles)."""
+    bit, and its own rows show it (sliced; 64 x 128 tiles, 128 x 256 tiles)."""
     L = 3
     w, s, _ = weights(1, N, K, "mxfp4", 6)
     la, lb, scaling = (t.cuda() for t in adapters(L, rank, N, K, 7))
