@@ -50,8 +50,22 @@ __device__ __forceinline__ uint32_t w16_eighths(uint32_t n, int x) {
   return (n >> 3) * (uint32_t)x + (((n & 7u) * (uint32_t)x) >> 3);
 }
 
-// Item j of XCD x: the units' items (n-tile by n-tile inside an expert, unit by unit inside
-// an n-tile) are split into 8 contiguous ranges, one per XCD, so that the workgroups of an
+// Item w of units x ntiles items: groups of 8 units, n-tile by n-tile in a group, so that the some
+// 64 items that an XCD has at work are about 8 units x 8 n-tiles, which take the fewest bytes
+// into its L2. N-tile by n-tile over all units, an XCD reads all of the activations: 4096 x 4096 x
+// 7168 with adapters 250 us, so 241; 8192 rows 433, 416; 8192 rows over 2 experts 436, 424; 16 units
+// 244, 421, 426. Groups of n-tiles instead lose where an expert has few units (32 experts of 384
+// rows 621, 635). ntiles x 8 stays in 32 bits: ntiles < 2^25.
+__device__ __forceinline__ void w16_place(uint32_t w, uint32_t units, uint32_t ntiles, int& n_tile, int& unit) {
+  constexpr uint32_t kGroup = 8;
+  const uint32_t grp = w / (ntiles * kGroup), rem = w - grp * ntiles * kGroup;
+  const uint32_t width = min(kGroup, units - grp * kGroup), n = rem / width;
+  n_tile = (int)n;
+  unit = (int)(grp * kGroup + rem - n * width);
+}
+
+// Item j of XCD x: the units' items (in an expert of more than 16 rows as w16_place puts them, else
+// n-tile by n-tile) are split into 8 contiguous ranges, one per XCD, so that the workgroups of an
 // XCD share activation rows and weight tiles in its L2. Called by whole waves; false: none.
 // Every workgroup starts with this, so its latency counts: with CE > 0 (E <= 64 CE) each
 // lane takes its experts' offsets in one batch of loads and keeps them.
@@ -124,8 +138,13 @@ __device__ __forceinline__ bool w16_item_of(const int32_t* __restrict__ off, int
   c = __builtin_amdgcn_readlane(c, src);
   lo = __builtin_amdgcn_readlane(lo, src);
   const uint32_t local = w - (uint32_t)ue * (uint32_t)ntiles;
-  n_out = (int)(local / (uint32_t)ke);
-  const int loc = (int)(local - (uint32_t)n_out * (uint32_t)ke);
+  int loc;
+  if constexpr (BM >= 64) {
+    w16_place(local, (uint32_t)ke, (uint32_t)ntiles, n_out, loc);
+  } else {
+    n_out = (int)(local / (uint32_t)ke);
+    loc = (int)(local - (uint32_t)n_out * (uint32_t)ke);
+  }
   if (n_out < 0 || n_out >= ntiles || loc < 0) return false;
   row0 = lo + (int64_t)loc * BM;
   m = min(BM, c - loc * BM);

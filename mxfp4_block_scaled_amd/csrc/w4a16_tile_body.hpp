@@ -84,12 +84,13 @@ __device__ __forceinline__ void w16_tile(const W16TileArgs& a, W16Ring<BM, BN, N
   } else {
     if (a.offsets) {
       if (!w16_item<BM>(a.offsets, a.E, a.R, a.min_rows, a.max_rows, a.ntiles, x, j, e, n_tile, row0, m)) return;
-    } else {  // the items of an n-tile are its units; 8 contiguous ranges of items, one per XCD
+    } else {  // 8 contiguous ranges of items, one per XCD
       const uint32_t units = (uint32_t)((a.R + BM - 1) / BM), total = units * (uint32_t)a.ntiles;
       const uint32_t w = w16_eighths(total, x) + (uint32_t)j;
       if (w >= w16_eighths(total, x + 1)) return;
-      n_tile = (int)(w / units);
-      row0 = (int64_t)(w - (uint32_t)n_tile * units) * BM;
+      int unit;
+      w16_place(w, units, (uint32_t)a.ntiles, n_tile, unit);
+      row0 = (int64_t)unit * BM;
       m = (int)min((int64_t)BM, a.R - row0);
     }
   }

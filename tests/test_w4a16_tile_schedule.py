@@ -225,3 +225,18 @@ def test_segment_search(S):
     ends = [(i * 5) // 3 for i in range(S)]  # some empty
     for t in range(-1, (ends[-1] if S else 0) + 2):
         assert first_segment(ends, S, t) == next((s for s in range(S) if ends[s] > t), S)
+
+
+def place(w, units, ntiles, group=8):
+    grp, rem = divmod(w, ntiles * group)
+    width = min(group, units - grp * group)
+    return rem // width, grp * group + rem % width
+
+
+@pytest.mark.parametrize("units", [1, 2, 3, 7, 8, 9, 32, 129])
+@pytest.mark.parametrize("ntiles", [1, 5, 8, 9, 16, 28, 61])
+def test_every_tile_is_placed_once(units, ntiles):
+    seen = [place(w, units, ntiles) for w in range(units * ntiles)]
+    assert sorted(seen) == [(n, u) for n in range(ntiles) for u in range(units)]
+    if units <= 8:  # n-tile by n-tile
+        assert seen == sorted(seen)
