@@ -145,6 +145,20 @@ __device__ __forceinline__ void w16_tile(const W16TileArgs& a, W16Ring<BM, BN, N
   for (int i = 0; i < NA - 1; ++i)
     if (st0 + i < nst) issue_a(ring.A[i], st0 + i);
 
+  // adapters: the first 64 segments of the wave's rows, on their way during the product
+  const int64_t rlo = row0 + 64 * wm, rhi = min(rlo + 64, row0 + m);
+  int s0 = 0, seg_b0 = 0, seg_b1 = 0, seg_ad = -1;
+  auto fetch_segments = [&]() {
+    const int s = s0 + lane < a.S ? s0 + lane : -1;
+    seg_b0 = a.seg_off[max(s, 0)];
+    seg_b1 = a.seg_off[s + 1];
+    seg_ad = a.seg_adapter[max(s, 0)];
+  };
+  if constexpr (kLora) {
+    s0 = first_segment(a.seg_off, a.S, rlo);
+    if (s0 < a.S) fetch_segments();
+  }
+
   v16f acc[2][FN];
 #pragma unroll
   for (int i = 0; i < 2; ++i)
@@ -247,8 +261,6 @@ __device__ __forceinline__ void w16_tile(const W16TileArgs& a, W16Ring<BM, BN, N
   // operands of the next 16 ranks are loaded before the current ones are multiplied, so that
   // many short segments cost their loads and not their latency.
   if (kLora) {
-    const int64_t rlo = row0 + 64 * wm, rhi = min(rlo + 64, row0 + m);
-    int s0 = first_segment(a.seg_off, a.S, rlo);
     int lo_l = 0, hi_l = 0, l_l = 0, k_next = a.rank;
     int lo = 0, hi = 0, l = 0, sl = a.lslices;  // the segment (relative to rlo) and slice of low of the operands to load
     unsigned long long mask = 0;
@@ -262,15 +274,15 @@ __device__ __forceinline__ void w16_tile(const W16TileArgs& a, W16Ring<BM, BN, N
       }
       while (mask == 0) {
         if (!more) return false;
-        const int s = s0 + lane;
-        const bool in = s < a.S;
-        const int64_t b0 = a.seg_off[in ? s : 0], b1 = a.seg_off[in ? s + 1 : 0];
-        l_l = in ? a.seg_adapter[s] : -1;
+        const bool in = s0 + lane < a.S;
+        const int64_t b0 = seg_b0, b1 = seg_b1;
+        l_l = seg_ad;
         lo_l = (int)(max(b0, rlo) - rlo);
         hi_l = (int)(min(b1, rhi) - rlo);
         mask = __ballot(in && b0 < rhi && b1 > rlo && hi_l > lo_l && l_l >= 0 && l_l < a.L);
+        more = s0 + 64 < a.S && __ballot(in && b0 >= rhi) == 0;
         s0 += 64;
-        more = s0 < a.S && __ballot(in && b0 >= rhi) == 0;
+        if (more) fetch_segments();
       }
       const int i = __ffsll((long long)mask) - 1;
       mask &= mask - 1;
