@@ -2,7 +2,7 @@
 // weight matrix, either grouped by expert with ragged row ranges (moe_grouped_gemm_w4a16)
 // or over one matrix with low-rank adapters beside it (fp4_gemm_w4a16_lora).
 //
-// A workgroup computes BM rows x BN weight rows with waves of 64 rows x 32 FN weight rows
+// A workgroup computes BM rows x BN weight rows with waves of 32 FM rows x 32 FN weight rows
 // on the 32x32x16 bf16 MFMA (weights as the first operand, so a lane ends up with runs of
 // 4 consecutive columns of one row). A stage is 64 k. Everything is copied HBM -> LDS
 // directly: NA slots of BM x 128 bytes of activations, one stage each; two of BN x 64 bytes
@@ -24,7 +24,9 @@
 // 7168, 12288 rows, SwiGLU (0.72 TFLOP) 605 us = 1.19 PFLOP/s, the MFMA busy 65 % of the time
 // at 1.8 GHz; a plain bf16 product of the same size from the library 552 us. There the 128 x
 // 256 tile has two slots (73 KB: two workgroups a compute unit, whose stages interleave); 256
-// x 256 and 128 x 512, one workgroup a compute unit, were slower (742 us). Few tiles are
+// x 256 and 128 x 512, one workgroup a compute unit, were slower (742 us). Without adapters a wave
+// there takes all 128 rows, so that a weight is decoded once (2 experts of 4096 rows 426 -> 417 us
+// against waves of 64 rows x 128), and half of the MFMAs where a unit has at most 64 rows. Few tiles are
 // bound by the length of a stage, 0.36 us with 64 x 128 tiles: copy, barrier, decode and MFMA
 // of one wave after each other. Three slots there; four or five take the room of a workgroup
 // (256 rows x 4096 x 7168 in K slices 35 -> 38 us).
@@ -59,12 +61,12 @@ __device__ __forceinline__ v16f mfma32x32x16(v8bf a, v8bf b, v16f c) {
 #endif
 }
 
-// One workgroup's tile: BM x BN by NW waves, BM / 64 of them over rows, the others over
+// One workgroup's tile: BM x BN by NW waves, BM / (32 FM) of them over rows, the others over
 // columns; x, j: its XCD and item. kSlices (one matrix, j = unit x ntiles + n-tile): only the
 // K slice `slice` of a.kslices, whose sums go to slice `slice` of out, [kslices][R][N] fp32.
 template <int BM, int BN, int NW, int NA, bool kNV, bool kSwiglu, bool kOutBF16, bool kLora, bool kSlices>
 __device__ __forceinline__ void w16_tile(const W16TileArgs& a, W16Ring<BM, BN, NA>& ring, int x, int j, int slice) {
-  constexpr int WMN = BM / 64, WNN = NW / WMN, FN = BN / WNN / 32;
+  constexpr int FM = BM == 128 && !kLora ? 4 : 2, WM = 32 * FM, WMN = BM / WM, WNN = NW / WMN, FN = BN / WNN / 32;
   constexpr int IA = BM * 8 / 64 / NW, IB = BN * 4 / 64 / NW;  // 16-byte copies per lane per 64 / 128 k
   constexpr int P = kNV ? 4 : 8;  // stages per scale group
   static_assert(IA >= 1 && IB >= 1 && BN / 64 <= NW && (!kSwiglu || FN % 2 == 0), "tile shape");
@@ -146,7 +148,7 @@ __device__ __forceinline__ void w16_tile(const W16TileArgs& a, W16Ring<BM, BN, N
     if (st0 + i < nst) issue_a(ring.A[i], st0 + i);
 
   // adapters: the first 64 segments of the wave's rows, on their way during the product
-  const int64_t rlo = row0 + 64 * wm, rhi = min(rlo + 64, row0 + m);
+  const int64_t rlo = row0 + WM * wm, rhi = min(rlo + 64, row0 + m);
   int s0 = 0, seg_b0 = 0, seg_b1 = 0, seg_ad = -1;
   auto fetch_segments = [&]() {
     const int s = s0 + lane < a.S ? s0 + lane : -1;
@@ -159,12 +161,12 @@ __device__ __forceinline__ void w16_tile(const W16TileArgs& a, W16Ring<BM, BN, N
     if (s0 < a.S) fetch_segments();
   }
 
-  v16f acc[2][FN];
+  v16f acc[FM][FN];
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+  for (int i = 0; i < FM; ++i)
 #pragma unroll
     for (int f = 0; f < FN; ++f) acc[i][f] = v16f{};
-  int brow_l[FN], aoff[2], boff[FN];
+  int brow_l[FN], aoff[FM], boff[FN];
 #pragma unroll
   for (int f = 0; f < FN; ++f) {
     if (kSwiglu) brow_l[f] = (f < FN / 2 ? 0 : BN / 2) + FN * 16 * wn + 32 * (f % (FN > 1 ? FN / 2 : 1)) + r32;
@@ -172,15 +174,16 @@ __device__ __forceinline__ void w16_tile(const W16TileArgs& a, W16Ring<BM, BN, N
     boff[f] = brow_l[f] * 64 + 16 * (g ^ swz_b16(brow_l[f]));
   }
 #pragma unroll
-  for (int f = 0; f < 2; ++f) {
-    const int r = 64 * wm + 32 * f + r32;
+  for (int f = 0; f < FM; ++f) {
+    const int r = WM * wm + 32 * f + r32;
     aoff[f] = r * 128 + 16 * ((4 * g) ^ swz_a16(r));
   }
 
-  auto compute = [&](const uint8_t* As, const uint8_t* Bs, auto Odd, int st) {
+  auto compute = [&](const uint8_t* As, const uint8_t* Bs, auto Odd, auto Rows, int st) {
+    constexpr int nf = decltype(Rows)::value;  // fragments of 32 rows
     constexpr int odd = decltype(Odd)::value;  // stages of 128 k: blocks 0, 1 then 2, 3 of a row's codes
     const uint8_t* const Ss = &ring.S[(st / P) & 1][4 * (kNV ? st & 3 : (st & 7) >> 1)];
-    v4i b[FN], av[2][4];
+    v4i b[FN], av[nf][4];
     uint32_t sd[FN];
 #pragma unroll
     for (int f = 0; f < FN; ++f) {
@@ -192,7 +195,7 @@ __device__ __forceinline__ void w16_tile(const W16TileArgs& a, W16Ring<BM, BN, N
 #pragma unroll
     for (int j = 0; j < 4; ++j)
 #pragma unroll
-      for (int f = 0; f < 2; ++f) {
+      for (int f = 0; f < nf; ++f) {
         int o = aoff[f];
         asm volatile("" : "+v"(o));
         av[f][j] = *reinterpret_cast<const v4i*>(As + (o ^ (16 * j)));
@@ -213,17 +216,17 @@ __device__ __forceinline__ void w16_tile(const W16TileArgs& a, W16Ring<BM, BN, N
       for (int f = 0; f < FN; ++f) {
         const v8bf wv = kNV ? decode8_nv((uint32_t)b[f][j], sc[f][j >> 1]) : decode8((uint32_t)b[f][j], sc[f][0]);
 #pragma unroll
-        for (int fm = 0; fm < 2; ++fm) acc[fm][f] = mfma32x32x16(wv, __builtin_bit_cast(v8bf, av[fm][j]), acc[fm][f]);
+        for (int fm = 0; fm < nf; ++fm) acc[fm][f] = mfma32x32x16(wv, __builtin_bit_cast(v8bf, av[fm][j]), acc[fm][f]);
       }
   };
-  const bool active = 64 * wm < m;
+  const bool active = WM * wm < m;
   // stage st: wait for the copies it needs, meet the other waves (their parts have landed
   // too, and everyone is done with stage st - 1), issue into what stage st - 1 freed, compute.
   // Issue order at stage t: on even t the codes of stages t + 2, t + 3 and, where a scale
   // group begins, the next group, then the activations of t + NA - 1. So with NA == 3 only the last
   // stage's issues may stay in flight: A, and after an even stage B (and S) before it.
   auto next_s = [&](int st) { return (st % P == 0 || (kSlices && st == st0)) && (st / P + 1) * P < nst; };
-  auto step = [&](auto I, int st) {
+  auto step = [&](auto I, auto Rows, int st) {
     constexpr int i = decltype(I)::value;  // of the slots: st - st0 modulo whole turns
     if (NA == 2 || st + 1 >= nst) {
       wait_vmcnt<0>();
@@ -239,17 +242,21 @@ __device__ __forceinline__ void w16_tile(const W16TileArgs& a, W16Ring<BM, BN, N
     if (i % 2 == 0 && next_s(st)) issue_s(st / P + 1);
     if (st + NA - 1 < nst) issue_a(ring.A[(i + NA - 1) % NA], st + NA - 1);
     __builtin_amdgcn_sched_barrier(0);
-    if (active) compute(ring.A[i % NA], ring.B[(i / 2) % 2], std::integral_constant<int, i % 2>{}, st);
+    if (active) compute(ring.A[i % NA], ring.B[(i / 2) % 2], std::integral_constant<int, i % 2>{}, Rows, st);
   };
   constexpr int U = NA == 3 ? 12 : 4;  // whole turns of the A and B slots
-  for (int st = st0; st < nst; st += U)  // nst is even
-    static_for<0, U / 2>([&](auto X_) {
-      constexpr int X = 2 * decltype(X_)::value;
-      if (st + X < nst) {
-        step(std::integral_constant<int, X>{}, st + X);
-        step(std::integral_constant<int, X + 1>{}, st + X + 1);
-      }
-    });
+  auto stages = [&](auto Rows) {
+    for (int st = st0; st < nst; st += U)  // nst is even
+      static_for<0, U / 2>([&](auto X_) {
+        constexpr int X = 2 * decltype(X_)::value;
+        if (st + X < nst) {
+          step(std::integral_constant<int, X>{}, Rows, st + X);
+          step(std::integral_constant<int, X + 1>{}, Rows, st + X + 1);
+        }
+      });
+  };
+  if (FM > 2 && m <= WM / 2) stages(std::integral_constant<int, FM / 2>{});  // half a unit of rows
+  else stages(std::integral_constant<int, FM>{});
 
   lds_barrier();  // every wave is done with the ring
   if (!active) return;
@@ -392,7 +399,7 @@ __device__ __forceinline__ void w16_tile(const W16TileArgs& a, W16Ring<BM, BN, N
   uint8_t* const out = static_cast<uint8_t*>(a.out) + (kSlices ? (int64_t)slice * a.R * N * 4 : 0);
   const int64_t col0 = ((int64_t)n_tile * BN >> (kSwiglu ? 1 : 0)) + OF * 32 * wn;
 #pragma unroll
-  for (int fm = 0; fm < 2; ++fm)
+  for (int fm = 0; fm < FM; ++fm)
 #pragma unroll
     for (int p = 0; p < OF / PF; ++p) {
 #pragma unroll
@@ -420,7 +427,7 @@ __device__ __forceinline__ void w16_tile(const W16TileArgs& a, W16Ring<BM, BN, N
       for (int k = 0; k < NCH / 2; ++k) {
         const int idx = lane + 64 * k, rr = idx / NCH, c = idx % NCH;
         const v4i v = *reinterpret_cast<const v4i*>(stg + RB * rr + 16 * (c ^ (rr & (NCH - 1))));
-        const int lrow = 64 * wm + 32 * fm + rr;
+        const int lrow = WM * wm + 32 * fm + rr;
         const int64_t col = col0 + p * PF * 32 + c * (16 / ES);
         if (lrow < m && col < ocols)
           *reinterpret_cast<v4i*>(out + ((row0 + lrow) * ocols + col) * ES) = v;

@@ -7,6 +7,8 @@ import pytest
 
 SHAPES = [(128, 256, 4, False), (128, 256, 4, True), (64, 256, 4, False), (64, 256, 4, True),
           (64, 128, 4, False)]
+# rows per wave: 128 in the 128 x 256 tiles of experts, else 64
+WAVES = [(*shape, 64) for shape in SHAPES] + [(*shape, 128) for shape in SHAPES[:2]]
 
 
 def swz_a(r):
@@ -36,9 +38,9 @@ def copies(BM, BN, NW):
                 yield "S", wave * 1024 + 16 * lane, (64 * wave + lane, 0)
 
 
-@pytest.mark.parametrize("BM,BN,NW,swiglu", SHAPES)
-def test_slot_is_filled_and_read_in_one_layout(BM, BN, NW, swiglu):
-    WMN = BM // 64
+@pytest.mark.parametrize("BM,BN,NW,swiglu,WM", WAVES)
+def test_slot_is_filled_and_read_in_one_layout(BM, BN, NW, swiglu, WM):
+    WMN = BM // WM
     WNN = NW // WMN
     FN = BN // WNN // 32
     slot = {"A": {}, "B": {}, "S": {}}
@@ -66,9 +68,9 @@ def test_slot_is_filled_and_read_in_one_layout(BM, BN, NW, swiglu):
                         assert slot["B"][at] == (row, 2 * odd + g)
                 if wm == 0:
                     cols_seen.append(row)
-        for f in range(2):
+        for f in range(WM // 32):
             for r32 in range(32):
-                r = 64 * wm + 32 * f + r32
+                r = WM * wm + 32 * f + r32
                 if wn == 0:
                     rows_seen.append(r)
                 for g in range(2):
@@ -79,9 +81,9 @@ def test_slot_is_filled_and_read_in_one_layout(BM, BN, NW, swiglu):
     assert sorted(rows_seen) == list(range(BM)) and sorted(cols_seen) == list(range(BN))
 
 
-@pytest.mark.parametrize("BM,BN,NW,swiglu", SHAPES)
-def test_output_columns_are_those_of_the_weight_rows(BM, BN, NW, swiglu):
-    WNN = NW // (BM // 64)
+@pytest.mark.parametrize("BM,BN,NW,swiglu,WM", WAVES)
+def test_output_columns_are_those_of_the_weight_rows(BM, BN, NW, swiglu, WM):
+    WNN = NW // (BM // WM)
     FN = BN // WNN // 32
     OF = FN // 2 if swiglu else FN
     half = 4096
