@@ -372,8 +372,7 @@ int moe_grouped_gemm_w4a16(const uint16_t* a, int64_t a_rows, int64_t R, const i
  *   lora_a       [L][rank][K] bf16;  lora_b [L][N][rank] bf16;  scaling [L] fp32. An adapter
  *                of a smaller rank is padded with zero rows of lora_a.
  *   c            [M][N] fp32 or bf16 (c_dtype), one rounding at the end; between its
- *                two factors the low-rank product is held in fp32 (few rows) or as two bf16
- *                terms (16 significant bits)
+ *                two factors the low-rank product is held in fp32
  *   workspace    fp4_w4a16_lora_workspace_bytes() bytes, 16-byte aligned, contents
  *                irrelevant; calls that may overlap need one each
  * Requires K % 512 == 0, N % 16 == 0, rank % 8 == 0, 8 <= rank <= 128, and the codes and one

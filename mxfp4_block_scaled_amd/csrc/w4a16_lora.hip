@@ -4,7 +4,9 @@
 //   shrink:  low[t] = scaling[l] * a[t] . lora_a[l]^T in fp32
 //   tiles enough to fill the chip: the shrink, then the tiled product (w4a16_tile_body.hpp),
 //            which takes low . lora_b^T into its accumulators after the last stage, so c is
-//            written once.
+//            written once. A tile adds its rows' K slices of low and splits the fp32 sums once, into
+//            three bf16 terms that give them back exactly (4096 x 4096 x 7168, rank 64, 227 us; as two
+//            rounded terms slice by slice, 16 bits, 234; each wave splitting its operands itself 241).
 //   fewer:   a launch in which some workgroups compute K slices of the projection's tiles and the
 //            others shrink, then one pass that adds the slices and the fp32 expansion: at these
 //            sizes a call costs its launches and the length of its K chain (256 requests of one
@@ -27,8 +29,7 @@ struct ShrinkArgs {
   const float* scaling;
   const int32_t* seg_off;
   const int32_t* seg_adapter;
-  float* low;                 // kSplit: [slices][M][rank] fp32
-  uint16_t *low_hi, *low_lo;  // else [M][rank] bf16 each, the sum's two terms
+  float* low;  // [slices][M][rank]
   int64_t M, K;
   int rank, L, S, zsplit, slices;
 };
@@ -50,7 +51,7 @@ struct ShrinkLds {
   v4i part[NW][(MF * RF * 1024 > 2048 ? MF * RF * 1024 : 2048) / 16];  // per wave: a fragment, then its partial sums
 };
 
-template <int MF, int RF, int NW, bool kSplit>
+template <int MF, int RF, int NW>
 __device__ __forceinline__ void lora_shrink(const ShrinkArgs& p, ShrinkLds<MF, RF, NW>& lds, uint32_t blk, int slice, int z) {
   auto& part = lds.part;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -132,15 +133,7 @@ __device__ __forceinline__ void lora_shrink(const ShrinkArgs& p, ShrinkLds<MF, R
       t *= scale;
       const int64_t row = lo + 16 * (i / (4 * RF)) + 4 * g + (i & 3);
       const int r = 16 * ((i >> 2) % RF) + r16;
-      if (row >= hi || r >= p.rank) continue;
-      if (kSplit) {
-        p.low[((int64_t)slice * p.M + row) * p.rank + r] = t;
-      } else {
-        const __bf16 h = (__bf16)t, d = (__bf16)(isfinite((float)h) ? t - (float)h : 0.0f);  // an infinity stays one
-        const int64_t at = ((int64_t)slice * p.M + row) * p.rank + r;
-        p.low_hi[at] = __builtin_bit_cast(uint16_t, h);
-        p.low_lo[at] = __builtin_bit_cast(uint16_t, d);
-      }
+      if (row < hi && r < p.rank) p.low[((int64_t)slice * p.M + row) * p.rank + r] = t;
     }
     __syncthreads();  // the sums have been read: the areas are free for the next segment
   }
@@ -153,7 +146,7 @@ __global__ void __launch_bounds__(NW * 64) lora_shrink_kernel(ShrinkArgs p) {
   const uint32_t nb = (uint32_t)((p.M + 16 * MF - 1) / (16 * MF));
   const int x = (int)(blockIdx.x & 7u);
   const uint32_t blk = w16_eighths(nb, x) + (blockIdx.x >> 3);
-  if (blk < w16_eighths(nb, x + 1)) lora_shrink<MF, RF, NW, false>(p, lds, blk, (int)blockIdx.y, (int)blockIdx.z);
+  if (blk < w16_eighths(nb, x + 1)) lora_shrink<MF, RF, NW>(p, lds, blk, (int)blockIdx.y, (int)blockIdx.z);
 }
 
 // Sliced: the first workgroups each take a tile of the projection over a K slice, the others
@@ -169,7 +162,7 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) l
     w16_tile<64, 128, 4, 3, kNV, false, false, false, true>(a, lds.ring, 0, b % items, b / items);
   } else {
     const int per = p.slices * p.zsplit, i = (b - nbase) % per;
-    lora_shrink<1, RF, 4, true>(p, lds.s, (uint32_t)((b - nbase) / per), i % p.slices, i / p.slices);
+    lora_shrink<1, RF, 4>(p, lds.s, (uint32_t)((b - nbase) / per), i % p.slices, i / p.slices);
   }
 }
 
@@ -315,14 +308,11 @@ int launch_w16_lora(const W16LoraArgs& p, bool nv, bool out_bf16, hipStream_t st
   if (bs == 0 && !shrink_wide(p.M, p.S)) ls = 1;  // short segments: every slice is another pass over their adapters
   float* const base = p.workspace;
   float* const low = base + (int64_t)bs * p.M * p.N;
-  uint16_t* const low_hi = reinterpret_cast<uint16_t*>(low);  // not sliced: two bf16 terms in fp32's place
-  uint16_t* const low_lo = low_hi + (int64_t)ls * p.M * p.rank;
   const int64_t blocks = cdiv(p.M, 16), per_block = cdiv(p.S, blocks);
   const int z = (int)(per_block < 1 ? 1 : per_block < 16 ? per_block : 16);
   // what fits the compute units beside the projection's tiles
   if (bs > 0 && ls > 512 / (blocks * z)) ls = (int)(512 / (blocks * z) > 1 ? 512 / (blocks * z) : 1);
-  const ShrinkArgs s{p.a, p.lora_a, p.scaling, p.seg_off, p.seg_adapter, low, low_hi, low_lo, p.M, p.K, p.rank, p.L, p.S,
-                     z, ls};
+  const ShrinkArgs s{p.a, p.lora_a, p.scaling, p.seg_off, p.seg_adapter, low, p.M, p.K, p.rank, p.L, p.S, z, ls};
   W16TileArgs a{};
   a.a = p.a;
   a.a_rows = a.R = p.M;
@@ -332,8 +322,7 @@ int launch_w16_lora(const W16LoraArgs& p, bool nv, bool out_bf16, hipStream_t st
   a.N = p.N;
   a.K = p.K;
   a.out = p.out;
-  a.low_hi = low_hi;
-  a.low_lo = low_lo;
+  a.low = low;
   a.rank = p.rank;
   a.L = p.L;
   a.S = p.S;

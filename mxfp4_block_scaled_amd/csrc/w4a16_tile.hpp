@@ -20,8 +20,8 @@ struct W16TileArgs {
   void* out;               // [R][N] or, with SwiGLU, [R][N/2]
   int ntiles;
   // adapters (w4a16_lora.hip)
-  const uint16_t *low_hi, *low_lo;  // [R][rank] bf16 each: scaling * a . lora_a^T as the sum of two terms
-  int rank, L, S, lslices;  // low: lslices K slices [lslices][R][rank], each as its two terms
+  const float* low;         // [lslices][R][rank]: scaling * a . lora_a^T, K slice by K slice
+  int rank, L, S, lslices;
   int kslices;              // K slices of a sliced product
   const int32_t* seg_off;      // [S+1]
   const int32_t* seg_adapter;  // [S]

@@ -259,80 +259,67 @@ __device__ __forceinline__ void w16_tile(const W16TileArgs& a, W16Ring<BM, BN, N
   else stages(std::integral_constant<int, FM>{});
 
   lds_barrier();  // every wave is done with the ring
-  if (!active) return;
+  if (!kLora && !active) return;
   uint8_t* const stg = reinterpret_cast<uint8_t*>(&ring) + wave * 8192;
 
-  // adapters: for each segment with rows here, acc += low . lora_b^T over the rank, low
-  // (scaled, fp32) held as two bf16 terms (16 significant bits: the adapter's share keeps an
-  // error of 2^-16 of itself). 64 segments' bounds and adapters are read at once, and the
-  // operands of the next 16 ranks are loaded before the current ones are multiplied, so that
-  // many short segments cost their loads and not their latency.
-  if (kLora) {
-    int lo_l = 0, hi_l = 0, l_l = 0, k_next = a.rank;
-    int lo = 0, hi = 0, l = 0, sl = a.lslices;  // the segment (relative to rlo) and slice of low of the operands to load
-    unsigned long long mask = 0;
-    bool more = s0 < a.S;
-    auto advance = [&]() -> bool {  // the next 16 ranks: of the same slice, the segment's next slice, the next segment
-      k_next += 16;
-      if (k_next < a.rank) return true;
-      if (++sl < a.lslices) {
-        k_next = 0;
-        return true;
-      }
-      while (mask == 0) {
-        if (!more) return false;
-        const bool in = s0 + lane < a.S;
-        const int64_t b0 = seg_b0, b1 = seg_b1;
-        l_l = seg_ad;
-        lo_l = (int)(max(b0, rlo) - rlo);
-        hi_l = (int)(min(b1, rhi) - rlo);
-        mask = __ballot(in && b0 < rhi && b1 > rlo && hi_l > lo_l && l_l >= 0 && l_l < a.L);
-        more = s0 + 64 < a.S && __ballot(in && b0 >= rhi) == 0;
-        s0 += 64;
-        if (more) fetch_segments();
-      }
-      const int i = __ffsll((long long)mask) - 1;
-      mask &= mask - 1;
-      lo = __builtin_amdgcn_readlane(lo_l, i);
-      hi = __builtin_amdgcn_readlane(hi_l, i);
-      l = __builtin_amdgcn_readlane(l_l, i);
-      k_next = sl = 0;
-      return true;
-    };
-    struct Ops {
-      v4i h[2], lo[2], b[FN];
-      int first, end;  // the segment's rows
-    };
-    // per-lane byte offsets; the item adds scalars only (rows past N of lora_b read as zero)
-    uint32_t loff[2], boff_l[FN];
+  // adapters: for each segment with rows here, acc += low . lora_b^T over the rank, 32 ranks at a
+  // time. A row has one adapter, so the tile's low is read once: its K slices are added in fp32, and
+  // the sum t is split exactly into three bf16 terms t = x0 + x1 + x2, which the waves read from LDS
+  // as operands. Each term is the leading 8 bits of what the ones before leave, so of t's sign and
+  // never larger than t (rounded terms could overflow or differ in sign); an infinity is x0 alone.
+  // 64 segments' bounds and adapters are read at once, and the operands of D further items are
+  // loaded before the current ones are multiplied, so that many short segments cost their loads and
+  // not their latency.
+  if constexpr (kLora) {
+    uint8_t* const terms = reinterpret_cast<uint8_t*>(&ring) + NW * 8192;  // [3][BM rows][32 ranks] bf16
+    static_assert(sizeof(ring) >= NW * 8192 + 3 * BM * 64, "the terms stand behind the staging areas");
+    auto stage_terms = [&](int rc) {
+      constexpr int kSlicesMost = 4;  // of low
+#pragma unroll 1
+      for (int i = 0; i < BM * 4 / (NW * 64); ++i) {
+        const int idx = (int)threadIdx.x + NW * 64 * i, r = idx >> 2, c = idx & 3;  // 8 ranks of a row
+        float t[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        if (r < m && rc + 8 * c < a.rank) {
+          const float* const p = a.low + (row0 + r) * a.rank + rc + 8 * c;
+          float4 u[kSlicesMost][2];
 #pragma unroll
-    for (int fm = 0; fm < 2; ++fm) loff[fm] = (uint32_t)((32 * fm + r32) * a.rank + 8 * g) * 2;
+          for (int sl = 0; sl < kSlicesMost; ++sl)
+            if (sl < a.lslices) {
+              u[sl][0] = *reinterpret_cast<const float4*>(p + sl * a.R * a.rank);
+              u[sl][1] = *reinterpret_cast<const float4*>(p + sl * a.R * a.rank + 4);
+            }
 #pragma unroll
-    for (int f = 0; f < FN; ++f) boff_l[f] = (uint32_t)((n_tile * BN + brow_l[f]) * a.rank + 8 * g) * 2;
-    const uint32_t nrank = (uint32_t)N * (uint32_t)a.rank * 2, lrank = 64u * (uint32_t)a.rank * 2;
-    auto load = [&](Ops& o) {
-      const int64_t lat = ((int64_t)sl * a.R + rlo) * a.rank;
-      const buf_rsrc rh = make_rsrc(a.low_hi + lat, lrank), rl = make_rsrc(a.low_lo + lat, lrank);
-      const buf_rsrc rw = make_rsrc(a.lora_b + (int64_t)l * N * a.rank, nrank);
-      const uint32_t k2 = 2 * (uint32_t)k_next;
-      const bool kin = k_next + 8 * g < a.rank;  // the last 8 of a rank that is no multiple of 16
-      o.first = lo;
-      o.end = hi;
+          for (int sl = 0; sl < kSlicesMost; ++sl)
+            if (sl < a.lslices)
 #pragma unroll
-      for (int fm = 0; fm < 2; ++fm) {
-        const int t = 32 * fm + r32;
-        o.h[fm] = o.lo[fm] = v4i{};
-        if (t >= lo && t < hi && kin) {  // lanes that are off cost no address cycles
-          o.h[fm] = buf_load16(rh, loff[fm], k2);
-          o.lo[fm] = buf_load16(rl, loff[fm], k2);
+              for (int h = 0; h < 2; ++h)
+                t[4 * h] += u[sl][h].x, t[4 * h + 1] += u[sl][h].y, t[4 * h + 2] += u[sl][h].z, t[4 * h + 3] += u[sl][h].w;
+        }
+        uint32_t x[3][8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          x[0][k] = __float_as_uint(t[k]) & 0xFFFF0000u;
+          const float d = __builtin_isinf(t[k]) ? 0.0f : t[k] - __uint_as_float(x[0][k]);
+          x[1][k] = __float_as_uint(d) & 0xFFFF0000u;
+          x[2][k] = __float_as_uint(d - __uint_as_float(x[1][k]));
+        }
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+          v4i w;
+#pragma unroll
+          for (int h = 0; h < 4; ++h) w[h] = (int)(x[k][2 * h] >> 16 | (x[k][2 * h + 1] & 0xFFFF0000u));
+          *reinterpret_cast<v4i*>(terms + k * BM * 64 + r * 64 + 16 * (c ^ swz_b16(r))) = w;
         }
       }
-#pragma unroll
-      for (int f = 0; f < FN; ++f) {
-        o.b[f] = v4i{};
-        if (kin) o.b[f] = buf_load16(rw, boff_l[f], k2);
-      }
     };
+    struct Ops {
+      v4i b[FN];
+      int first, end, k;  // the segment's rows (relative to rlo), the first of 16 ranks
+    };
+    uint32_t boff_l[FN];  // per-lane byte offsets; the item adds scalars only (rows past N of lora_b read as zero)
+#pragma unroll
+    for (int f = 0; f < FN; ++f) boff_l[f] = (uint32_t)((n_tile * BN + brow_l[f]) * a.rank + 8 * g) * 2;
+    const uint32_t nrank = (uint32_t)N * (uint32_t)a.rank * 2;
     // an infinity or NaN of the adapter would reach the rows beside the segment (0 times it is NaN):
     // those rows' sums wait in LDS meanwhile
     auto spills = [&](const Ops& o) -> bool {
@@ -345,48 +332,106 @@ __device__ __forceinline__ void w16_tile(const W16TileArgs& a, W16Ring<BM, BN, N
       return __ballot((any & 0x80008000u) != 0) != 0;
     };
     float* const kept = reinterpret_cast<float*>(stg) + lane;
-    constexpr int D = FN == 1 ? 4 : 2;  // operands in flight
-    Ops o[D];
-    bool have[D];
-#pragma unroll
-    for (int d = 0; d < D; ++d) {
-      have[d] = advance();
-      if (have[d]) load(o[d]);
-    }
-    while (have[0]) {
-#pragma unroll
-      for (int d = 0; d < D; ++d) {
-        if (!have[d]) break;
-        const bool apart = __builtin_expect(spills(o[d]), 0);
+    constexpr int D = FN == 1 ? 4 : 2;  // items in flight
+    const int s_first = s0;
+    for (int rc = 0; rc < a.rank && a.S > 0; rc += 32) {
+      const int rc_end = min(rc + 32, a.rank);
+      int lo_l = 0, hi_l = 0, l_l = 0, k_next = rc_end;
+      int lo = 0, hi = 0, l = 0;  // the segment of the item to load
+      unsigned long long mask = 0;
+      s0 = s_first;
+      bool more = active && s0 < a.S;
+      if (rc > 0 && more) fetch_segments();
+      auto advance = [&]() -> bool {  // the next 16 ranks, else the next segment
+        k_next += 16;
+        if (k_next < rc_end) return true;
+        while (mask == 0) {
+          if (!more) return false;
+          const bool in = s0 + lane < a.S;
+          const int64_t b0 = seg_b0, b1 = seg_b1;
+          l_l = seg_ad;
+          lo_l = (int)(max(b0, rlo) - rlo);
+          hi_l = (int)(min(b1, rhi) - rlo);
+          mask = __ballot(in && b0 < rhi && b1 > rlo && hi_l > lo_l && l_l >= 0 && l_l < a.L);
+          more = s0 + 64 < a.S && __ballot(in && b0 >= rhi) == 0;
+          s0 += 64;
+          if (more) fetch_segments();
+        }
+        const int i = __ffsll((long long)mask) - 1;
+        mask &= mask - 1;
+        lo = __builtin_amdgcn_readlane(lo_l, i);
+        hi = __builtin_amdgcn_readlane(hi_l, i);
+        l = __builtin_amdgcn_readlane(l_l, i);
+        k_next = rc;
+        return true;
+      };
+      auto load = [&](Ops& o) {
+        const buf_rsrc rw = make_rsrc(a.lora_b + (int64_t)l * N * a.rank, nrank);
+        o.first = lo;
+        o.end = hi;
+        o.k = k_next;
+        const bool kin = k_next + 8 * g < a.rank;  // the last 8 of a rank that is no multiple of 16
 #pragma unroll
         for (int f = 0; f < FN; ++f) {
-          if (apart) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) kept[64 * i] = acc[i / 16][f][i % 16];
-            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-          }
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int fm = 0; fm < 2; ++fm)
-              acc[fm][f] = mfma32x32x16(__builtin_bit_cast(v8bf, o[d].b[f]),
-                                        __builtin_bit_cast(v8bf, h ? o[d].h[fm] : o[d].lo[fm]), acc[fm][f]);
-          if (apart) {
-#pragma unroll
-            for (int fm = 0; fm < 2; ++fm) {
-              const int t = 32 * fm + r32;
-              if (t < o[d].first || t >= o[d].end) {
-#pragma unroll
-                for (int i = 0; i < 16; ++i) acc[fm][f][i] = kept[64 * (16 * fm + i)];
-              }
-            }
-            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-          }
+          o.b[f] = v4i{};
+          if (kin) o.b[f] = buf_load16(rw, boff_l[f], 2 * (uint32_t)k_next);
         }
+      };
+      Ops o[D];
+      bool have[D];
+#pragma unroll
+      for (int d = 0; d < D; ++d) {
         have[d] = advance();
         if (have[d]) load(o[d]);
       }
+      if (rc > 0) lds_barrier();  // the terms before have been read
+      stage_terms(rc);
+      lds_barrier();
+      while (have[0]) {
+#pragma unroll
+        for (int d = 0; d < D; ++d) {
+          if (!have[d]) break;
+          const bool apart = __builtin_expect(spills(o[d]), 0);
+          v8bf x[2][3];
+#pragma unroll
+          for (int fm = 0; fm < 2; ++fm) {
+            const int t = 32 * fm + r32, r = WM * wm + t;
+            const uint8_t* const at = terms + r * 64 + 16 * ((((o[d].k - rc) >> 3) + g) ^ swz_b16(r));
+            const bool in = t >= o[d].first && t < o[d].end;
+#pragma unroll
+            for (int k = 0; k < 3; ++k)
+              x[fm][k] = __builtin_bit_cast(v8bf, in ? *reinterpret_cast<const v4i*>(at + k * BM * 64) : v4i{});
+          }
+#pragma unroll
+          for (int f = 0; f < FN; ++f) {
+            if (apart) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) kept[64 * i] = acc[i / 16][f][i % 16];
+              asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            }
+#pragma unroll
+            for (int k = 2; k >= 0; --k)
+#pragma unroll
+              for (int fm = 0; fm < 2; ++fm)
+                acc[fm][f] = mfma32x32x16(__builtin_bit_cast(v8bf, o[d].b[f]), x[fm][k], acc[fm][f]);
+            if (apart) {
+#pragma unroll
+              for (int fm = 0; fm < 2; ++fm) {
+                const int t = 32 * fm + r32;
+                if (t < o[d].first || t >= o[d].end) {
+#pragma unroll
+                  for (int i = 0; i < 16; ++i) acc[fm][f][i] = kept[64 * (16 * fm + i)];
+                }
+              }
+              asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            }
+          }
+          have[d] = advance();
+          if (have[d]) load(o[d]);
+        }
+      }
     }
+    if (!active) return;
   }
 
   // epilogue: 32 rows x CP columns at a time through the wave's 8 KB of the ring (runs of

@@ -176,3 +176,48 @@ def test_no_rows():
     c = ops.fp4_gemm_w4a16_lora(torch.empty(0, 512, dtype=torch.bfloat16, device="cuda"), w[0], s[0], z, z[:1], la, lb,
                                 scaling)
     assert c.shape == (0, 32)
+
+
+def single_terms(M, N, K, rank, seed, scaling):
+    """An adapter 0 whose first product is one term a row and nothing else, so that its fp32 value is known exactly:
+    low[t][0] = fp32(scaling * a[t][17] * lora_a[0][17]). Adapter 1 is all zeros."""
+    g = torch.Generator().manual_seed(seed)
+    a = bf16(seed, M, K)
+    la, lb = torch.zeros(2, rank, K, dtype=torch.bfloat16), torch.zeros(2, N, rank, dtype=torch.bfloat16)
+    la[0, 0, 17] = 1.3828125  # all eight bits of a bf16 in use
+    lb[0] = torch.randn(N, rank, generator=g).to(torch.bfloat16)
+    sc = torch.tensor([scaling, 1.0])
+    low = (a[:, 17].float() * la[0, 0, 17].float()) * sc[0]  # the product of two bf16 is exact in fp32
+    return a, la, lb, sc, low
+
+
+# sliced; 64 x 128 tiles; 128 x 256 tiles
+PATHS = [(9, 272, 512, 24), (777, 1520, 512, 24), (200, 4112, 512, 128), (4100, 4352, 512, 16)]
+
+
+@pytest.mark.parametrize("scaling", [1.1, -2.9e38])
+@pytest.mark.parametrize("M,N,K,rank", PATHS)
+def test_the_first_product_is_held_in_fp32(M, N, K, rank, scaling):
+    """With one term a row and a weight of next to nothing the result is low * B: low has 24 bits, B 8, and a path
+    that holds low in fp32 only rounds in the sums of the at most three products it may split that into (2^-23 each,
+    rounded or cut off) and, the weights' part being below 2^-23 of it, once more. The larger scaling makes some low
+    greater than the largest bf16 and others larger than the largest fp32."""
+    w, s, hat = weights(1, N, K, "mxfp4", 6)
+    s = (s - 118) // 6 + 2  # 2^-125 .. 2^-123
+    a, la, lb, sc, low = single_terms(M, N, K, rank, 2, scaling)
+    a[:, 17] = torch.linspace(0.06, 0.9, M).to(torch.bfloat16)
+    low = (a[:, 17].float() * la[0, 0, 17].float()) * sc[0]
+    edge = (low.abs() > torch.finfo(torch.bfloat16).max) & torch.isfinite(low)
+    if abs(scaling) > 2:
+        lb = (lb.float() * 2.0 ** -30).to(torch.bfloat16)
+        assert torch.isinf(low).any() and torch.isfinite(low).any()
+        if M > 4000:
+            assert edge.any()
+    got = ops.fp4_gemm_w4a16_lora(a.cuda(), w[0], s[0], torch.tensor([0, M], dtype=torch.int32).cuda(),
+                                  torch.zeros(1, dtype=torch.int32).cuda(), la.cuda(), lb.cuda(), sc.cuda()).cpu()
+    B = lb[0, :, 0].double()
+    want = low.double()[:, None] * B
+    fin = torch.isfinite(low)
+    err, lim = (got.double() - want).abs()[fin], (4 * 2.0 ** -23 * want.abs() + K * 2.0 ** -110)[fin]
+    assert (err <= lim).all(), f"{float((err / lim).max()):.3g} of its bound"
+    assert torch.equal(got[~fin].double(), want[~fin])
