@@ -320,10 +320,10 @@ __device__ __forceinline__ void w16_tile(const W16TileArgs& a, W16Ring<BM, BN, N
 #pragma unroll
     for (int f = 0; f < FN; ++f) boff_l[f] = (uint32_t)((n_tile * BN + brow_l[f]) * a.rank + 8 * g) * 2;
     const uint32_t nrank = (uint32_t)N * (uint32_t)a.rank * 2;
-    // an infinity or NaN of the adapter would reach the rows beside the segment (0 times it is NaN):
-    // those rows' sums wait in LDS meanwhile
-    auto spills = [&](const Ops& o) -> bool {
-      if (o.first <= 0 && o.end >= 64) return false;
+    // An infinity or NaN of lora_b meets x0 only, which is 0 only where t is (or below 2^-133; the
+    // other terms may be 0, and 0 times it is NaN); and it would reach the rows beside the segment:
+    // those rows' sums wait in LDS meanwhile.
+    auto not_finite = [&](const Ops& o) -> bool {
       uint32_t any = 0;  // exponents of all ones carry into the sign
 #pragma unroll
       for (int f = 0; f < FN; ++f)
@@ -391,7 +391,7 @@ __device__ __forceinline__ void w16_tile(const W16TileArgs& a, W16Ring<BM, BN, N
 #pragma unroll
         for (int d = 0; d < D; ++d) {
           if (!have[d]) break;
-          const bool apart = __builtin_expect(spills(o[d]), 0);
+          const bool odd = __builtin_expect(not_finite(o[d]), 0), apart = odd && (o[d].first > 0 || o[d].end < 64);
           v8bf x[2][3];
 #pragma unroll
           for (int fm = 0; fm < 2; ++fm) {
@@ -410,10 +410,18 @@ __device__ __forceinline__ void w16_tile(const W16TileArgs& a, W16Ring<BM, BN, N
               asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
             }
 #pragma unroll
-            for (int k = 2; k >= 0; --k)
+            for (int k = 2; k >= 0; --k) {
+              v4i b = o[d].b[f];
+              if (k > 0 && odd) {
 #pragma unroll
-              for (int fm = 0; fm < 2; ++fm)
-                acc[fm][f] = mfma32x32x16(__builtin_bit_cast(v8bf, o[d].b[f]), x[fm][k], acc[fm][f]);
+                for (int i = 0; i < 4; ++i) {
+                  if ((b[i] & 0x7F80) == 0x7F80) b[i] &= (int)0xFFFF0000u;
+                  if ((b[i] & 0x7F800000) == 0x7F800000) b[i] &= 0xFFFF;
+                }
+              }
+#pragma unroll
+              for (int fm = 0; fm < 2; ++fm) acc[fm][f] = mfma32x32x16(__builtin_bit_cast(v8bf, b), x[fm][k], acc[fm][f]);
+            }
             if (apart) {
 #pragma unroll
               for (int fm = 0; fm < 2; ++fm) {

@@ -221,3 +221,28 @@ def test_the_first_product_is_held_in_fp32(M, N, K, rank, scaling):
     err, lim = (got.double() - want).abs()[fin], (4 * 2.0 ** -23 * want.abs() + K * 2.0 ** -110)[fin]
     assert (err <= lim).all(), f"{float((err / lim).max()):.3g} of its bound"
     assert torch.equal(got[~fin].double(), want[~fin])
+
+
+@pytest.mark.parametrize("whole", [True, False])
+@pytest.mark.parametrize("bad", [float("inf"), float("-inf")])
+@pytest.mark.parametrize("M,N,K,rank", PATHS)
+def test_an_infinite_second_factor_gives_signed_infinities(M, N, K, rank, bad, whole):
+    """low * B with B infinite is the infinity of their signs, whatever the bits of low, and NaN where low is 0; the
+    same in every path, in segments that fill tiles and in ones that do not."""
+    w, s, _ = weights(1, N, K, "mxfp4", 6)
+    a, la, lb, sc, low = single_terms(M, N, K, rank, 2, 1.1)
+    a[M // 2], low[M // 2] = 0, 0
+    assert (low != 0).sum() == M - 1
+    lo, hi = (0, M) if whole else (M // 3, M - 2)
+    args = (torch.tensor([0, lo, hi, M], dtype=torch.int32).cuda(), torch.tensor([1, 0, 1], dtype=torch.int32).cuda(),
+            la.cuda())
+    plain = ops.fp4_gemm_w4a16_lora(a.cuda(), w[0], s[0], *args, lb.cuda(), sc.cuda())
+    cols = [5, N - 1]
+    lb[0, cols, 0] = bad
+    got = ops.fp4_gemm_w4a16_lora(a.cuda(), w[0], s[0], *args, lb.cuda(), sc.cuda()).cpu()
+    want = plain.cpu().clone()
+    for c in cols:
+        want[lo:hi, c] = low[lo:hi] * bad
+    assert torch.equal(torch.isnan(got), torch.isnan(want)) and int(torch.isnan(want).sum()) == len(cols)
+    assert torch.equal(got.nan_to_num(7.0, posinf=float("inf"), neginf=float("-inf")),
+                       want.nan_to_num(7.0, posinf=float("inf"), neginf=float("-inf")))
