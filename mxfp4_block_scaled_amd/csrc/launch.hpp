@@ -75,7 +75,7 @@ int lora_shrink_slices(int64_t M, int64_t N, int64_t K, int rank);
 int lora_base_slices(int64_t M, int64_t N, int64_t K, int rank);
 int launch_w16_lora(const W16LoraArgs& a, bool nvfp4, bool out_bf16, hipStream_t stream);
 
-// post-norm, gate, residual, pre-norm and quantisation of a block's output (block_norm.hip)
+// post-norm, gate, residual, pre-norm and quantisation of a block's output (block_norm.hpp)
 enum { kGateNone = 0, kGateChannel = 1, kGateToken = 2, kGateFull = 3 };
 struct BlockNormArgs {
   const void* y;                // [T][H], or with topk > 0 [y_rows][H]
@@ -90,6 +90,7 @@ struct BlockNormArgs {
   bool x_bf16, weight_bf16, gate_bf16, n_bf16, q_fp4;
 };
 int launch_block_norm(const BlockNormArgs& a, bool y_bf16, hipStream_t stream);
+void launch_block_norm_f32(const BlockNormArgs& a, hipStream_t stream);
 
 // the lookup-table route (gemm_q8.hip): Q8 activations and int8-expanded MXFP4 weights
 int launch_q8_quantize(const uint16_t* x, int64_t rows, int64_t K, int8_t* q, uint16_t* d, hipStream_t stream);

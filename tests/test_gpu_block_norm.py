@@ -198,3 +198,60 @@ def test_without_weights():
 def test_no_rows():
     got = ops.moe_block_norm(torch.empty(0, 64, dtype=BF, device="cuda"))
     assert got["r"].shape == (0, 64) and got["n"].shape == (0, 64)
+
+
+@pytest.mark.parametrize("H", [512, 2048, 7168, 16416, 40000])  # one, two, four and eight chunks a thread
+@pytest.mark.parametrize("yd", [BF, F32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("topk", range(1, 9))
+def test_every_number_of_combined_rows(topk, yd, H):
+    """1 to 8 expert rows a token, a dropped pair and a token without any row among them; the combine alone has the
+    bits of moe_unpermute_combine."""
+    T = 300 if H < 7168 else 5
+    i = inputs(T, H, topk, True, "channel", BF, yd, F32, topk * H)
+    pair = i["pair"].clone()
+    pair[topk - 1], pair[2 * topk:3 * topk] = -1, T * topk
+    got = ops.moe_block_norm(cu(i["y"]), x=cu(i["x"]), post_weight=cu(i["post"]), gate=cu(i["gate"]),
+                             residual_scale=0.75, pre_weight=cu(i["pre"]), eps=EPS, n_dtype=F32,
+                             expert_gates=cu(i["gates"]), pair_row=cu(pair))
+    r, dr, n, dn = reference(i["y"], i["x"], i["post"], i["gate"], 0.75, i["pre"], i["gates"], pair)
+    close(got["r"], r, dr, "r")
+    close(got["n"], n, dn, "n")
+    alone = ops.moe_block_norm(cu(i["y"]), want_n=False, r_dtype=F32, expert_gates=cu(i["gates"]), pair_row=cu(i["pair"]))
+    want = ops.moe_unpermute_combine(cu(i["y"]), cu(i["gates"]), cu(i["pair"]), T, topk, F32)
+    assert torch.equal(alone["r"], want)
+
+
+@pytest.mark.parametrize("topk,yd", [(3, BF), (8, BF), (7, F32)], ids=["3-bf16", "8-bf16", "7-fp32"])
+def test_large_combined_batches_are_their_parts(topk, yd):
+    T, H = 4224, 8064
+    i = {k: cu(v) for k, v in inputs(T, H, topk, True, None, BF, yd, F32, 31).items()}
+    whole = ops.moe_block_norm(i["y"], x=i["x"], post_weight=i["post"], pre_weight=i["pre"], act_fmt="e4m3",
+                               expert_gates=i["gates"], pair_row=i["pair"])
+    for at in range(0, T, 1056):
+        rows = slice(at, at + 1056)
+        got = ops.moe_block_norm(i["y"], x=i["x"][rows], post_weight=i["post"], pre_weight=i["pre"], act_fmt="e4m3",
+                                 expert_gates=i["gates"][rows].contiguous(),
+                                 pair_row=i["pair"][at * topk:(at + 1056) * topk])
+        for k, v in got.items():
+            assert torch.equal(v, whole[k][rows]), k
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("topk", [1, 2, 6, 8])
+def test_dropped_pairs_take_nothing_from_any_row(topk, bad):
+    """A dropped pair adds nothing, whatever its gate and the rows of y hold."""
+    T, H = 4, 512
+    i = inputs(T, H, topk, False, None, BF, BF, F32, 40 + topk)
+    pair = i["pair"].clone()
+    pair[::topk] = torch.tensor([-1, T * topk, -5, 2 ** 31 - 1], dtype=torch.int32)
+    used = {int(p) for p in pair if 0 <= p < T * topk}
+    free = [r for r in range(T * topk) if r not in used]
+    i["y"][free] = bad
+    i["gates"][:, 0] = bad
+    got = ops.moe_block_norm(cu(i["y"]), x=cu(i["x"]), pre_weight=cu(i["pre"]), eps=EPS, expert_gates=cu(i["gates"]),
+                             pair_row=cu(pair))
+    clean_y, clean_g = i["y"].clone(), i["gates"].clone()
+    clean_y[free], clean_g[:, 0] = 0, 0
+    r, dr, n, dn = reference(clean_y, i["x"], None, None, 1.0, i["pre"], clean_g, pair)
+    close(got["r"], r, dr, "r")
+    close(got["n"], n, dn, "n")
