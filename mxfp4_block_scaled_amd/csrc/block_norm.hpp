@@ -113,6 +113,7 @@ __device__ __forceinline__ float block_sum(float v, float* part) {
 }
 
 constexpr int64_t kFewRows = 256;
+constexpr int64_t kMaxThreads = (int64_t(1) << 32) - 1;  // of a launch: the runtime counts them in 32 bits
 constexpr int64_t kOnce = int64_t(1) << 25;  // elements of a batch that the caches do not hold (64 MB in bf16)
 
 // KT rows of y per token, 0: no combine. The rows' loads are in flight together (of rows wider than
@@ -120,7 +121,7 @@ constexpr int64_t kOnce = int64_t(1) << 25;  // elements of a batch that the cac
 template <bool kYBF16, int KT, int C, bool kNT>
 __global__ void __launch_bounds__(1024) block_norm_kernel(BlockNormArgs a) {
   __shared__ float part[2][16];
-  const int64_t t = blockIdx.x;
+  const int64_t t = a.t0 + blockIdx.x;
   const int64_t H = a.H;
   const int tid = threadIdx.x, nt = blockDim.x;
   float v[C][8];
@@ -275,16 +276,20 @@ __global__ void __launch_bounds__(1024) block_norm_kernel(BlockNormArgs a) {
 }
 
 template <bool kYBF16, int KT, bool kNT>
-void launch_c(const BlockNormArgs& a, hipStream_t stream) {
+void launch_c(BlockNormArgs a, hipStream_t stream) {
   // chunks of 8 columns per thread: one for few rows (the fewest steps of a row's latency), else
   // two while 1024 threads hold the row, more beyond
   const int64_t chunks = a.H / 8;
   const int C = chunks <= (a.T <= kFewRows ? 1024 : 64) ? 1 : chunks <= 2048 ? 2 : chunks <= 4096 ? 4 : 8;
-  const dim3 grid((unsigned)a.T), block((unsigned)(cdiv(cdiv(chunks, C), 64) * 64));
-  if (C == 1) block_norm_kernel<kYBF16, KT, 1, kNT><<<grid, block, 0, stream>>>(a);
-  else if (C == 2) block_norm_kernel<kYBF16, KT, 2, kNT><<<grid, block, 0, stream>>>(a);
-  else if (C == 4) block_norm_kernel<kYBF16, KT, 4, kNT><<<grid, block, 0, stream>>>(a);
-  else block_norm_kernel<kYBF16, KT, 8, kNT><<<grid, block, 0, stream>>>(a);
+  const dim3 block((unsigned)(cdiv(cdiv(chunks, C), 64) * 64));
+  const int64_t most = kMaxThreads / block.x;  // rows of a launch
+  for (a.t0 = 0; a.t0 < a.T; a.t0 += most) {
+    const dim3 grid((unsigned)(a.T - a.t0 < most ? a.T - a.t0 : most));
+    if (C == 1) block_norm_kernel<kYBF16, KT, 1, kNT><<<grid, block, 0, stream>>>(a);
+    else if (C == 2) block_norm_kernel<kYBF16, KT, 2, kNT><<<grid, block, 0, stream>>>(a);
+    else if (C == 4) block_norm_kernel<kYBF16, KT, 4, kNT><<<grid, block, 0, stream>>>(a);
+    else block_norm_kernel<kYBF16, KT, 8, kNT><<<grid, block, 0, stream>>>(a);
+  }
 }
 
 template <bool kYBF16, int KT>

@@ -85,6 +85,7 @@ struct BlockNormArgs {
   void *r, *n;
   uint8_t *q, *q_scale;
   int64_t T, H, y_rows;
+  int64_t t0;                   // the launch's first row
   float residual_scale, eps;
   int topk, gate_mode;
   bool x_bf16, weight_bf16, gate_bf16, n_bf16, q_fp4;

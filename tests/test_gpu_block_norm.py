@@ -255,3 +255,21 @@ def test_dropped_pairs_take_nothing_from_any_row(topk, bad):
     r, dr, n, dn = reference(clean_y, i["x"], None, None, 1.0, i["pre"], clean_g, pair)
     close(got["r"], r, dr, "r")
     close(got["n"], n, dn, "n")
+
+
+@pytest.mark.parametrize("T", [2 ** 26 - 1, 2 ** 26, 2 ** 26 + 3])
+def test_more_threads_than_32_bits(T):
+    """A wave a token: up to 2^32 threads and more in one call. Every row, operand and result of it is the row's own."""
+    H = 32
+    y = torch.randn(7, H, generator=torch.Generator().manual_seed(1)).to(BF).cuda()
+    t = torch.arange(T, device="cuda")
+    args = dict(x=((t % 11).to(BF)[:, None] + torch.arange(H, device="cuda").to(BF)).contiguous(),
+                gate=(1 + t % 3).to(BF)[:, None].contiguous(), expert_gates=(1 + t % 5).float().view(T, 1),
+                pair_row=(t % 7).to(torch.int32))
+    r = torch.full((T, H), float("nan"), dtype=BF, device="cuda")
+    got = ops.moe_block_norm(y, act_fmt="e2m1", r=r, **args)
+    for rows in (slice(0, 5000), slice(2 ** 26 - 5000, 2 ** 26), slice(T - 5000, T)):
+        want = ops.moe_block_norm(y, act_fmt="e2m1", **{k: v[rows].clone() for k, v in args.items()})
+        for k, v in want.items():
+            assert torch.equal(got[k][rows], v), k
+    assert torch.isfinite(r[::4096]).all()
