@@ -296,8 +296,8 @@ int moe_grouped_gemm_w4a16(const uint16_t* a, int64_t a_rows, int64_t R, const i
 
 size_t fp4_w4a16_lora_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t rank) {
   if (M <= 0 || N <= 0 || K <= 0 || rank <= 0) return 0;
-  const size_t base = (size_t)mxf::lora_base_slices(M, N, K, rank) * (size_t)M * (size_t)N;
-  const size_t low = (size_t)mxf::lora_shrink_slices(M, N, K, rank) * (size_t)M * (size_t)rank;
+  const size_t base = (size_t)mxf::w16_lora_base_slices(M, N, K, rank) * (size_t)M * (size_t)N;
+  const size_t low = (size_t)mxf::w16_lora_low_slices(M, N, K, rank) * (size_t)M * (size_t)rank;
   return round_up((base + low) * sizeof(float), 256);
 }
 
@@ -369,6 +369,25 @@ int moe_block_norm(const void* y, int y_dtype, int64_t y_rows, const float* expe
   b.n_bf16 = n_dtype == MXF_BF16;
   b.q_fp4 = fmt == MXF_E2M1;
   return mxf::launch_block_norm(b, y_dtype == MXF_BF16, as_stream(stream)) ? MXF_ERR_LAUNCH : MXF_OK;
+}
+
+// The kernels that a call of these sizes runs, as the launcher has them (for tests and profiles):
+// per launch its rows and weight rows a workgroup, the experts' rows it is for, workgroups
+int mxf_w16_grouped_plan(int64_t R, int32_t E, int64_t N, int64_t K, int swiglu, int64_t* out) {
+  mxf::W16Launch l[3];
+  const int n = mxf::w16_grouped_plan(R, E, N, K, swiglu != 0, l);
+  for (int i = 0; i < n; ++i) {
+    const int64_t v[5] = {l[i].bm, l[i].bn, l[i].min_rows, l[i].max_rows, l[i].workgroups()};
+    for (int j = 0; j < 5; ++j) out[5 * i + j] = v[j];
+  }
+  return n;
+}
+
+int mxf_w16_lora_plan(int64_t M, int64_t N, int64_t K, int32_t rank, int64_t S, int32_t* out) {
+  const mxf::W16LoraPlan p = mxf::w16_lora_plan(M, N, K, rank, S);
+  const int32_t v[6] = {p.base_slices, p.low_slices, p.low_rows, p.low_share, p.bm, p.bn};
+  for (int j = 0; j < 6; ++j) out[j] = v[j];
+  return 6;
 }
 
 }  // extern "C"

@@ -56,10 +56,10 @@ int launch_w4a16_gemm(bool nvfp4, const uint16_t* a, int64_t M, int64_t N, int64
 
 // ragged grouped products of bf16 activations and FP4 expert weights (w4a16_grouped.hip)
 struct W16TileArgs;
-int launch_w16_grouped(W16TileArgs a, bool nvfp4, bool swiglu, bool out_bf16, hipStream_t stream);
+int launch_w16_grouped(const W16TileArgs& a, bool nvfp4, bool swiglu, bool out_bf16, hipStream_t stream);
 
 // a shared FP4 projection with low-rank adapters (w4a16_lora.hip); the workspace holds
-// lora_base_slices x M x N (0 slices: none) and lora_shrink_slices x M x rank fp32
+// w16_lora_base_slices x M x N (0 slices: none) and w16_lora_low_slices x M x rank fp32
 struct W16LoraArgs {
   const uint16_t* a;
   const uint8_t *w, *ws;
@@ -71,8 +71,6 @@ struct W16LoraArgs {
   int64_t M, N, K;
   int rank, L, S;
 };
-int lora_shrink_slices(int64_t M, int64_t N, int64_t K, int rank);
-int lora_base_slices(int64_t M, int64_t N, int64_t K, int rank);
 int launch_w16_lora(const W16LoraArgs& a, bool nvfp4, bool out_bf16, hipStream_t stream);
 
 // post-norm, gate, residual, pre-norm and quantisation of a block's output (block_norm.hpp)

@@ -200,64 +200,30 @@ void launch_stream_t(const W16TileArgs& a, bool out_bf16, dim3 grid, hipStream_t
 }
 
 template <int kSub>
-void launch_stream_s(W16TileArgs a, bool nv, bool swiglu, bool out_bf16, int64_t units, hipStream_t stream) {
-  a.ntiles = (int)cdiv(a.N, 64 * kSub);
-  const dim3 grid((unsigned)(8 * cdiv(units * a.ntiles, 8)));
+void launch_stream_s(const W16TileArgs& a, bool nv, bool swiglu, bool out_bf16, dim3 grid, hipStream_t stream) {
   if (nv && swiglu) launch_stream_t<true, true, kSub>(a, out_bf16, grid, stream);
   else if (nv) launch_stream_t<true, false, kSub>(a, out_bf16, grid, stream);
   else if (swiglu) launch_stream_t<false, true, kSub>(a, out_bf16, grid, stream);
   else launch_stream_t<false, false, kSub>(a, out_bf16, grid, stream);
 }
 
-// A short K (at most one super-step a wave) leaves a workgroup little between its lookup and its
-// sums: where there are many, each takes four runs of 64 weight rows (7168 x 2048, 384 rows over 256
-// experts: 276 -> 259 us); a longer K loses by it (4096 x 7168, 48 rows: 112 -> 120 us).
-void launch_stream(const W16TileArgs& a, bool nv, bool swiglu, bool out_bf16, int64_t units, hipStream_t stream) {
-  if (a.K <= 2048 && units * cdiv(a.N, 64) >= 8192) launch_stream_s<4>(a, nv, swiglu, out_bf16, units, stream);
-  else launch_stream_s<1>(a, nv, swiglu, out_bf16, units, stream);
+void launch_stream(W16TileArgs a, bool nv, bool swiglu, bool out_bf16, const W16Launch& l, hipStream_t stream) {
+  a.min_rows = l.min_rows;
+  a.max_rows = l.max_rows;
+  a.ntiles = (int)l.ntiles;
+  const dim3 grid((unsigned)l.workgroups());
+  if (l.bn == 256) launch_stream_s<4>(a, nv, swiglu, out_bf16, grid, stream);
+  else launch_stream_s<1>(a, nv, swiglu, out_bf16, grid, stream);
 }
-
-// units that experts of lo < rows <= hi can make of R rows in all
-int64_t most_units(int64_t R, int E, int64_t lo, int bm) {
-  const int64_t experts = R / (lo + 1) < E ? R / (lo + 1) : E;
-  return bm == 0 ? experts : experts + R / bm;
-}
-
-// Which kernels a call runs; what the experts hold is on the device, so by bounds on it.
-// Measured in us (8 experts: rows in all; streamed | 64 x 128 | 64 x 256 | 128 x 256 tiles):
-//   2048 x 2048, 512 rows   18 | 20 | 24 | 33     4 experts 4096 x 7168, 512 rows   90 | 59 | 65 | 96
-//                1024       28 | 23 | 25 | 34                            2048      351 | 144 | 155 | 154
-//                6000      139 | 60 | 56 | 57                            6000      977 | 411 | 354 | 308
-// The streaming kernel's time grows with workgroups x K (5 us a million) and needs one launch;
-// a tiled launch lasts at least its K chain (0.36 us for 64 k of 64 x 128 tiles).
-bool streams_all(int64_t R, int64_t workgroups, int64_t K) { return R <= 128 || workgroups <= 1100 + 600000 / K; }
 
 }  // namespace
 
-int launch_w16_grouped(W16TileArgs a, bool nv, bool swiglu, bool out_bf16, hipStream_t stream) {
-  constexpr int kAll = 0x7FFFFFFF;
-  const int64_t R = a.R;
-  const bool all = streams_all(R, most_units(R, a.E, 0, 16) * cdiv(a.N, 64), a.K);
-  a.min_rows = 0;
-  a.max_rows = all ? kAll : 16;  // units of 16 rows read an expert's weights again from the cache
-  launch_stream(a, nv, swiglu, out_bf16, most_units(R, a.E, 0, all ? 16 : 0), stream);
-  if (!all) {
-    const int64_t nt = cdiv(a.N, 256), w128 = most_units(R, a.E, 16, 128) * nt;
-    a.min_rows = 16;
-    if (w128 < 1024) {  // few tiles: one tiled launch, of the shape that keeps the chip busy
-      const W16Shape shape = R >= 96 * (int64_t)a.E && w128 >= 384              ? W16Shape::k128x256
-                             : !swiglu && most_units(R, a.E, 16, 64) * nt < 600 ? W16Shape::k64x128
-                                                                                : W16Shape::k64x256;
-      a.max_rows = kAll;
-      launch_w16_tile_grouped(a, nv, swiglu, out_bf16, shape, most_units(R, a.E, 16, shape == W16Shape::k128x256 ? 128 : 64),
-                              stream);
-    } else {  // a large call, perhaps a skewed one: by the expert's own rows
-      a.max_rows = 64;
-      launch_w16_tile_grouped(a, nv, swiglu, out_bf16, W16Shape::k64x256, most_units(R, a.E, 16, 0), stream);
-      a.min_rows = 64;
-      a.max_rows = kAll;
-      launch_w16_tile_grouped(a, nv, swiglu, out_bf16, W16Shape::k128x256, most_units(R, a.E, 64, 128), stream);
-    }
+int launch_w16_grouped(const W16TileArgs& a, bool nv, bool swiglu, bool out_bf16, hipStream_t stream) {
+  W16Launch l[3];
+  const int n = w16_grouped_plan(a.R, a.E, a.N, a.K, swiglu, l);
+  for (int i = 0; i < n; ++i) {
+    if (l[i].bm == 16) launch_stream(a, nv, swiglu, out_bf16, l[i], stream);
+    else launch_w16_tile_grouped(a, nv, swiglu, out_bf16, l[i], stream);
   }
   return hipGetLastError() == hipSuccess ? 0 : -1;
 }

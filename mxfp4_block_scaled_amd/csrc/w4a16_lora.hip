@@ -166,22 +166,11 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) l
   }
 }
 
-// Rows of a workgroup of the shrink (not sliced): 32 where segments are long, so that an adapter is
-// read for twice the rows
-bool shrink_wide(int64_t M, int64_t S) { return M >= 32 * S; }
-
 template <int RF>
-void launch_shrink(const ShrinkArgs& s, hipStream_t stream) {
-  const bool wide = shrink_wide(s.M, s.S);
-  const int64_t blocks = cdiv(s.M, wide ? 32 : 16);
-  ShrinkArgs a = s;
-  a.zsplit = (int)(cdiv(s.S, blocks) < 16 ? cdiv(s.S, blocks) : 16);
-  // long segments: a block over the end of one has a second workgroup on the same compute unit
-  // instead of twice the time (4096 x 4096 x 7168, 16 segments, 8 waves each: 250 -> 246 us)
-  if (wide && s.S > 1 && a.zsplit < 2) a.zsplit = 2;
-  const dim3 grid((unsigned)(8 * cdiv(blocks, 8)), (unsigned)a.slices, (unsigned)a.zsplit);
+void launch_shrink(const ShrinkArgs& a, int rows, hipStream_t stream) {
+  const dim3 grid((unsigned)(8 * cdiv(cdiv(a.M, rows), 8)), (unsigned)a.slices, (unsigned)a.zsplit);
   constexpr int NW = RF == 8 ? 8 : 16;  // what fits the registers
-  if (wide) lora_shrink_kernel<2, RF, 8><<<grid, 512, 0, stream>>>(a);
+  if (rows == 32) lora_shrink_kernel<2, RF, 8><<<grid, 512, 0, stream>>>(a);
   else lora_shrink_kernel<1, RF, NW><<<grid, NW * 64, 0, stream>>>(a);
 }
 
@@ -203,8 +192,6 @@ struct FinishArgs {
   int64_t M, N;
   int bslices, lslices, rank, L, S;
 };
-
-constexpr int kMaxBaseSlices = 8, kMaxLowSlices = 16;
 
 // One row, 256 columns per workgroup of one wave: 4 columns per lane. Latency bound (a chain of
 // segment lookup, low, sum over the rank): about 5 of the 18 us of 64 requests at 4096 x 7168.
@@ -276,43 +263,13 @@ __global__ void __launch_bounds__(64) lora_finish_kernel(FinishArgs p) {
 
 }  // namespace
 
-namespace {
-
-// Fewer than 256 tiles of 64 x 128, where the pass over the rows does not read lora_b too often
-// (N x rank for each row, from the cache)
-bool sliced(int64_t M, int64_t N, int rank) {
-  return M <= 64 || (cdiv(M, 64) * cdiv(N, 128) < 256 && M * N * rank <= (int64_t(1) << 26));
-}
-
-int clamp_slices(int64_t want, int64_t most) { return (int)(want < most ? (want > 1 ? want : 1) : (most > 1 ? most : 1)); }
-
-}  // namespace
-
-int lora_shrink_slices(int64_t M, int64_t N, int64_t K, int rank) {
-  // sliced: K slices of at least 256 (64 for each of a workgroup's 4 waves), as many as fit the
-  // compute units beside the projection's tiles. Else, with blocks of 32 rows, about a workgroup
-  // a compute unit, each slice of at least 1024
-  if (sliced(M, N, rank)) return clamp_slices(512 / cdiv(M, 16), K / 256 < kMaxLowSlices ? K / 256 : kMaxLowSlices);
-  return clamp_slices(256 / cdiv(M, 32), K / 1024 < 4 ? K / 1024 : 4);
-}
-
-int lora_base_slices(int64_t M, int64_t N, int64_t K, int rank) {
-  // K slices of at least 256 for two workgroups a compute unit
-  if (!sliced(M, N, rank)) return 0;
-  return clamp_slices(512 / (cdiv(M, 64) * cdiv(N, 128)), K / 256 < kMaxBaseSlices ? K / 256 : kMaxBaseSlices);
-}
-
 int launch_w16_lora(const W16LoraArgs& p, bool nv, bool out_bf16, hipStream_t stream) {
-  const int bs = lora_base_slices(p.M, p.N, p.K, p.rank);
-  int ls = lora_shrink_slices(p.M, p.N, p.K, p.rank);
-  if (bs == 0 && !shrink_wide(p.M, p.S)) ls = 1;  // short segments: every slice is another pass over their adapters
+  const W16LoraPlan l = w16_lora_plan(p.M, p.N, p.K, p.rank, p.S);
+  const int bs = l.base_slices, ls = l.low_slices;
   float* const base = p.workspace;
   float* const low = base + (int64_t)bs * p.M * p.N;
-  const int64_t blocks = cdiv(p.M, 16), per_block = cdiv(p.S, blocks);
-  const int z = (int)(per_block < 1 ? 1 : per_block < 16 ? per_block : 16);
-  // what fits the compute units beside the projection's tiles
-  if (bs > 0 && ls > 512 / (blocks * z)) ls = (int)(512 / (blocks * z) > 1 ? 512 / (blocks * z) : 1);
-  const ShrinkArgs s{p.a, p.lora_a, p.scaling, p.seg_off, p.seg_adapter, low, p.M, p.K, p.rank, p.L, p.S, z, ls};
+  const ShrinkArgs s{p.a, p.lora_a, p.scaling, p.seg_off, p.seg_adapter, low, p.M, p.K, p.rank, p.L, p.S, l.low_share,
+                     ls};
   W16TileArgs a{};
   a.a = p.a;
   a.a_rows = a.R = p.M;
@@ -333,12 +290,12 @@ int launch_w16_lora(const W16LoraArgs& p, bool nv, bool out_bf16, hipStream_t st
   a.lora_b = p.lora_b;
   if (bs == 0) {
     if (p.S > 0) {
-      if (p.rank <= 16) launch_shrink<1>(s, stream);
-      else if (p.rank <= 32) launch_shrink<2>(s, stream);
-      else if (p.rank <= 64) launch_shrink<4>(s, stream);
-      else launch_shrink<8>(s, stream);
+      if (p.rank <= 16) launch_shrink<1>(s, l.low_rows, stream);
+      else if (p.rank <= 32) launch_shrink<2>(s, l.low_rows, stream);
+      else if (p.rank <= 64) launch_shrink<4>(s, l.low_rows, stream);
+      else launch_shrink<8>(s, l.low_rows, stream);
     }
-    launch_w16_tile_lora(a, nv, out_bf16, stream);
+    launch_w16_tile_lora(a, nv, out_bf16, l, stream);
   } else {
     a.out = base;
     a.ntiles = (int)cdiv(p.N, 128);

@@ -48,9 +48,6 @@ struct alignas(16) W16Ring {
   uint8_t S[2][BN * 16];
 };
 
-__device__ __forceinline__ int swz_a16(int r) { return (r & 7) ^ ((r >> 3) & 1); }  // 8 chunks per row
-__device__ __forceinline__ int swz_b16(int r) { return (r >> 2) & 3; }              // 4 chunks per row
-
 __device__ __forceinline__ v16f mfma32x32x16(v8bf a, v8bf b, v16f c) {
 #if defined(__HIP_DEVICE_COMPILE__)
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
@@ -88,8 +85,8 @@ __device__ __forceinline__ void w16_tile(const W16TileArgs& a, W16Ring<BM, BN, N
       if (!w16_item<BM>(a.offsets, a.E, a.R, a.min_rows, a.max_rows, a.ntiles, x, j, e, n_tile, row0, m)) return;
     } else {  // 8 contiguous ranges of items, one per XCD
       const uint32_t units = (uint32_t)((a.R + BM - 1) / BM), total = units * (uint32_t)a.ntiles;
-      const uint32_t w = w16_eighths(total, x) + (uint32_t)j;
-      if (w >= w16_eighths(total, x + 1)) return;
+      uint32_t w;
+      if (!w16_range(total, x, j, w)) return;
       int unit;
       w16_place(w, units, (uint32_t)a.ntiles, n_tile, unit);
       row0 = (int64_t)unit * BM;
@@ -106,11 +103,7 @@ __device__ __forceinline__ void w16_tile(const W16TileArgs& a, W16Ring<BM, BN, N
   const buf_rsrc rb = make_rsrc(a.w + (int64_t)e * N * wrow, (uint32_t)(N * wrow));
   const buf_rsrc rbs = make_rsrc(a.ws + (int64_t)e * N * srow, (uint32_t)(N * srow));
 
-  // the weight row that tile row r holds (N and beyond: reads as zero)
-  auto b_row = [&](int r) -> int64_t {
-    if (kSwiglu) return (r < BN / 2 ? 0 : half - BN / 2) + (int64_t)n_tile * (BN / 2) + r;
-    return (int64_t)n_tile * BN + r;
-  };
+  auto b_row = [&](int r) -> int64_t { return w16_weight_row(kSwiglu, BN, half, n_tile, r); };
   uint32_t va[IA], vb[IB];
 #pragma unroll
   for (int q = 0; q < IB; ++q) {
@@ -222,29 +215,21 @@ __device__ __forceinline__ void w16_tile(const W16TileArgs& a, W16Ring<BM, BN, N
   const bool active = WM * wm < m;
   // stage st: wait for the copies it needs, meet the other waves (their parts have landed
   // too, and everyone is done with stage st - 1), issue into what stage st - 1 freed, compute.
-  // Issue order at stage t: on even t the codes of stages t + 2, t + 3 and, where a scale
-  // group begins, the next group, then the activations of t + NA - 1. So with NA == 3 only the last
-  // stage's issues may stay in flight: A, and after an even stage B (and S) before it.
-  auto next_s = [&](int st) { return (st % P == 0 || (kSlices && st == st0)) && (st / P + 1) * P < nst; };
+  // Order, slots and counts: w4a16_plan.hpp.
+  auto next_s = [&](int st) { return w16_begins_scales(st, kSlices ? st0 : 0, P, nst); };
   auto step = [&](auto I, auto Rows, int st) {
     constexpr int i = decltype(I)::value;  // of the slots: st - st0 modulo whole turns
-    if (NA == 2 || st + 1 >= nst) {
-      wait_vmcnt<0>();
-    } else if (i % 2 == 0) {
-      wait_vmcnt<IA>();
-    } else if (has_sc && next_s(st - 1)) {
-      wait_vmcnt<IA + IB + 1>();
-    } else {
-      wait_vmcnt<IA + IB>();
-    }
+    if (st + 1 >= nst) wait_vmcnt<w16_in_flight(i, NA, IA, IB, true, false)>();
+    else if (i % 2 == 1 && has_sc && next_s(st - 1)) wait_vmcnt<w16_in_flight(i, NA, IA, IB, false, true)>();
+    else wait_vmcnt<w16_in_flight(i, NA, IA, IB, false, false)>();
     lds_barrier();
-    if (i % 2 == 0 && st + 2 < nst) issue_b(ring.B[(i / 2 + 1) % 2], st / 2 + 1);
+    if (w16_issues_codes(i, st, nst)) issue_b(ring.B[w16_code_slot(i + 2)], st / 2 + 1);
     if (i % 2 == 0 && next_s(st)) issue_s(st / P + 1);
-    if (st + NA - 1 < nst) issue_a(ring.A[(i + NA - 1) % NA], st + NA - 1);
+    if (w16_issues_a(st, NA, nst)) issue_a(ring.A[w16_a_slot(i + NA - 1, NA)], st + NA - 1);
     __builtin_amdgcn_sched_barrier(0);
-    if (active) compute(ring.A[i % NA], ring.B[(i / 2) % 2], std::integral_constant<int, i % 2>{}, Rows, st);
+    if (active) compute(ring.A[w16_a_slot(i, NA)], ring.B[w16_code_slot(i)], std::integral_constant<int, i % 2>{}, Rows, st);
   };
-  constexpr int U = NA == 3 ? 12 : 4;  // whole turns of the A and B slots
+  constexpr int U = w16_turn(NA);
   auto stages = [&](auto Rows) {
     for (int st = st0; st < nst; st += U)  // nst is even
       static_for<0, U / 2>([&](auto X_) {
@@ -274,22 +259,21 @@ __device__ __forceinline__ void w16_tile(const W16TileArgs& a, W16Ring<BM, BN, N
     uint8_t* const terms = reinterpret_cast<uint8_t*>(&ring) + NW * 8192;  // [3][BM rows][32 ranks] bf16
     static_assert(sizeof(ring) >= NW * 8192 + 3 * BM * 64, "the terms stand behind the staging areas");
     auto stage_terms = [&](int rc) {
-      constexpr int kSlicesMost = 4;  // of low
 #pragma unroll 1
       for (int i = 0; i < BM * 4 / (NW * 64); ++i) {
         const int idx = (int)threadIdx.x + NW * 64 * i, r = idx >> 2, c = idx & 3;  // 8 ranks of a row
         float t[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
         if (r < m && rc + 8 * c < a.rank) {
           const float* const p = a.low + (row0 + r) * a.rank + rc + 8 * c;
-          float4 u[kSlicesMost][2];
+          float4 u[kMaxTileLowSlices][2];
 #pragma unroll
-          for (int sl = 0; sl < kSlicesMost; ++sl)
+          for (int sl = 0; sl < kMaxTileLowSlices; ++sl)
             if (sl < a.lslices) {
               u[sl][0] = *reinterpret_cast<const float4*>(p + sl * a.R * a.rank);
               u[sl][1] = *reinterpret_cast<const float4*>(p + sl * a.R * a.rank + 4);
             }
 #pragma unroll
-          for (int sl = 0; sl < kSlicesMost; ++sl)
+          for (int sl = 0; sl < kMaxTileLowSlices; ++sl)
             if (sl < a.lslices)
 #pragma unroll
               for (int h = 0; h < 2; ++h)
