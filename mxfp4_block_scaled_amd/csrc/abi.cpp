@@ -271,6 +271,9 @@ int moe_grouped_gemm_w4a16(const uint16_t* a, int64_t a_rows, int64_t R, const i
   if (sorted_pair && (a_rows + 2) * K * 2 >= kMaxOffset) return MXF_ERR_UNSUPPORTED;
   // the grid: at most E + R / 64 units of ceil(N / 64) workgroups
   if ((E + R / 64) * mxf::cdiv(N, 64) > kMaxRows - 8) return MXF_ERR_UNSUPPORTED;
+  mxf::W16Launch l[3];
+  for (int i = R > 0 ? mxf::w16_grouped_plan(R, E, N, K, swiglu != 0, l) : 0; i-- > 0;)
+    if (!l[i].fits()) return MXF_ERR_UNSUPPORTED;
   if (R == 0) return MXF_OK;
   if (!a || !expert_offsets || !w || !w_scale || !y) return MXF_ERR_NULL;
   const void* ptrs[] = {a, sorted_pair, expert_offsets, w, w_scale, y};
@@ -313,6 +316,7 @@ int fp4_gemm_w4a16_lora(const uint16_t* a, int64_t M, int64_t N, int64_t K, int 
   if (mxf::cdiv(M, 64) * mxf::cdiv(N, 128) > kMaxRows - 8) return MXF_ERR_UNSUPPORTED;
   if ((N + 256) * rank * 2 >= kMaxOffset) return MXF_ERR_UNSUPPORTED;  // an adapter's second factor
   if (M == 0) return MXF_OK;
+  if (!mxf::w16_lora_plan(M, N, K, rank, S).fits) return MXF_ERR_UNSUPPORTED;
   if (!a || !w || !w_scale || !c) return MXF_ERR_NULL;
   if (S > 0 && (!seg_offsets || !seg_adapter)) return MXF_ERR_NULL;
   if (S > 0 && L > 0 && (!lora_a || !lora_b || !scaling)) return MXF_ERR_NULL;

@@ -22,6 +22,7 @@
 #pragma once
 
 #include "gemm_common.hpp"
+#include "w4a16_plan.hpp"
 
 namespace mxf {
 
@@ -113,7 +114,6 @@ __device__ __forceinline__ float block_sum(float v, float* part) {
 }
 
 constexpr int64_t kFewRows = 256;
-constexpr int64_t kMaxThreads = (int64_t(1) << 32) - 1;  // of a launch: the runtime counts them in 32 bits
 constexpr int64_t kOnce = int64_t(1) << 25;  // elements of a batch that the caches do not hold (64 MB in bf16)
 
 // KT rows of y per token, 0: no combine. The rows' loads are in flight together (of rows wider than

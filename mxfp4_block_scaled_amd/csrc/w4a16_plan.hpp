@@ -21,12 +21,16 @@ MXF_BOTH int64_t w16_cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // ---- which kernels a call launches (host) ---------------------------------------------------------
 
+// Threads of a launch: the runtime counts them in 32 bits
+constexpr int64_t kMaxThreads = (int64_t(1) << 32) - 1;
+
 // One launch over the experts of min_rows < rows <= max_rows: workgroups of bm rows x bn weight rows
 // (bm == 16: the streaming kernel; else tiles, 64 x 128 without SwiGLU only)
 struct W16Launch {
   int bm, bn, min_rows, max_rows;
   int64_t units, ntiles;
   int64_t workgroups() const { return 8 * w16_cdiv(units * ntiles, 8); }
+  bool fits() const { return workgroups() * 256 <= kMaxThreads; }
 };
 
 // units of bm rows (0: whole experts) that experts of more than lo rows can make of R rows in all
@@ -82,6 +86,7 @@ struct W16LoraPlan {
   int low_rows;     // rows of a workgroup of the first product
   int low_share;    // workgroups that share a row block's segments
   int bm, bn;
+  bool fits;        // every launch has fewer threads than the runtime counts
 };
 
 constexpr int kMaxBaseSlices = 8, kMaxLowSlices = 16, kMaxTileLowSlices = 4;
@@ -93,8 +98,8 @@ inline bool w16_lora_sliced(int64_t M, int64_t N, int rank) {
 }
 
 // Rows of a workgroup of the first product (not sliced): 32 where segments are long, so that an
-// adapter is read for twice the rows
-inline bool w16_lora_wide(int64_t M, int64_t S) { return M >= 32 * S; }
+// adapter is read for twice the rows, and where 16 (of 1024 threads) would be more threads than a launch has
+inline bool w16_lora_wide(int64_t M, int64_t S) { return M >= 32 * S || M >= int64_t(1) << 26; }
 
 inline int w16_clamp_slices(int64_t want, int64_t most) {
   return (int)(want < most ? (want > 1 ? want : 1) : (most > 1 ? most : 1));
@@ -127,6 +132,7 @@ inline W16LoraPlan w16_lora_plan(int64_t M, int64_t N, int64_t K, int rank, int6
     p.low_slices = (int)w16_min<int64_t>(p.low_slices, w16_max<int64_t>(1, 512 / (blocks * p.low_share)));
     p.bm = 64;
     p.bn = 128;
+    p.fits = true;  // M < 2^14
     return p;
   }
   const bool wide = w16_lora_wide(M, S);
@@ -144,6 +150,8 @@ inline W16LoraPlan w16_lora_plan(int64_t M, int64_t N, int64_t K, int rank, int6
   const bool large = w16_cdiv(M, 128) * w16_cdiv(N, 256) >= 240;
   p.bm = large ? 128 : 64;
   p.bn = large ? 256 : 128;
+  p.fits = 8 * w16_cdiv(w16_cdiv(M, p.low_rows), 8) * (wide ? 512 : 1024) <= kMaxThreads &&
+           W16Launch{p.bm, p.bn, 0, 0, w16_cdiv(M, p.bm), w16_cdiv(N, p.bn)}.fits();
   return p;
 }
 

@@ -115,3 +115,26 @@ def test_bf16_layer_has_no_fused_form():
         ops.moe_layer(x, None, None, None, None, None, 2, act_fmt="bf16", fused=True)
     with pytest.raises(RuntimeError, match="w_fmt"):
         ops.moe_layer(x, None, None, None, None, None, 2, act_fmt="e4m3", w_fmt="nvfp4")
+
+
+def test_launches_of_too_many_threads_are_refused():
+    """A launch of 2^32 threads or more would run modulo 2^32: sizes that need one are UNSUPPORTED, those below are not."""
+    fn = _lib().moe_grouped_gemm_w4a16
+    good = dict(a=None, a_rows=128, R=128, pair=None, topk=1, offs=A, E=8, N=2 ** 26 - 512, K=128, fmt=0, w=A, ws=A, swiglu=0,
+                y=A, yd=1, stream=None)
+    assert call(fn, good, E=48) == NULL  # 56 units of 16 rows, each with 2^18 - 2 workgroups of 256 threads
+    assert call(fn, good, E=64) == UNSUPPORTED  # 72
+    assert call(fn, good, E=1024, N=2 ** 20, R=2 ** 16, a_rows=2 ** 16) == UNSUPPORTED
+    assert call(fn, good, E=1024, N=2 ** 18, R=2 ** 16, a_rows=2 ** 16) == NULL
+    fn = _lib().fp4_gemm_w4a16_lora
+    good = dict(a=None, M=2 ** 28 - 256, N=64, K=512, fmt=0, w=A, ws=A, so=A, sa=A, S=2 ** 28, la=A, lb=A, sc=A, L=2, rank=16,
+                c=A, cd=0, wk=A, wb=0, stream=None)
+    assert call(fn, good) == NULL
+    assert call(fn, good, M=2 ** 28) == UNSUPPORTED
+    assert call(fn, good, M=2 ** 25, N=2 ** 12) == UNSUPPORTED
+    out = (ctypes.c_int32 * 6)()
+    plan = _lib().mxf_w16_lora_plan
+    plan.argtypes = [ctypes.c_int64] * 3 + [ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p]
+    for M, rows in ((2 ** 26 - 1, 16), (2 ** 26, 32)):  # 16 rows take 1024 threads, 32 take 512
+        plan(M, 64, 512, 16, M, out)
+        assert out[2] == rows
