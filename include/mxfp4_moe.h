@@ -353,8 +353,8 @@ typedef enum { MXF_W_MXFP4 = 0, MXF_W_NVFP4 = 1 } mxf_weight;
  * runs in, and with it the order, follows from R, E, N, K and its own rows); a row's result does
  * not depend on what other rows hold. Requires K % 128 == 0, N % 16 == 0 (swiglu: N % 32 == 0),
  * E <= 1024, and the bytes of one expert's codes below 4 GiB with a margin of 257 rows;
- * with sorted_pair also a below 4 GiB; and fewer than 2^24 workgroups a launch (E N, R N
- * beyond 2^30, 2^37). R == 0 is a no-op.
+ * with sorted_pair also a below 4 GiB; and fewer than 2^24 workgroups a launch, which E N below
+ * 2^30 with R N below 2^38 keeps to. R == 0 is a no-op.
  * Errors: NULL, SHAPE, ALIGN, FORMAT, UNSUPPORTED.
  */
 int moe_grouped_gemm_w4a16(const uint16_t* a, int64_t a_rows, int64_t R, const int32_t* sorted_pair, int32_t topk,
@@ -377,7 +377,7 @@ int moe_grouped_gemm_w4a16(const uint16_t* a, int64_t a_rows, int64_t R, const i
  *   workspace    fp4_w4a16_lora_workspace_bytes() bytes, 16-byte aligned, contents
  *                irrelevant; calls that may overlap need one each
  * Requires K % 512 == 0, N % 16 == 0, rank % 8 == 0, 8 <= rank <= 128, and the codes and one
- * adapter's lora_b below 4 GiB (with a margin of 257 rows), M < 2^28 and M N below 2^37. S == 0 (with L == 0
+ * adapter's lora_b below 4 GiB (with a margin of 257 rows), M < 2^28 and M N below 2^38. S == 0 (with L == 0
  * or not): the projection alone. M == 0 is a no-op.
  * Errors: NULL, SHAPE, ALIGN, FORMAT, UNSUPPORTED, WORKSPACE.
  */

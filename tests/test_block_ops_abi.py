@@ -124,14 +124,14 @@ def test_launches_of_too_many_threads_are_refused():
                 y=A, yd=1, stream=None)
     assert call(fn, good, E=48) == NULL  # 56 units of 16 rows, each with 2^18 - 2 workgroups of 256 threads
     assert call(fn, good, E=64) == UNSUPPORTED  # 72
-    assert call(fn, good, E=1024, N=2 ** 20, R=2 ** 16, a_rows=2 ** 16) == UNSUPPORTED
-    assert call(fn, good, E=1024, N=2 ** 18, R=2 ** 16, a_rows=2 ** 16) == NULL
+    assert call(fn, good, E=1024, N=2 ** 22, R=2 ** 16, a_rows=2 ** 16) == UNSUPPORTED
+    assert call(fn, good, E=1024, N=2 ** 21, R=2 ** 16, a_rows=2 ** 16) == NULL
     fn = _lib().fp4_gemm_w4a16_lora
     good = dict(a=None, M=2 ** 28 - 256, N=64, K=512, fmt=0, w=A, ws=A, so=A, sa=A, S=2 ** 28, la=A, lb=A, sc=A, L=2, rank=16,
                 c=A, cd=0, wk=A, wb=0, stream=None)
     assert call(fn, good) == NULL
     assert call(fn, good, M=2 ** 28) == UNSUPPORTED
-    assert call(fn, good, M=2 ** 25, N=2 ** 12) == UNSUPPORTED
+    assert call(fn, good, M=2 ** 25, N=2 ** 14) == UNSUPPORTED
     out = (ctypes.c_int32 * 6)()
     plan = _lib().mxf_w16_lora_plan
     plan.argtypes = [ctypes.c_int64] * 3 + [ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p]
