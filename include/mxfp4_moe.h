@@ -322,7 +322,8 @@ int moe_grouped_mxfp4_gemm_combine(const uint8_t* q, const uint8_t* q_scale, int
  * V4】Triton FP4 优化实战" section "FP4 MoE GEMM 是什么？".
  * accumulated in fp32 in slot order j = 0, 1, ..., then stored as out_dtype
  * (bf16: round to nearest even). y [T*topk][H] (y_dtype), out [T][H].
- * Requires H % 8 == 0. Errors: NULL, SHAPE, ALIGN, FORMAT.
+ * Requires H % 8 == 0, T H below 2^35 and T topk below 2^31. Errors: NULL, SHAPE, ALIGN,
+ * FORMAT, UNSUPPORTED.
  */
 int moe_unpermute_combine(const void* y, int y_dtype, const float* gates,
                           const int32_t* pair_row, int64_t T, int32_t topk, int64_t H,

@@ -248,7 +248,7 @@ int moe_unpermute_combine(const void* y, int y_dtype, const float* gates, const 
                           int32_t topk, int64_t H, void* out, int out_dtype, mxf_stream stream) {
   if (!valid_dtype(y_dtype) || !valid_dtype(out_dtype)) return MXF_ERR_FORMAT;
   if (T < 0 || topk < 1 || topk > 8 || H <= 0 || H % 8 != 0) return MXF_ERR_SHAPE;
-  if (T * (int64_t)topk > kMaxRows) return MXF_ERR_UNSUPPORTED;
+  if (T * (int64_t)topk > kMaxRows || mxf::cdiv(T * (H / 8), 256) * 256 > mxf::kMaxThreads) return MXF_ERR_UNSUPPORTED;
   if (T == 0) return MXF_OK;
   if (!y || !gates || !pair_row || !out) return MXF_ERR_NULL;
   if (!aligned16(y) || !aligned16(gates) || !aligned16(pair_row) || !aligned16(out)) return MXF_ERR_ALIGN;

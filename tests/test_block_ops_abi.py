@@ -138,3 +138,11 @@ def test_launches_of_too_many_threads_are_refused():
     for M, rows in ((2 ** 26 - 1, 16), (2 ** 26, 32)):  # 16 rows take 1024 threads, 32 take 512
         plan(M, 64, 512, 16, M, out)
         assert out[2] == rows
+
+
+def test_a_combine_of_too_many_threads_is_refused():
+    fn = _lib().moe_unpermute_combine
+    good = dict(y=None, yd=1, gates=A, pr=A, T=2 ** 25 - 1, topk=1, H=1024, out=A, od=1, stream=None)
+    assert call(fn, good) == NULL
+    assert call(fn, good, T=2 ** 25) == UNSUPPORTED
+    assert call(fn, good, T=2 ** 19, H=65536) == UNSUPPORTED
