@@ -142,7 +142,7 @@ def test_launches_of_too_many_threads_are_refused():
 
 def test_a_combine_of_too_many_threads_is_refused():
     fn = _lib().moe_unpermute_combine
-    good = dict(y=None, yd=1, gates=A, pr=A, T=2 ** 25 - 1, topk=1, H=1024, out=A, od=1, stream=None)
+    good = dict(y=None, yd=1, gates=A, pr=A, T=2 ** 25 - 2, topk=1, H=1024, out=A, od=1, stream=None)
     assert call(fn, good) == NULL
     assert call(fn, good, T=2 ** 25) == UNSUPPORTED
     assert call(fn, good, T=2 ** 19, H=65536) == UNSUPPORTED
