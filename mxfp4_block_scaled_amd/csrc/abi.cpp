@@ -272,7 +272,7 @@ int moe_grouped_gemm_w4a16(const uint16_t* a, int64_t a_rows, int64_t R, const i
   // the grid: at most E + R / 64 units of ceil(N / 64) workgroups
   if ((E + R / 64) * mxf::cdiv(N, 64) > kMaxRows - 8) return MXF_ERR_UNSUPPORTED;
   mxf::W16Launch l[3];
-  for (int i = R > 0 ? mxf::w16_grouped_plan(R, E, N, K, swiglu != 0, l) : 0; i-- > 0;)
+  for (int i = R > 0 ? mxf::w16_grouped_plan(R, E, N, K, w_fmt == MXF_W_NVFP4, swiglu != 0, l) : 0; i-- > 0;)
     if (!l[i].fits()) return MXF_ERR_UNSUPPORTED;
   if (R == 0) return MXF_OK;
   if (!a || !expert_offsets || !w || !w_scale || !y) return MXF_ERR_NULL;
@@ -377,9 +377,9 @@ int moe_block_norm(const void* y, int y_dtype, int64_t y_rows, const float* expe
 
 // The kernels that a call of these sizes runs, as the launcher has them (for tests and profiles):
 // per launch its rows and weight rows a workgroup, the experts' rows it is for, workgroups
-int mxf_w16_grouped_plan(int64_t R, int32_t E, int64_t N, int64_t K, int swiglu, int64_t* out) {
+int mxf_w16_grouped_plan(int64_t R, int32_t E, int64_t N, int64_t K, int w_fmt, int swiglu, int64_t* out) {
   mxf::W16Launch l[3];
-  const int n = mxf::w16_grouped_plan(R, E, N, K, swiglu != 0, l);
+  const int n = mxf::w16_grouped_plan(R, E, N, K, w_fmt == MXF_W_NVFP4, swiglu != 0, l);
   for (int i = 0; i < n; ++i) {
     const int64_t v[5] = {l[i].bm, l[i].bn, l[i].min_rows, l[i].max_rows, l[i].workgroups()};
     for (int j = 0; j < 5; ++j) out[5 * i + j] = v[j];

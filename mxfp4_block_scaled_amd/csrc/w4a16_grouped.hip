@@ -199,12 +199,10 @@ void launch_stream_t(const W16TileArgs& a, bool out_bf16, dim3 grid, hipStream_t
   else w16_stream_kernel<kNV, kSwiglu, false, kSub><<<grid, 256, 0, stream>>>(a);
 }
 
-template <int kSub>
-void launch_stream_s(const W16TileArgs& a, bool nv, bool swiglu, bool out_bf16, dim3 grid, hipStream_t stream) {
-  if (nv && swiglu) launch_stream_t<true, true, kSub>(a, out_bf16, grid, stream);
-  else if (nv) launch_stream_t<true, false, kSub>(a, out_bf16, grid, stream);
-  else if (swiglu) launch_stream_t<false, true, kSub>(a, out_bf16, grid, stream);
-  else launch_stream_t<false, false, kSub>(a, out_bf16, grid, stream);
+template <bool kNV, int kSub>
+void launch_stream_s(const W16TileArgs& a, bool swiglu, bool out_bf16, dim3 grid, hipStream_t stream) {
+  if (swiglu) launch_stream_t<kNV, true, kSub>(a, out_bf16, grid, stream);
+  else launch_stream_t<kNV, false, kSub>(a, out_bf16, grid, stream);
 }
 
 void launch_stream(W16TileArgs a, bool nv, bool swiglu, bool out_bf16, const W16Launch& l, hipStream_t stream) {
@@ -212,15 +210,16 @@ void launch_stream(W16TileArgs a, bool nv, bool swiglu, bool out_bf16, const W16
   a.max_rows = l.max_rows;
   a.ntiles = (int)l.ntiles;
   const dim3 grid((unsigned)l.workgroups());
-  if (l.bn == 256) launch_stream_s<4>(a, nv, swiglu, out_bf16, grid, stream);
-  else launch_stream_s<1>(a, nv, swiglu, out_bf16, grid, stream);
+  if (nv) launch_stream_s<true, 1>(a, swiglu, out_bf16, grid, stream);
+  else if (l.bn == 256) launch_stream_s<false, 4>(a, swiglu, out_bf16, grid, stream);
+  else launch_stream_s<false, 1>(a, swiglu, out_bf16, grid, stream);
 }
 
 }  // namespace
 
 int launch_w16_grouped(const W16TileArgs& a, bool nv, bool swiglu, bool out_bf16, hipStream_t stream) {
   W16Launch l[3];
-  const int n = w16_grouped_plan(a.R, a.E, a.N, a.K, swiglu, l);
+  const int n = w16_grouped_plan(a.R, a.E, a.N, a.K, nv, swiglu, l);
   for (int i = 0; i < n; ++i) {
     if (l[i].bm == 16) launch_stream(a, nv, swiglu, out_bf16, l[i], stream);
     else launch_w16_tile_grouped(a, nv, swiglu, out_bf16, l[i], stream);

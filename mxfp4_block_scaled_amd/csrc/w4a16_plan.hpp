@@ -51,18 +51,25 @@ inline bool w16_streams_all(int64_t R, int64_t workgroups, int64_t K) {
 }
 
 // A short K (at most one super-step a wave) leaves a streaming workgroup little between its lookup and
-// its sums: where there are many, each takes four runs of 64 weight rows (7168 x 2048, 384 rows over
-// 256 experts: 276 -> 259 us); a longer K loses by it (4096 x 7168, 48 rows: 112 -> 120 us).
-inline int w16_stream_runs(int64_t units, int64_t N, int64_t K) {
-  return K <= 2048 && units * w16_cdiv(N, 64) >= 8192 ? 4 : 1;
+// its sums: where there are many, each takes four runs of 64 MXFP4 weight rows. Measured in us, one
+// and a half rows an expert, one | four runs:
+//   workgroups    K 512          1024         1536         2048         2560         4096         7168
+//    4096       28.2 | 34.7  36.7 | 42.7  42.2 | 48.9  53.2 | 66.3  66.7 | 83.8  91.3 | 116   157 | 188
+//    8192       56.2 | 55.8  70.9 | 70.0  80.8 | 85.6   104 | 101    127 | 136    176 | 187   299 | 315
+//   16384        108 | 102    137 | 128    155 | 156    195 | 187    240 | 248    340 | 347   585 | 613
+//   28672        183 | 165    235 | 211    263 | 260    330 | 316    409 | 413    585 | 600  1045 | 1088
+// NVFP4, whose decoding hides the lookup: 76.1 | 84.6, 93.3 | 102 and 126 | 136 at 8192 workgroups of K
+// 512, 1024 and 2048, 245 | 239, 308 | 298 and 427 | 432 at 28672: always one.
+inline int w16_stream_runs(int64_t units, int64_t N, int64_t K, bool nv) {
+  return !nv && K <= 2048 && units * w16_cdiv(N, 64) >= 8192 ? 4 : 1;
 }
 
 // The launches of a grouped call, in order; returns how many
-inline int w16_grouped_plan(int64_t R, int E, int64_t N, int64_t K, bool swiglu, W16Launch (&l)[3]) {
+inline int w16_grouped_plan(int64_t R, int E, int64_t N, int64_t K, bool nv, bool swiglu, W16Launch (&l)[3]) {
   constexpr int kAll = 0x7FFFFFFF;
   const bool all = w16_streams_all(R, w16_most_units(R, E, 0, 16) * w16_cdiv(N, 64), K);
   const int64_t su = w16_most_units(R, E, 0, all ? 16 : 0);  // units of 16 rows read an expert's weights again from the cache
-  const int runs = w16_stream_runs(su, N, K);
+  const int runs = w16_stream_runs(su, N, K, nv);
   l[0] = W16Launch{16, 64 * runs, 0, all ? kAll : 16, su, w16_cdiv(N, 64 * runs)};
   if (all) return 1;
   const int64_t nt = w16_cdiv(N, 256), w128 = w16_most_units(R, E, 16, 128) * nt;

@@ -26,16 +26,16 @@ def host(tmp_path_factory):
     lib.items.restype = lib.matrix_items.restype = lib.weight_row.restype = i64
     lib.items.argtypes = [i32, ctypes.c_void_p, i32, i64, i32, i32, i64, i64, ctypes.c_void_p]
     lib.matrix_items.argtypes = [i64, i64, i64, ctypes.c_void_p]
-    lib.grouped_plan.argtypes = [i64, i32, i64, i64, i32, ctypes.c_void_p]
+    lib.grouped_plan.argtypes = [i64, i32, i64, i64, i32, i32, ctypes.c_void_p]
     lib.segment.argtypes = [ctypes.c_void_p, i32, i64]
     lib.weight_row.argtypes = [i32, i32, i64, i32, i32]
     lib.share.restype = ctypes.c_uint32
     return lib
 
 
-def plan(host, R, E, N, K, swiglu):
+def plan(host, R, E, N, K, swiglu, nv=0):
     out = np.zeros(18, np.int64)
-    n = host.grouped_plan(R, E, N, K, int(swiglu), out.ctypes.data)
+    n = host.grouped_plan(R, E, N, K, int(nv), int(swiglu), out.ctypes.data)
     return [tuple(int(v) for v in row) for row in out.reshape(3, 6)[:n]]
 
 
@@ -71,7 +71,7 @@ def test_every_item_is_taken_once(host, E, kind):
         if R == 0 or R * (N // 64 + 1) > 2_000_000:
             continue
         offs = (before + np.concatenate([[0], np.cumsum(counts)])).astype(np.int32)
-        launches = plan(host, R, E, N, K, swiglu)
+        launches = plan(host, R, E, N, K, swiglu, E % 2)
         for c in range(1, max(2, int(counts.max()) + 1)):  # an expert of c rows belongs to one launch
             assert sum(lo < c <= hi for _, _, lo, hi, _, _ in launches) == 1
         for launch in launches:
@@ -210,9 +210,17 @@ def test_the_library_has_this_plan(host):
     if not os.path.exists(ops.lib_path()):
         pytest.skip("library not built (run __graft_entry__.build())")
     fn = ops.load().mxf_w16_grouped_plan
-    fn.argtypes = [i64, i32, i64, i64, i32, ctypes.c_void_p]
+    fn.argtypes = [i64, i32, i64, i64, i32, i32, ctypes.c_void_p]
     for R, E, N, K, sw in [(1, 1, 16, 128, 0), (48, 256, 4096, 7168, 1), (512, 4, 4096, 7168, 0), (12288, 256, 7168, 2048, 0),
                            (12288, 32, 4096, 7168, 1), (6000, 8, 2048, 2048, 0)]:
-        out = np.zeros((3, 5), np.int64)
-        n = fn(R, E, N, K, sw, out.ctypes.data)
-        assert [tuple(v[:5]) for v in plan(host, R, E, N, K, sw)] == [tuple(v) for v in out[:n].tolist()]
+        for nv in (0, 1):
+            out = np.zeros((3, 5), np.int64)
+            n = fn(R, E, N, K, nv, sw, out.ctypes.data)
+            assert [tuple(v[:5]) for v in plan(host, R, E, N, K, sw, nv)] == [tuple(v) for v in out[:n].tolist()]
+
+
+def test_runs_of_a_streaming_workgroup(host):
+    """Four runs of weight rows where K is short, workgroups are many and the weights MXFP4, else one."""
+    runs = lambda R, E, N, K, nv: plan(host, R, E, N, K, 0, nv)[0][1] // 64  # noqa: E731
+    assert runs(384, 256, 7168, 2048, 0) == runs(192, 128, 4096, 512, 0) == 4
+    assert runs(384, 256, 7168, 2048, 1) == runs(384, 256, 7168, 2176, 0) == runs(96, 64, 4096, 512, 0) == 1

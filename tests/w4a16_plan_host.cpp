@@ -61,9 +61,9 @@ int64_t matrix_items(int64_t units, int64_t ntiles, int64_t workgroups, int64_t*
   return n;
 }
 
-int grouped_plan(int64_t R, int E, int64_t N, int64_t K, int swiglu, int64_t* out) {
+int grouped_plan(int64_t R, int E, int64_t N, int64_t K, int nv, int swiglu, int64_t* out) {
   W16Launch l[3];
-  const int n = w16_grouped_plan(R, E, N, K, swiglu != 0, l);
+  const int n = w16_grouped_plan(R, E, N, K, nv != 0, swiglu != 0, l);
   for (int i = 0; i < n; ++i) {
     const int64_t v[6] = {l[i].bm, l[i].bn, l[i].min_rows, l[i].max_rows, l[i].workgroups(), l[i].ntiles};
     for (int j = 0; j < 6; ++j) out[6 * i + j] = v[j];
