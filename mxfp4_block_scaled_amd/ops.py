@@ -444,9 +444,10 @@ def moe_grouped_gemm_w4a16(a, expert_offsets, w, w_scale, fmt="mxfp4", sorted_pa
     """Ragged grouped GEMM of bf16 activations with FP4 expert weights: rows expert_offsets[e] ..
     expert_offsets[e + 1] of the result are a's rows times expert e's weights. w [E][N][K/2] uint8, w_scale
     [E][N][K/32] (fmt "mxfp4") or [E][N][K/16] (fmt "nvfp4") uint8. a [R][K], or with sorted_pair [R] (from
-    moe_route_permute) a [R/topk][K] and row r reads a[sorted_pair[r] // topk]. swiglu: the first N/2 weight rows
-    are gate rows and the result is silu(gate) * up. Returns y [R][N] or [R][N/2]; with `out` given, rows outside
-    every expert keep what it holds (in a new tensor they are uninitialised)."""
+    moe_route_permute: all pairs, or those of the experts at hand) a [rows][K] and row r reads
+    a[sorted_pair[r] // topk]. swiglu: the first N/2 weight rows are gate rows and the result is silu(gate) * up.
+    Returns y [R][N] or [R][N/2]; with `out` given, rows outside every expert keep what it holds (in a new tensor
+    they are uninitialised)."""
     _dev(a)
     i = a.get_device()
     if a.dim() != 2 or w.dim() != 3:
@@ -454,21 +455,25 @@ def moe_grouped_gemm_w4a16(a, expert_offsets, w, w_scale, fmt="mxfp4", sorted_pa
     rows, K = a.shape
     E, N, _ = w.shape
     f = _one_of(fmt, WEIGHT_FMTS, "fmt")
-    R = rows * topk if sorted_pair is not None else rows
+    R = rows if sorted_pair is None else sorted_pair.numel()
     _is(a, "a", torch.bfloat16, (rows, K), i)
     _is(expert_offsets, "expert_offsets", torch.int32, (E + 1,), i)
     _is(w, "w", torch.uint8, (E, N, K // 2), i)
     _is(w_scale, "w_scale", torch.uint8, (E, N, K // (16 if f else 32)), i)
+    pairs = None
     if sorted_pair is not None:
         _is(sorted_pair, "sorted_pair", torch.int32, (R,), i)
+        pairs = sorted_pair.data_ptr() or expert_offsets.data_ptr()  # no pairs: a tensor without an address
+        if R > rows * topk:
+            raise RuntimeError(f"sorted_pair: {R} pairs, expected at most a's {rows} rows x topk {topk}")
     shape = (R, N // 2 if swiglu else N)
     if out is None:
         _one_of(out_dtype, DTYPES, "out_dtype")
         out = _new(a, out_dtype, shape)
     else:
         _is(out, "out", (torch.float32, torch.bfloat16), shape, i)
-    _call("moe_grouped_gemm_w4a16", i, a.data_ptr(), rows, R, _at(sorted_pair), topk, expert_offsets.data_ptr(), E, N,
-          K, f, w.data_ptr(), w_scale.data_ptr(), int(swiglu), out.data_ptr(), DTYPES[out.dtype])
+    _call("moe_grouped_gemm_w4a16", i, a.data_ptr(), rows, R, pairs, topk, expert_offsets.data_ptr(), E, N, K, f,
+          w.data_ptr(), w_scale.data_ptr(), int(swiglu), out.data_ptr(), DTYPES[out.dtype])
     return out
 
 

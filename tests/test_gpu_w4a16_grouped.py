@@ -237,3 +237,28 @@ def test_no_rows():
     z = torch.zeros(3, dtype=torch.int32, device="cuda")
     y = ops.moe_grouped_gemm_w4a16(torch.empty(0, 128, dtype=torch.bfloat16, device="cuda"), z, w, s)
     assert y.shape == (0, 32)
+
+
+@pytest.mark.parametrize("T,lo,hi", [(9, 0, 3), (9, 2, 6), (700, 3, 6), (700, 5, 5)])
+def test_the_pairs_of_some_experts(T, lo, hi):
+    """Experts lo .. hi - 1 with their own pairs and offsets give those experts' rows of the whole call."""
+    E, N, K, topk = 6, 4112, 512, 2
+    w, s, _ = weights(E, N, K, "mxfp4", 12)
+    a = torch.from_numpy(dg.activations(13, T, K).view(np.int16)).view(torch.bfloat16).cuda()
+    ids, gates, offs, sp, pr = ops.moe_route_permute(torch.from_numpy(dg.logits(13, T, E)).cuda(), topk)
+    whole = ops.moe_grouped_gemm_w4a16(a, offs, w, s, sorted_pair=sp, topk=topk, out_dtype=torch.float32)
+    o = offs.tolist()
+    mine = ops.moe_grouped_gemm_w4a16(a, (offs[lo:hi + 1] - offs[lo]).contiguous() if hi > lo else offs[:2] * 0,
+                                      w[lo:max(hi, lo + 1)], s[lo:max(hi, lo + 1)], sorted_pair=sp[o[lo]:o[hi]].clone(),
+                                      topk=topk, out_dtype=torch.float32)
+    assert mine.shape == (o[hi] - o[lo], N)
+    err = (mine - whole[o[lo]:o[hi]]).abs()
+    # another kernel may run an expert in the smaller call: the same products in another order
+    x = a.float().abs()[(sp[o[lo]:o[hi]] // topk).long()]
+    hat = torch.from_numpy(np.stack([oracle.dequant_weights(w[e].cpu().numpy(), s[e].cpu().numpy()) for e in range(lo, hi)])
+                           ).float().cuda() if hi > lo else None
+    for e in range(lo, hi):
+        rows = slice(o[e] - o[lo], o[e + 1] - o[lo])
+        assert (err[rows] <= 2 * (K / 16 + 32) * 2.0 ** -23 * (x[rows] @ hat[e - lo].abs().t().contiguous()) * 1.01).all()
+    with pytest.raises(RuntimeError, match="sorted_pair"):
+        ops.moe_grouped_gemm_w4a16(a, offs, w, s, sorted_pair=sp)  # topk forgotten
