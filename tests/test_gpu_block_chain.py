@@ -250,3 +250,14 @@ def test_binding_checks():
         ops.moe_block_norm(b.y, pair_row=torch.zeros(4, dtype=torch.int32, device="cuda"))
     with pytest.raises(RuntimeError, match="act_fmt"):
         ops.moe_block_norm(b.y, act_fmt="e5m2")
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+def test_layer_of_no_tokens(fmt):
+    b = Block(1, 1, 95, fmt)
+    m = ops.moe_layer(b.x[:0], b.logits[:0], b.w1, b.s1, b.w2, b.s2, TOPK, act_fmt="bf16", w_fmt=fmt)
+    assert m["out"].shape == (0, H) and m["h"].shape == (0, I) and m["y"].shape == (0, H)
+    assert (m["expert_offsets"] == 0).all()
+    z = ops.moe_block_norm(m["y"], x=b.x[:0], pre_weight=b.pre, act_fmt="e4m3", expert_gates=m["gates"],
+                           pair_row=m["pair_row"])
+    assert z["r"].shape == (0, H) and z["q_scale"].shape == (0, H // 32)
