@@ -13,10 +13,11 @@
 // non-temporal loads of y and x and stores of r and n too (a batch this size passes through
 // the caches only once; smaller ones keep theirs for the next operator). Walking several rows per
 // workgroup with the weights in LDS and the next row loaded ahead was slower (456 us: half the
-// waves). One chunk per thread instead of two for few rows: one row of 7168 4.2 instead of 4.7 us,
-// 64 rows with the combine 7.3 instead of 8.5 us; for 4096 rows two chunks (55 against 66 us).
+// waves). One chunk per thread instead of two for few rows: one row of 7168 4.5 us, 0.5 less, 64 rows
+// with the combine 7.2 us, 1.2 less; for 4096 rows two chunks (55 against 66 us).
 // Combines of 1 to 8 rows: 64 tokens 6.5 to 7.6 us, 16384 tokens 184, 207, 240, 279, 315, 357, 400,
-// 452 us = 4.5 to 5.6 TB/s (one row after the other 195, 229, 264, 302, 343, -, 426, 467).
+// 452 us = 4.5 to 5.6 TB/s (one row after the other 195, 229, 264, 302, 343, -, 426, 467). All by
+// replays of a captured graph.
 // Roundings: everything is fp32 until each result is stored; n and the codes come from
 // the unrounded r (not from its bf16 copy), the codes from the unrounded n.
 #pragma once

@@ -11,10 +11,11 @@
 // 4 s + g of a 512-k super-step at step s, and instruction j takes their codes 8 j + [0, 8)
 // against activations k = 128 s + 32 g + 8 j + [0, 8). Activations and scales pass through
 // LDS too: loaded by the lane that needs them, 16 rows in 16 neighbouring lanes, they cost the
-// address unit 64 accesses an instruction, and that was the bound (48 rows over 48 of 256
-// experts of 4096 x 7168, SwiGLU, 0.67 GB: 158 us with both, 123 with the scales, 111 with
-// both through LDS = 6.1 TB/s). A launch that stays on the chip and walks the experts was
-// slower (143 us), and so were a super-step's activations loaded one super-step ahead (115).
+// address unit 64 accesses an instruction, and that was the bound (48 rows, which touch 44 or 45
+// of 256 experts of 4096 x 7168, SwiGLU, 0.69 GB: 158 us with neither, 123 with the scales, 111 with
+// both through LDS = 6.2 TB/s; NVFP4, 0.73 GB, 147 us = 5.0 TB/s, the vector unit busy 58 % of the time
+// where it is 23 % with MXFP4). A launch that stays on the chip and walks the experts was slower (143 us), and so were a
+// super-step's activations loaded one super-step ahead (115).
 #include "w4a16_tile.hpp"
 
 namespace mxf {

@@ -12,11 +12,10 @@
 //            sizes a call costs its launches and the length of its K chain (256 requests of one
 //            row at 4096 x 7168, rank 16: 77 us with whole-K tiles, whose last stage walks 64
 //            segments, 35 us sliced).
-// Measured: 4096 x 4096 x 7168, rank 64, 16 segments (0.25 TFLOP) 236-246 us by the card's clock, of
-// which the shrink 23-27 and the tiles 209-220 = 1.15 PFLOP/s, bound as the tiled product is (12 to
-// 17 of them the adapters' share, a chain of loads at the end); 64 requests of one row at
-// 4096 x 7168, rank 16 (26 MB) 18 us, one row at rank 32 10 us, two launches of which one lasts at least
-// 3.4 us.
+// Measured: 4096 x 4096 x 7168, rank 64, 16 segments (0.25 TFLOP) 227-240 us by the card, of which the
+// shrink 24-28, bound as the tiled product is (with no adapter in use 188-193); fp32 results 230, NVFP4
+// 286; 64 requests of one row at 4096 x 7168, rank 16 (26 MB) 18 us (NVFP4 19), one row at rank 32 10
+// us, two launches of which one lasts at least 3.4 us.
 #include "w4a16_tile_body.hpp"
 
 namespace mxf {
@@ -43,9 +42,8 @@ struct ShrinkArgs {
 // lines of 8 rows, and each fragment then passes through 2 KB of the wave's LDS into the lane
 // layout (loaded in that layout, 16 rows in 16 neighbouring lanes, it costs the address unit
 // 64 accesses an instruction: 73 us instead of 37 for 4096 x 7168 activations and rank 64).
-// With K slices, so that there is a workgroup for each compute unit, 23-27 us: 175 MB, as each 32
-// rows read their adapters, at about 7 TB/s out of the caches. More slices cost the tiles'
-// epilogue more than they save here (four instead of two 271 instead of 250 us in all).
+// With K slices, so that there is a workgroup for each compute unit, 24-28 us: 175 MB, as each 32
+// rows read their adapters, at about 7 TB/s out of the caches.
 template <int MF, int RF, int NW>
 struct ShrinkLds {
   v4i part[NW][(MF * RF * 1024 > 2048 ? MF * RF * 1024 : 2048) / 16];  // per wave: a fragment, then its partial sums

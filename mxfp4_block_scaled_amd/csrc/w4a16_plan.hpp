@@ -45,7 +45,10 @@ inline int64_t w16_most_units(int64_t R, int E, int64_t lo, int bm) {
 //                1024       28 | 23 | 25 | 34                            2048      351 | 144 | 155 | 154
 //                6000      139 | 60 | 56 | 57                            6000      977 | 411 | 354 | 308
 // The streaming kernel's time grows with workgroups x K (5 us a million) and needs one launch;
-// a tiled launch lasts at least its K chain (0.36 us for 64 k of 64 x 128 tiles).
+// a tiled launch lasts at least its K chain (0.36 us for 64 k of 64 x 128 tiles). Between them, where
+// about half of the experts hold at most 16 rows, the streaming and the tiled launch follow each other
+// with half of the weights each: 32 experts of 4096 x 4096, 256, 384, 512, 768 and 1024 rows 64, 84, 85,
+// 83 and 79 us (NVFP4 80, 107, 109, 101, 100).
 inline bool w16_streams_all(int64_t R, int64_t workgroups, int64_t K) {
   return R <= 128 || workgroups <= 1100 + 600000 / K;
 }
@@ -80,7 +83,11 @@ inline int w16_grouped_plan(int64_t R, int E, int64_t N, int64_t K, bool nv, boo
     l[1] = W16Launch{bm, bn, 16, kAll, w16_most_units(R, E, 16, bm), w16_cdiv(N, bn)};
     return 2;
   }
-  // a large call, perhaps a skewed one: by the expert's own rows
+  // A large call, perhaps a skewed one: by the expert's own rows. Measured in us against one 128 x 256
+  // launch for all of more than 16 rows: top 6 of 256 experts of 7168 x 2048, 2048 tokens 556 | 581, Zipf
+  // 446 | 448, 1024 tokens 501 | 526, Zipf 298 | 288; of 4096 x 7168 with SwiGLU, 2048 tokens 1099 | 1171,
+  // Zipf 865 | 876, 4096 tokens 1571 | 1567, Zipf 1444 | 1423; of 64 of 4096 x 4096, 1024 tokens 238 |
+  // 235, Zipf 288 | 272; of 32 of 4096 x 7168, 2048 tokens 615 | 612. NVFP4 alike.
   l[1] = W16Launch{64, 256, 16, 64, w16_most_units(R, E, 16, 0), nt};
   l[2] = W16Launch{128, 256, 64, kAll, w16_most_units(R, E, 64, 128), nt};
   return 3;
@@ -99,7 +106,15 @@ struct W16LoraPlan {
 constexpr int kMaxBaseSlices = 8, kMaxLowSlices = 16, kMaxTileLowSlices = 4;
 
 // Fewer than 256 tiles of 64 x 128, where the pass over the rows does not read lora_b too often
-// (N x rank for each row, from the cache)
+// (N x rank for each row, from the cache). Measured in us, sliced | whole tiles:
+//   200 rows of 4096 x 7168, rank 16 and 64      30 | 63, 38 | 89     rank 128, 10 and 100 segments  56 | 127, 74 | 210
+//   500 rows of 2048 x 2048, rank 16 and 64      25 | 27, 37 | 39     rank 128, 10 and 200 segments  58 | 58, 64 | 145
+//   777 rows of 1520 x 2048, 101 segments, rank 24     31 | 39        rank 128  73 | 88
+//   1000 rows of 1024 x 4096, rank 64, and rank 32 with 400 segments  45 | 47, 44 | 73     rank 128  66 | 63
+//   3000 rows of 512 x 2048, rank 32                   34 | 28        rank 128  77 | 53
+//   120 rows of 7168 x 2048, rank 64                   30 | 46        250 rows  49 | 47
+// The left column is sliced by this rule, the right one is not; with a long K or many segments the
+// border could lie higher.
 inline bool w16_lora_sliced(int64_t M, int64_t N, int rank) {
   return M <= 64 || (w16_cdiv(M, 64) * w16_cdiv(N, 128) < 256 && M * N * rank <= (int64_t(1) << 26));
 }

@@ -21,8 +21,9 @@
 // cycle hit different banks.
 //
 // Many rows are bound by the MFMA at the clock that the power allows: 32 experts x 4096 x
-// 7168, 12288 rows, SwiGLU (0.72 TFLOP) 605-650 us by the card = 1.1-1.2 PFLOP/s, the MFMA busy 64 %
-// of the time at 1.8 GHz; a plain bf16 product of the same size from the library 552 us. There the 128 x
+// 7168, 12288 rows, SwiGLU (0.72 TFLOP) 605-650 us by the card = 1.1-1.2 PFLOP/s, the MFMA busy 65 %
+// of the time at 1.8 GHz; a plain bf16 product of the same size from the library 552 us. NVFP4 715-755 us,
+// 50 %: its decoding multiplies each weight by the scale's mantissa first. There the 128 x
 // 256 tile has two slots (73 KB: two workgroups a compute unit, whose stages interleave); 256
 // x 256 and 128 x 512, one workgroup a compute unit, were slower (742 us). Without adapters a wave
 // there takes all 128 rows, so that a weight is decoded once (2 experts of 4096 rows 426 -> 417 us
