@@ -415,6 +415,118 @@ int moe_block_norm(const void* y, int y_dtype, int64_t y_rows, const float* expe
                    int gate_dtype, int gate_mode, void* r, void* n, int n_dtype, int fmt, uint8_t* q,
                    uint8_t* q_scale, mxf_stream stream);
 
+/*
+ * moe_balance_loss - the load-balance and z losses of a router, with its per-expert counts.
+ * With p = softmax(logits[t]) over all E experts, lse = log(sum exp(logits[t])), sequences s =
+ * [seg_offsets[s], seg_offsets[s+1]), n_s its tokens that count, n = sum n_s, S' the sequences with
+ * n_s > 0, c_si the pairs of those tokens that go to expert i, P_si = 1/n_s sum_t p_ti:
+ *   losses[0] = 1/S' sum_s E / (topk n_s) sum_i c_si P_si    (1 where both are spread evenly)
+ *   losses[1] = 1/n sum_t lse_t^2
+ * Both are 0 where no token counts. A token counts if it is in a sequence, token_mask does not
+ * exclude it and one of its logits at least is not -inf (experts ruled out hold -inf: p = 0).
+ *   logits       [T][E] fp32 or bf16 (logits_dtype)
+ *   topk_ids     [T][topk] int32 as moe_route_permute writes them; an id outside [0, E) is a
+ *                dropped pair and counts for nothing, the same id twice counts twice
+ *   token_mask   [T] bytes, 0 excludes the token (any alignment); NULL: none excluded
+ *   seg_offsets  [S+1] int32, ascending within [0, T] (values outside are held to it; empty
+ *                sequences are fine); NULL: one sequence of all tokens, S must be 1
+ *   counts       [S][E] int32: c;  prob_mean [S][E] fp32: P (0 in an empty sequence)
+ *   tokens       [S+2] int32: n_s, then n, then S'
+ *   lse          [T] fp32, -inf for a token that does not count (the gradient reads it)
+ *   losses       [2] fp32
+ *   workspace    moe_balance_loss_workspace_bytes(T, E, S) bytes, 16-byte aligned, contents
+ *                irrelevant; calls that may overlap need one each
+ * Sums in fp32 and above in a fixed order: deterministic. NaN and +inf logits make the losses NaN.
+ * Requires 1 <= topk <= min(E, 8), E <= 1024, S >= 1, T topk below 2^31, T below 2^26 and
+ * S ceil(E / 64) below 2^23. T == 0 writes zeros. Errors: NULL, SHAPE, ALIGN, FORMAT, UNSUPPORTED,
+ * WORKSPACE.
+ */
+size_t moe_balance_loss_workspace_bytes(int64_t T, int32_t E, int32_t S);
+int moe_balance_loss(const void* logits, int logits_dtype, const int32_t* topk_ids, const uint8_t* token_mask,
+                     const int32_t* seg_offsets, int32_t S, int64_t T, int32_t E, int32_t topk, int32_t* counts,
+                     int32_t* tokens, float* prob_mean, float* lse, float* losses, void* workspace,
+                     size_t workspace_bytes, mxf_stream stream);
+
+/*
+ * moe_route_backward - the gradient of the logits, from the gates' and the losses':
+ *   dlogits[t][i] = sum_{j: topk_ids[t][j] = i} gates[t][j] (dgates[t][j] - sum_k gates[t][k] dgates[t][k])
+ *     + dlosses[0] E / (S' topk n_s^2) p_i (c_si - sum_j p_j c_sj) + dlosses[1] 2/n lse p_i
+ * (the first line: the softmax over the selected logits of moe_route_permute; the second for tokens
+ * that count, with the counts held constant).
+ *   gates, dgates [T][topk] fp32; dgates NULL: no such term (gates and topk_ids are ignored)
+ *   dlosses      [2] fp32 on the device (4-byte aligned); NULL: no such terms (logits, lse, counts,
+ *                tokens and seg_offsets are ignored)
+ *   lse, counts, tokens  as moe_balance_loss wrote them for these sequences (counts and tokens may be
+ *                those of several GPUs added up)
+ *   dlogits      [T][E], of logits_dtype; every value is written
+ * Sizes as for moe_balance_loss. T == 0 is a no-op. Errors: NULL (neither term wanted, too), SHAPE,
+ * ALIGN, FORMAT, UNSUPPORTED.
+ */
+int moe_route_backward(const void* logits, int logits_dtype, const int32_t* topk_ids, const float* gates,
+                       const float* dgates, const float* dlosses, const float* lse, const int32_t* counts,
+                       const int32_t* tokens, const int32_t* seg_offsets, int32_t S, int64_t T, int32_t E, int32_t topk,
+                       void* dlogits, mxf_stream stream);
+
+/*
+ * moe_combine_backward - the gradient of moe_unpermute_combine, p = t topk + j:
+ *   dy[pair_row[p]] = gates[p] * dout[t],   dgates[p] = sum_h dout[t][h] * y[pair_row[p]][h]
+ * in fp32, each result rounded once when it is stored.
+ *   dout         [T][H] fp32 or bf16 (dout_dtype);  y, dy [y_rows][H] (y_dtype)
+ *   pair_row     [T*topk] int32; an entry outside [0, y_rows) is a dropped pair (its dgates is 0).
+ *                The others name a row each, no row twice. Rows of dy that none names are left as
+ *                they were.
+ *   dy, dgates   either may be NULL (not wanted), not both; y may be NULL without dgates
+ * dy may be y itself. Requires H % 8 == 0, topk <= 8, T topk below 2^31, and T (or T topk below 256
+ * tokens) workgroups of at most 512 threads below 2^32 threads. T == 0 is a no-op.
+ * Errors: NULL, SHAPE, ALIGN, FORMAT, UNSUPPORTED.
+ */
+int moe_combine_backward(const void* dout, int dout_dtype, const void* y, int y_dtype, int64_t y_rows,
+                         const float* gates, const int32_t* pair_row, int64_t T, int32_t topk, int64_t H, void* dy,
+                         float* dgates, mxf_stream stream);
+
+/*
+ * nvfp4_tensor_scale - the scale of a whole tensor for NVFP4: the smallest power of two g (at least
+ * 2^-126) with max |x| <= 6 * 448 * g, and 1 for a tensor of zeros. A power of two, so that block scale
+ * times g, and with it every quantised value, is exact.
+ *   x  n values, fp32 or bf16 (n % 32 == 0);  scale [1] fp32 on the device (4-byte aligned)
+ *   workspace    nvfp4_tensor_scale_workspace_bytes() bytes, 16-byte aligned, contents irrelevant
+ * Errors: NULL, SHAPE, ALIGN, FORMAT, WORKSPACE.
+ */
+size_t nvfp4_tensor_scale_workspace_bytes(void);
+int nvfp4_tensor_scale(const void* x, int x_dtype, int64_t n, float* scale, void* workspace, size_t workspace_bytes,
+                       mxf_stream stream);
+
+/*
+ * fp4_quantize - a matrix to 4-bit blocks, along its rows, its columns, or both from one read:
+ *   MXFP4 (fmt MXF_W_MXFP4): blocks of B = 32, scale 2^(byte - 127) as in mxfp4_quantize_act, d = scale
+ *   NVFP4 (MXF_W_NVFP4): blocks of B = 16, scale s = E4M3(amax / (6 g)) (round to nearest even,
+ *     at most 448), d = s g; a block whose d is below 2^-126 is stored as zeros
+ *   code = E2M1(x / d) in fp32, the sign kept, at most 6: to nearest, ties to even, or with rnd the
+ *     upper of the two neighbours of |x / d| where the part above the lower one, as a share of
+ *     their distance, exceeds (rnd + 1/2) / 256
+ *   x            [rows][cols] fp32 or bf16 (x_dtype)
+ *   tensor_scale [1] fp32 on the device (4-byte aligned), positive: g (NULL: 1; MXFP4 has none)
+ *   rnd          [rows][cols] random bytes, the same for both directions; NULL: to nearest
+ *   q, q_scale   [rows][cols/2], [rows][cols/B] (both NULL: not wanted)
+ *   qt, qt_scale the codes of x^T, blocks along x's columns: [cols][R/2], [cols][R/B] with R = rows
+ *                rounded up to 128; elements past the rows are zeros (both NULL: not wanted)
+ * These are the operands of fp4_gemm, and q, q_scale the weights of the calls above. Values that are
+ * not finite are not handled: they spoil their own block (and a tensor scale taken from them).
+ * Requires cols % 32 == 0. rows == 0 is a no-op. Errors: NULL, SHAPE (a tensor scale with MXFP4,
+ * too), ALIGN, FORMAT, UNSUPPORTED.
+ */
+int fp4_quantize(const void* x, int x_dtype, int64_t rows, int64_t cols, int fmt, const float* tensor_scale,
+                 const uint8_t* rnd, uint8_t* q, uint8_t* q_scale, uint8_t* qt, uint8_t* qt_scale, mxf_stream stream);
+
+/*
+ * fp4_dequantize - out [rows][cols] (fp32 or bf16) = E2M1 value x block scale x g, one rounding to
+ * out_dtype (none is needed where g is a power of two and nothing leaves the type's range). Arguments
+ * as fp4_quantize writes them along the rows; a transposed result is read with its own rows and cols.
+ * Requires cols % 32 == 0. rows == 0 is a no-op. Errors: NULL, SHAPE, ALIGN, FORMAT, UNSUPPORTED.
+ */
+int fp4_dequantize(const uint8_t* q, const uint8_t* q_scale, int64_t rows, int64_t cols, int fmt,
+                   const float* tensor_scale, void* out, int out_dtype, mxf_stream stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -91,6 +91,51 @@ struct BlockNormArgs {
 int launch_block_norm(const BlockNormArgs& a, bool y_bf16, hipStream_t stream);
 void launch_block_norm_f32(const BlockNormArgs& a, hipStream_t stream);
 
+// losses and gradient of the router (route_loss.hip)
+struct RouteLossArgs {
+  const void* logits;  // [T][E]
+  const int32_t* topk_ids;
+  const uint8_t* token_mask;
+  const int32_t* seg_offsets;  // [S+1], or none: one sequence of all tokens
+  const float *gates, *dgates, *dlosses;
+  int64_t T;
+  int E, topk, S;
+  int32_t *counts, *tokens;  // [S][E]; [S + 2]: by sequence, in all, sequences that hold any
+  float *prob_mean, *lse, *losses;
+  void *dlogits, *workspace;
+};
+size_t route_loss_workspace(int64_t T, int64_t E, int64_t S);
+int launch_route_loss(const RouteLossArgs& a, bool bf16, hipStream_t stream);
+int launch_route_backward(const RouteLossArgs& a, bool bf16, hipStream_t stream);
+
+// backward pass of the combine (combine_backward.hip)
+struct CombineBackwardArgs {
+  const void *dout, *y;
+  const float* gates;
+  const int32_t* pair_row;
+  int64_t T, H, y_rows;
+  int topk;
+  void* dy;
+  float* dgates;
+};
+int combine_backward_pairs(int64_t T, int topk);
+int combine_backward_threads(int64_t H);
+int launch_combine_backward(const CombineBackwardArgs& a, bool y_bf16, bool dout_bf16, hipStream_t stream);
+
+// quantisation to MXFP4 / NVFP4 along rows and columns, and back (fp4_quant.hip)
+struct Fp4QuantArgs {
+  const void* x;
+  int64_t rows, cols;
+  const float* tensor_scale;
+  const uint8_t* rnd;
+  uint8_t *q, *q_scale, *qt, *qt_scale;
+};
+constexpr int kAmaxBlocks = 1024;
+int launch_fp4_quantize(const Fp4QuantArgs& a, bool x_bf16, bool nvfp4, hipStream_t stream);
+int launch_fp4_dequantize(const uint8_t* q, const uint8_t* q_scale, int64_t blocks32, bool nvfp4,
+                          const float* tensor_scale, void* out, bool out_bf16, hipStream_t stream);
+int launch_nvfp4_tensor_scale(const void* x, bool bf16, int64_t n16, float* scale, uint32_t* partial, hipStream_t stream);
+
 // the lookup-table route (gemm_q8.hip): Q8 activations and int8-expanded MXFP4 weights
 int launch_q8_quantize(const uint16_t* x, int64_t rows, int64_t K, int8_t* q, uint16_t* d, hipStream_t stream);
 int launch_q8_gemm(const int8_t* q, const uint16_t* d, int64_t M, int64_t N, int64_t K, const uint8_t* w,

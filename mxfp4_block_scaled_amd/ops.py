@@ -57,6 +57,15 @@ SIGNATURES = {
     "mxf_ceiling_read": (_c_int, [_p, _c_i64, _p, _p]),
     "mxf_ceiling_lds_copy_bytes": (_c_i64, [_c_int, _c_int]),
     "mxf_ceiling_lds_copy": (_c_int, [_p, _c_i64, _c_int, _c_int, _p, _p]),
+    "moe_balance_loss_workspace_bytes": (_sz, [_c_i64, _c_i32, _c_i32]),
+    "moe_balance_loss": (_c_int, [_p, _c_int, _p, _p, _p, _c_i32, _c_i64, _c_i32, _c_i32, _p, _p, _p, _p, _p, _p, _sz,
+                                  _p]),
+    "moe_route_backward": (_c_int, [_p, _c_int, _p, _p, _p, _p, _p, _p, _p, _p, _c_i32, _c_i64, _c_i32, _c_i32, _p, _p]),
+    "moe_combine_backward": (_c_int, [_p, _c_int, _p, _c_int, _c_i64, _p, _p, _c_i64, _c_i32, _c_i64, _p, _p, _p]),
+    "nvfp4_tensor_scale_workspace_bytes": (_sz, []),
+    "nvfp4_tensor_scale": (_c_int, [_p, _c_int, _c_i64, _p, _p, _sz, _p]),
+    "fp4_quantize": (_c_int, [_p, _c_int, _c_i64, _c_i64, _c_int, _p, _p, _p, _p, _p, _p, _p]),
+    "fp4_dequantize": (_c_int, [_p, _p, _c_i64, _c_i64, _c_int, _p, _p, _c_int, _p]),
 }
 
 CEILING_MFMA_GROUPS = 512
@@ -581,6 +590,184 @@ def moe_block_norm(y, x=None, post_weight=None, gate=None, residual_scale=1.0, p
           _at(x), x_dtype, residual_scale, _at(post_weight), _at(pre_weight), DTYPES[w_dtype], eps, _at(gate),
           DTYPES[g_dtype], mode, _at(r), _at(n), n_code, fmt or 0, _at(q), _at(qs))
     return dict(r=r, n=n, q=q, q_scale=qs)
+
+
+def moe_balance_loss(logits, topk_ids, token_mask=None, seg_offsets=None, workspace=None):
+    """Load-balance and z losses of a router, with per-expert counts. logits [T][E] fp32 or bf16, topk_ids [T][topk]
+    int32 (moe_route_permute's; an id outside the experts is a dropped pair), token_mask [T] uint8 or bool (0: the
+    token does not count), seg_offsets [S+1] int32 (sequences; None: one of all tokens). Returns a dict of losses [2]
+    fp32 (balance, averaged over the sequences that hold a token; z), counts [S][E] int32, prob_mean [S][E] fp32,
+    tokens [S+2] int32 (by sequence, in all, sequences that hold any) and lse [T] fp32: what moe_route_backward takes."""
+    _dev(logits)
+    i = logits.get_device()
+    if logits.dim() != 2 or topk_ids.dim() != 2:
+        raise RuntimeError("logits must be [T][E] and topk_ids [T][topk]")
+    T, E = logits.shape
+    topk = topk_ids.shape[1]
+    dt = _one_of(logits.dtype, DTYPES, "logits")
+    _is(topk_ids, "topk_ids", torch.int32, (T, topk), i)
+    if token_mask is not None:
+        _is(token_mask, "token_mask", (torch.uint8, torch.bool), (T,), i)
+    S = _segments(seg_offsets, i)
+    need = load().moe_balance_loss_workspace_bytes(T, E, S)
+    workspace = _workspace(workspace, need, topk_ids)
+    counts = topk_ids.new_empty((S, E))
+    tokens = topk_ids.new_empty((S + 2,))
+    mean = torch.empty((S, E), dtype=torch.float32, device=logits.device)
+    lse = mean.new_empty((T,))
+    losses = mean.new_empty((2,))
+    _call("moe_balance_loss", i, logits.data_ptr(), dt, topk_ids.data_ptr(), _at(token_mask), _at(seg_offsets), S, T, E,
+          topk, counts.data_ptr(), tokens.data_ptr(), mean.data_ptr(), lse.data_ptr(), losses.data_ptr(),
+          workspace.data_ptr(), workspace.numel())
+    return dict(losses=losses, counts=counts, prob_mean=mean, tokens=tokens, lse=lse)
+
+
+def _segments(seg_offsets, i):
+    """The number of sequences of seg_offsets [S+1] int32 on GPU i (None: one)."""
+    if seg_offsets is None:
+        return 1
+    if seg_offsets.dim() != 1 or seg_offsets.shape[0] < 2:
+        raise RuntimeError("seg_offsets must be [S+1] of one sequence at least")
+    _is(seg_offsets, "seg_offsets", torch.int32, tuple(seg_offsets.shape), i)
+    return seg_offsets.shape[0] - 1
+
+
+def _workspace(workspace, need, like):
+    """A byte workspace of at least `need` bytes beside `like`: the given one, checked, or a new one."""
+    if workspace is None:
+        return torch.empty((max(need, 1),), dtype=torch.uint8, device=like.device)
+    if _dev(workspace) != like.device:
+        raise RuntimeError(f"workspace is on {workspace.device}, expected {like.device}")
+    _need(workspace, "workspace", torch.uint8, ((">=", need),))
+    return workspace
+
+
+def moe_route_backward(logits, topk_ids, gates=None, dgates=None, balance=None, dlosses=None, seg_offsets=None):
+    """The gradient of the router's logits [T][E]: of the gates (the softmax over the selected logits) with gates and
+    dgates [T][topk] fp32, and of the losses with `balance`, moe_balance_loss's dict for these seg_offsets, and dlosses
+    [2] fp32 (the losses' own gradients, on the GPU). Either part may be left out. Returns dlogits, of logits' dtype."""
+    _dev(logits)
+    i = logits.get_device()
+    if logits.dim() != 2 or topk_ids.dim() != 2:
+        raise RuntimeError("logits must be [T][E] and topk_ids [T][topk]")
+    T, E = logits.shape
+    topk = topk_ids.shape[1]
+    dt = _one_of(logits.dtype, DTYPES, "logits")
+    _is(topk_ids, "topk_ids", torch.int32, (T, topk), i)
+    if (gates is None) != (dgates is None):
+        raise RuntimeError("gates and dgates go together")
+    if (balance is None) != (dlosses is None):
+        raise RuntimeError("balance and dlosses go together")
+    if gates is None and balance is None:
+        raise RuntimeError("neither dgates nor dlosses: nothing to compute")
+    S = _segments(seg_offsets, i)
+    lse = counts = tokens = None
+    if gates is not None:
+        _is(gates, "gates", torch.float32, (T, topk), i)
+        _is(dgates, "dgates", torch.float32, (T, topk), i)
+    if balance is not None:
+        lse, counts, tokens = balance["lse"], balance["counts"], balance["tokens"]
+        _is(dlosses, "dlosses", torch.float32, (2,), i)
+        _is(lse, "lse", torch.float32, (T,), i)
+        _is(counts, "counts", torch.int32, (S, E), i)
+        _is(tokens, "tokens", torch.int32, (S + 2,), i)
+    dlogits = torch.empty_like(logits)
+    _call("moe_route_backward", i, logits.data_ptr(), dt, topk_ids.data_ptr(), _at(gates), _at(dgates), _at(dlosses),
+          _at(lse), _at(counts), _at(tokens), _at(seg_offsets), S, T, E, topk, dlogits.data_ptr())
+    return dlogits
+
+
+def moe_combine_backward(dout, y, gates, pair_row, want_dy=True, want_dgates=True, dy=None):
+    """The gradient of moe_unpermute_combine: dout [T][H] bf16/fp32, y [rows][H] bf16/fp32, gates [T][topk] fp32,
+    pair_row [T*topk] int32 (an entry outside y's rows is a dropped pair; no row twice). Returns (dy [rows][H] of y's
+    dtype, dgates [T][topk] fp32); what is not wanted is None. Rows of dy that no pair names keep what a given `dy`
+    holds (in a new tensor they are uninitialised)."""
+    _dev(dout)
+    i = dout.get_device()
+    if dout.dim() != 2 or y.dim() != 2 or gates.dim() != 2:
+        raise RuntimeError("dout must be [T][H], y [rows][H] and gates [T][topk]")
+    T, H = dout.shape
+    rows = y.shape[0]
+    topk = gates.shape[1]
+    d_code, y_code = _one_of(dout.dtype, DTYPES, "dout"), _one_of(y.dtype, DTYPES, "y")
+    _is(y, "y", y.dtype, (rows, H), i)
+    _is(gates, "gates", torch.float32, (T, topk), i)
+    _is(pair_row, "pair_row", torch.int32, (T * topk,), i)
+    if dy is not None:
+        _is(dy, "dy", y.dtype, (rows, H), i)
+    elif want_dy:
+        dy = torch.empty_like(y)
+    dgates = torch.empty_like(gates) if want_dgates else None
+    _call("moe_combine_backward", i, dout.data_ptr(), d_code, _at(y), y_code, rows, gates.data_ptr(), pair_row.data_ptr(),
+          T, topk, H, _at(dy), _at(dgates))
+    return dy, dgates
+
+
+def nvfp4_tensor_scale(x, workspace=None):
+    """x [rows][cols] bf16/fp32 -> [1] fp32: the smallest power of two that takes max |x| to at most 6 * 448, for
+    fp4_quantize (1 for zeros)."""
+    _dev(x)
+    i = x.get_device()
+    dt = _one_of(x.dtype, DTYPES, "x")
+    out = torch.empty((1,), dtype=torch.float32, device=x.device)
+    workspace = _workspace(workspace, load().nvfp4_tensor_scale_workspace_bytes(), x)
+    _call("nvfp4_tensor_scale", i, x.data_ptr(), dt, x.numel(), out.data_ptr(), workspace.data_ptr(), workspace.numel())
+    return out
+
+
+def _tensor_scale(t, fmt, i, name="tensor_scale"):
+    if t is not None:
+        if not fmt:
+            raise RuntimeError(f"{name}: MXFP4 has none")
+        _is(t, name, torch.float32, (1,), i)
+
+
+def fp4_quantize(x, fmt="nvfp4", tensor_scale=None, rnd=None, rows=True, transposed=False):
+    """x [rows][cols] bf16/fp32 to 4-bit blocks: fmt "nvfp4" (16 elements, UE4M3 scales, times tensor_scale [1] fp32 if
+    given) or "mxfp4" (32 elements, UE8M0). To nearest, or stochastically with rnd [rows][cols] uint8 random bytes.
+    Returns a dict of q [rows][cols/2] and q_scale [rows][cols/B] (rows=True), and of qt [cols][R/2] and qt_scale
+    [cols][R/B] (transposed=True): the codes of x^T, R = rows rounded up to 128 with zeros; else None. uint8, as fp4_gemm
+    takes them."""
+    _dev(x)
+    i = x.get_device()
+    if x.dim() != 2:
+        raise RuntimeError("x must be 2-d [rows][cols]")
+    n, cols = x.shape
+    dt = _one_of(x.dtype, DTYPES, "x")
+    f = _one_of(fmt, WEIGHT_FMTS, "fmt")
+    B = 16 if f else 32
+    _tensor_scale(tensor_scale, f, i)
+    if rnd is not None:
+        _is(rnd, "rnd", torch.uint8, (n, cols), i)
+    if not rows and not transposed:
+        raise RuntimeError("neither rows nor transposed: nothing to compute")
+    q = qs = qt = qts = None
+    if rows:
+        q = torch.empty((n, cols // 2), dtype=torch.uint8, device=x.device)
+        qs = q.new_empty((n, cols // B))
+    if transposed:
+        padded = (n + 127) // 128 * 128
+        qt = torch.empty((cols, padded // 2), dtype=torch.uint8, device=x.device)
+        qts = qt.new_empty((cols, padded // B))
+    _call("fp4_quantize", i, x.data_ptr(), dt, n, cols, f, _at(tensor_scale), _at(rnd), _at(q), _at(qs), _at(qt), _at(qts))
+    return dict(q=q, q_scale=qs, qt=qt, qt_scale=qts)
+
+
+def fp4_dequantize(q, q_scale, fmt="nvfp4", tensor_scale=None, out_dtype=torch.bfloat16):
+    """q [rows][cols/2], q_scale [rows][cols/B] uint8 (as fp4_quantize writes them) -> [rows][cols] bf16 or fp32."""
+    _dev(q)
+    i = q.get_device()
+    if q.dim() != 2:
+        raise RuntimeError("q must be [rows][cols/2]")
+    n, half = q.shape
+    f = _one_of(fmt, WEIGHT_FMTS, "fmt")
+    _is(q, "q", torch.uint8, (n, half), i)
+    _is(q_scale, "q_scale", torch.uint8, (n, half * 2 // (16 if f else 32)), i)
+    _tensor_scale(tensor_scale, f, i)
+    out = torch.empty((n, 2 * half), dtype=out_dtype, device=q.device)
+    _call("fp4_dequantize", i, q.data_ptr(), q_scale.data_ptr(), n, 2 * half, f, _at(tensor_scale), out.data_ptr(),
+          _one_of(out_dtype, DTYPES, "out_dtype"))
+    return out
 
 
 def moe_layer(x, logits, w1, w1_scale, w2, w2_scale, topk, act_fmt="e4m3", y_dtype=torch.bfloat16,

@@ -1,0 +1,116 @@
+"""Refusals of the operators of training on the CPU: every bad argument returns its status before any device call, and
+the binding's own checks raise."""
+
+import ctypes
+import os
+
+import pytest
+import torch
+
+from mxfp4_block_scaled_amd import ops
+
+OK, NULL, SHAPE, ALIGN, FORMAT, UNSUPPORTED, LAUNCH, WORKSPACE = range(8)
+A, U = 4096, 4096 + 4  # never dereferenced: validation fails first
+U2 = 4096 + 2
+
+
+def _lib():
+    if not os.path.exists(ops.lib_path()):
+        pytest.skip("library not built (run __graft_entry__.build())")
+    return ops.load()
+
+
+def call(fn, good, **change):
+    return fn(*{**good, **change}.values())
+
+
+def test_balance_loss_errors():
+    lib = _lib()
+    fn = lib.moe_balance_loss
+    need = lib.moe_balance_loss_workspace_bytes(300, 60, 3)
+    assert need >= 8 * 60 * 8  # five workgroups and three sequences: slots of counts and sums
+    good = dict(lg=A, ld=0, ids=A, mask=A + 1, so=A, S=3, T=300, E=60, topk=4, c=A, n=A, p=A, lse=A, loss=A, ws=A, wb=need,
+                stream=None)
+    for change, want in [
+        (dict(ld=2), FORMAT), (dict(T=-1), SHAPE), (dict(E=0), SHAPE), (dict(topk=0), SHAPE), (dict(topk=9), SHAPE),
+        (dict(E=3), SHAPE), (dict(S=0), SHAPE), (dict(E=1025), UNSUPPORTED), (dict(T=2 ** 29), UNSUPPORTED),
+        (dict(T=2 ** 26), UNSUPPORTED), (dict(S=2 ** 23), UNSUPPORTED), (dict(so=None), NULL), (dict(lg=None), NULL),
+        (dict(ids=None), NULL), (dict(c=None), NULL), (dict(n=None), NULL), (dict(p=None), NULL), (dict(lse=None), NULL),
+        (dict(loss=None), NULL), (dict(lg=U), ALIGN), (dict(ids=U), ALIGN), (dict(so=U), ALIGN), (dict(c=U), ALIGN),
+        (dict(n=U), ALIGN), (dict(p=U), ALIGN), (dict(lse=U), ALIGN), (dict(loss=U), ALIGN), (dict(ws=U), ALIGN),
+        (dict(ws=None), WORKSPACE), (dict(wb=need - 1), WORKSPACE),
+    ]:
+        assert call(fn, good, **change) == want, change
+
+
+def test_route_backward_errors():
+    fn = _lib().moe_route_backward
+    good = dict(lg=A, ld=0, ids=A, g=A, dg=A, dl=A, lse=A, c=A, n=A, so=A, S=3, T=300, E=60, topk=4, out=A, stream=None)
+    assert call(fn, good, T=0) == OK
+    for change, want in [
+        (dict(ld=-1), FORMAT), (dict(T=-1), SHAPE), (dict(topk=61, E=60), SHAPE), (dict(S=0), SHAPE),
+        (dict(E=1025), UNSUPPORTED), (dict(T=2 ** 26), UNSUPPORTED), (dict(out=None), NULL), (dict(dg=None, dl=None), NULL),
+        (dict(g=None), NULL), (dict(ids=None), NULL), (dict(lg=None), NULL), (dict(lse=None), NULL), (dict(c=None), NULL),
+        (dict(n=None), NULL), (dict(so=None), NULL), (dict(lg=U), ALIGN), (dict(ids=U), ALIGN), (dict(g=U), ALIGN),
+        (dict(dg=U), ALIGN), (dict(dl=U2), ALIGN), (dict(lse=U), ALIGN), (dict(c=U), ALIGN), (dict(n=U), ALIGN),
+        (dict(so=U), ALIGN), (dict(out=U), ALIGN),
+    ]:
+        assert call(fn, good, **change) == want, change
+
+
+def test_combine_backward_errors():
+    fn = _lib().moe_combine_backward
+    good = dict(do=A, dd=1, y=A, yd=1, rows=24, g=A, pr=A, T=8, topk=3, H=64, dy=A, dg=A, stream=None)
+    assert call(fn, good, T=0) == OK
+    for change, want in [
+        (dict(dd=2), FORMAT), (dict(yd=2), FORMAT), (dict(T=-1), SHAPE), (dict(rows=-1), SHAPE), (dict(topk=0), SHAPE),
+        (dict(topk=9), SHAPE), (dict(H=0), SHAPE), (dict(H=12), SHAPE), (dict(T=2 ** 30), UNSUPPORTED),
+        (dict(T=2 ** 26, H=1024), UNSUPPORTED), (dict(T=2 ** 24, H=7168), UNSUPPORTED), (dict(do=None), NULL),
+        (dict(y=None), NULL), (dict(g=None), NULL), (dict(pr=None), NULL), (dict(dy=None, dg=None), NULL), (dict(do=U), ALIGN),
+        (dict(y=U), ALIGN), (dict(g=U), ALIGN), (dict(pr=U), ALIGN), (dict(dy=U), ALIGN), (dict(dg=U), ALIGN),
+    ]:
+        assert call(fn, good, **change) == want, change
+
+
+def test_quantise_errors():
+    lib = _lib()
+    fn = lib.nvfp4_tensor_scale
+    need = lib.nvfp4_tensor_scale_workspace_bytes()
+    good = dict(x=A, xd=1, n=64, out=A, ws=A, wb=need, stream=None)
+    for change, want in [
+        (dict(xd=2), FORMAT), (dict(n=0), SHAPE), (dict(n=48), SHAPE), (dict(x=None), NULL), (dict(out=None), NULL),
+        (dict(x=U), ALIGN), (dict(out=U2), ALIGN), (dict(ws=U), ALIGN), (dict(ws=None), WORKSPACE), (dict(wb=need - 1), WORKSPACE),
+    ]:
+        assert call(fn, good, **change) == want, change
+    fn = lib.fp4_quantize
+    good = dict(x=A, xd=1, rows=10, cols=64, fmt=1, g=U, rnd=A, q=A, qs=A, qt=A, qts=A, stream=None)
+    assert call(fn, good, rows=0) == OK
+    for change, want in [
+        (dict(xd=2), FORMAT), (dict(fmt=2), FORMAT), (dict(rows=-1), SHAPE), (dict(cols=0), SHAPE), (dict(cols=48), SHAPE),
+        (dict(fmt=0), SHAPE), (dict(rows=2 ** 31), UNSUPPORTED), (dict(cols=2 ** 31), UNSUPPORTED),
+        (dict(rows=2 ** 30, cols=2 ** 14), UNSUPPORTED), (dict(rows=2 ** 26, cols=1024, qt=None, qts=None), UNSUPPORTED),
+        (dict(x=None), NULL), (dict(q=None), NULL), (dict(qs=None), NULL), (dict(qt=None), NULL), (dict(qts=None), NULL),
+        (dict(q=None, qs=None, qt=None, qts=None), NULL), (dict(x=U), ALIGN), (dict(g=U2), ALIGN), (dict(rnd=U), ALIGN),
+        (dict(q=U), ALIGN), (dict(qs=U), ALIGN), (dict(qt=U), ALIGN), (dict(qts=U), ALIGN),
+    ]:
+        assert call(fn, good, **change) == want, change
+    fn = lib.fp4_dequantize
+    good = dict(q=A, qs=A, rows=10, cols=64, fmt=1, g=U, out=A, od=1, stream=None)
+    assert call(fn, good, rows=0) == OK
+    for change, want in [
+        (dict(od=2), FORMAT), (dict(fmt=-1), FORMAT), (dict(rows=-1), SHAPE), (dict(cols=16), SHAPE), (dict(fmt=0), SHAPE),
+        (dict(rows=2 ** 31), UNSUPPORTED), (dict(rows=2 ** 27, cols=1024), UNSUPPORTED), (dict(q=None), NULL),
+        (dict(qs=None), NULL), (dict(out=None), NULL), (dict(q=U), ALIGN), (dict(qs=U), ALIGN), (dict(g=U2), ALIGN),
+        (dict(out=U), ALIGN),
+    ]:
+        assert call(fn, good, **change) == want, change
+
+
+def test_binding_refuses_host_tensors():
+    z = torch.zeros
+    f, i = z(4, 64), z(4, 2, dtype=torch.int32)
+    for fn, args in [(ops.moe_balance_loss, (f, i)), (ops.moe_route_backward, (f, i, z(4, 2), z(4, 2))),
+                     (ops.moe_combine_backward, (f, z(8, 64), z(4, 2), i.view(-1))), (ops.nvfp4_tensor_scale, (f,)),
+                     (ops.fp4_quantize, (f,)), (ops.fp4_dequantize, (z(4, 32, dtype=torch.uint8), z(4, 4, dtype=torch.uint8)))]:
+        with pytest.raises(RuntimeError, match="GPU"):
+            fn(*args)
