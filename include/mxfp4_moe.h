@@ -527,6 +527,28 @@ int fp4_quantize(const void* x, int x_dtype, int64_t rows, int64_t cols, int fmt
 int fp4_dequantize(const uint8_t* q, const uint8_t* q_scale, int64_t rows, int64_t cols, int fmt,
                    const float* tensor_scale, void* out, int out_dtype, mxf_stream stream);
 
+/*
+ * fp4_gemm - the product of two quantised matrices, C = g_a g_b A_hat * B_hat^T
+ *   a, a_scale   [M][K/2] E2M1 codes, [M][K/32] UE8M0 bytes (fmt MXF_W_MXFP4) or [M][K/16] UE4M3 bytes
+ *                (MXF_W_NVFP4), as fp4_quantize writes them;  b, b_scale  [N][K/2], [N][K/32] or [N][K/16]
+ *   a_tensor_scale, b_tensor_scale  [1] fp32 on the device (4-byte aligned): g_a, g_b of NVFP4 (NULL: 1;
+ *                MXFP4 has none)
+ *   c            [M][N] fp32 or bf16 (c_dtype), one rounding at the end
+ *   workspace    fp4_gemm_workspace_bytes(M, N, K, fmt) bytes (0: none needed, may be NULL), 16-byte
+ *                aligned, contents irrelevant: K slices' sums, added in a fixed order; calls that may
+ *                overlap need one each
+ * A linear layer y = x W^T of [T][I] by [O][I] and its gradients: y = fp4_gemm(q(x), q(W)), dx =
+ * fp4_gemm(q(dy), qt(W)), dW = fp4_gemm(qt(dy), qt(x)), q and qt as fp4_quantize's.
+ * Every product is exact (NVFP4: code x scale is exact in the fp16 operands), accumulation in fp32.
+ * Requires K % 128 == 0, N % 16 == 0, K < 2^24, M N < 2^34 and at most 2^22 tiles of 128 x 128. The
+ * UE8M0 byte 255 and the UE4M3 byte 0x7F (NaN) are not valid scales. M == 0 is a no-op.
+ * Errors: NULL, SHAPE (a tensor scale with MXFP4, too), ALIGN, FORMAT, UNSUPPORTED, WORKSPACE.
+ */
+size_t fp4_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K, int fmt);
+int fp4_gemm(const uint8_t* a, const uint8_t* a_scale, int64_t M, const uint8_t* b, const uint8_t* b_scale, int64_t N,
+             int64_t K, int fmt, const float* a_tensor_scale, const float* b_tensor_scale, void* c, int c_dtype,
+             void* workspace, size_t workspace_bytes, mxf_stream stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -148,4 +148,30 @@ int fp4_dequantize(const uint8_t* q, const uint8_t* q_scale, int64_t rows, int64
              : MXF_OK;
 }
 
+size_t fp4_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K, int fmt) {
+  if (M <= 0 || N <= 0 || K <= 0 || !valid_weight(fmt)) return 0;
+  return round_up(mxf::fp4_pair_workspace(M, N, K, fmt == MXF_W_NVFP4), 256);
+}
+
+int fp4_gemm(const uint8_t* a, const uint8_t* a_scale, int64_t M, const uint8_t* b, const uint8_t* b_scale, int64_t N,
+             int64_t K, int fmt, const float* a_tensor_scale, const float* b_tensor_scale, void* c, int c_dtype,
+             void* workspace, size_t workspace_bytes, mxf_stream stream) {
+  if (!valid_weight(fmt) || !valid_dtype(c_dtype)) return MXF_ERR_FORMAT;
+  if (M < 0 || N <= 0 || N % 16 != 0 || K <= 0 || K % 128 != 0) return MXF_ERR_SHAPE;
+  if (fmt == MXF_W_MXFP4 && (a_tensor_scale || b_tensor_scale)) return MXF_ERR_SHAPE;
+  // 32-bit byte offsets inside a tile of 256 rows; items and threads of a launch counted in 32 bits
+  if (M > kMaxRows || N > kMaxRows || K >= (int64_t(1) << 24)) return MXF_ERR_UNSUPPORTED;
+  if (mxf::cdiv(M, 128) * mxf::cdiv(N, 128) > (int64_t(1) << 22) || M * N >= (int64_t(1) << 34)) return MXF_ERR_UNSUPPORTED;
+  if (M == 0) return MXF_OK;
+  if (!a || !a_scale || !b || !b_scale || !c) return MXF_ERR_NULL;
+  const void* ptrs[] = {a, a_scale, b, b_scale, c, workspace};
+  if (!all_aligned16(ptrs) || !aligned4(a_tensor_scale) || !aligned4(b_tensor_scale)) return MXF_ERR_ALIGN;
+  const size_t need = fp4_gemm_workspace_bytes(M, N, K, fmt);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return MXF_ERR_WORKSPACE;
+  return mxf::launch_fp4_pair(a, a_scale, M, b, b_scale, N, K, fmt == MXF_W_NVFP4, a_tensor_scale, b_tensor_scale, c,
+                              c_dtype == MXF_BF16, workspace, as_stream(stream))
+             ? MXF_ERR_LAUNCH
+             : MXF_OK;
+}
+
 }  // extern "C"

@@ -136,6 +136,12 @@ int launch_fp4_dequantize(const uint8_t* q, const uint8_t* q_scale, int64_t bloc
                           const float* tensor_scale, void* out, bool out_bf16, hipStream_t stream);
 int launch_nvfp4_tensor_scale(const void* x, bool bf16, int64_t n16, float* scale, uint32_t* partial, hipStream_t stream);
 
+// the product of two quantised matrices (fp4_pair.hip)
+size_t fp4_pair_workspace(int64_t M, int64_t N, int64_t K, bool nvfp4);
+int launch_fp4_pair(const uint8_t* a, const uint8_t* as, int64_t M, const uint8_t* b, const uint8_t* bs, int64_t N,
+                    int64_t K, bool nvfp4, const float* ga, const float* gb, void* c, bool c_bf16, void* workspace,
+                    hipStream_t stream);
+
 // the lookup-table route (gemm_q8.hip): Q8 activations and int8-expanded MXFP4 weights
 int launch_q8_quantize(const uint16_t* x, int64_t rows, int64_t K, int8_t* q, uint16_t* d, hipStream_t stream);
 int launch_q8_gemm(const int8_t* q, const uint16_t* d, int64_t M, int64_t N, int64_t K, const uint8_t* w,

@@ -12,6 +12,7 @@
 // sequence: both ascend along the tokens, so each pair that meets has a slot of its own) and added
 // in a fixed order by a second launch: no floating-point atomics, the same result every time.
 #include "launch.hpp"
+#include "w4a16_tile.hpp"
 #include "wave.hpp"
 
 namespace mxf {
@@ -55,20 +56,9 @@ __device__ __forceinline__ int64_t seg_begin(const RouteLossArgs& a, int s) {
   return a.seg_offsets ? min(max((int64_t)a.seg_offsets[s], (int64_t)0), a.T) : (s > 0 ? a.T : 0);
 }
 
-// The number of sequences that end at or before token t, by a whole wave: 64 probes a step.
+// the first sequence that ends past token t, by a whole wave
 __device__ __forceinline__ int seg_of(const RouteLossArgs& a, int64_t t) {
-  if (!a.seg_offsets) return 0;
-  const int lane = threadIdx.x & 63;
-  int lo = 0, len = a.S;
-  while (len > 0) {
-    const int stride = (len + 63) >> 6, i = lane * stride + stride - 1;  // the last of this lane's part
-    const bool before = i < len && (int64_t)a.seg_offsets[lo + i + 1] <= t;
-    const int whole = __popcll(__ballot(before));  // parts that lie before t
-    const int next = whole * stride;
-    len = min(len - next, stride - 1);
-    lo += next;
-  }
-  return lo;
+  return a.seg_offsets ? first_segment(a.seg_offsets, a.S, t) : 0;
 }
 
 __device__ __forceinline__ double wave_sum_f64(double v) {

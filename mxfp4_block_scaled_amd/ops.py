@@ -66,6 +66,8 @@ SIGNATURES = {
     "nvfp4_tensor_scale": (_c_int, [_p, _c_int, _c_i64, _p, _p, _sz, _p]),
     "fp4_quantize": (_c_int, [_p, _c_int, _c_i64, _c_i64, _c_int, _p, _p, _p, _p, _p, _p, _p]),
     "fp4_dequantize": (_c_int, [_p, _p, _c_i64, _c_i64, _c_int, _p, _p, _c_int, _p]),
+    "fp4_gemm_workspace_bytes": (_sz, [_c_i64, _c_i64, _c_i64, _c_int]),
+    "fp4_gemm": (_c_int, [_p, _p, _c_i64, _p, _p, _c_i64, _c_i64, _c_int, _p, _p, _p, _c_int, _p, _sz, _p]),
 }
 
 CEILING_MFMA_GROUPS = 512
@@ -767,6 +769,38 @@ def fp4_dequantize(q, q_scale, fmt="nvfp4", tensor_scale=None, out_dtype=torch.b
     out = torch.empty((n, 2 * half), dtype=out_dtype, device=q.device)
     _call("fp4_dequantize", i, q.data_ptr(), q_scale.data_ptr(), n, 2 * half, f, _at(tensor_scale), out.data_ptr(),
           _one_of(out_dtype, DTYPES, "out_dtype"))
+    return out
+
+
+def fp4_gemm(a, a_scale, b, b_scale, fmt="nvfp4", a_tensor_scale=None, b_tensor_scale=None, out_dtype=torch.bfloat16,
+             out=None, workspace=None):
+    """The product of two quantised matrices (as fp4_quantize writes them): a [M][K/2], b [N][K/2] uint8 codes with
+    their scales [.][K/16] (fmt "nvfp4") or [.][K/32] ("mxfp4"), tensor scales [1] fp32 of NVFP4 (None: 1) ->
+    c [M][N] bf16 or fp32."""
+    _dev(a)
+    i = a.get_device()
+    if a.dim() != 2 or b.dim() != 2:
+        raise RuntimeError("a must be [M][K/2] and b [N][K/2]")
+    M, half = a.shape
+    N = b.shape[0]
+    f = _one_of(fmt, WEIGHT_FMTS, "fmt")
+    blocks = half * 2 // (16 if f else 32)
+    _is(a, "a", torch.uint8, (M, half), i)
+    _is(a_scale, "a_scale", torch.uint8, (M, blocks), i)
+    _is(b, "b", torch.uint8, (N, half), i)
+    _is(b_scale, "b_scale", torch.uint8, (N, blocks), i)
+    _tensor_scale(a_tensor_scale, f, i, "a_tensor_scale")
+    _tensor_scale(b_tensor_scale, f, i, "b_tensor_scale")
+    if out is None:
+        _one_of(out_dtype, DTYPES, "out_dtype")
+        out = torch.empty((M, N), dtype=out_dtype, device=a.device)
+    else:
+        _is(out, "out", (torch.float32, torch.bfloat16), (M, N), i)
+    need = load().fp4_gemm_workspace_bytes(M, N, 2 * half, f)
+    if need or workspace is not None:
+        workspace = _workspace(workspace, need, a)
+    _call("fp4_gemm", i, a.data_ptr(), a_scale.data_ptr(), M, b.data_ptr(), b_scale.data_ptr(), N, 2 * half, f,
+          _at(a_tensor_scale), _at(b_tensor_scale), out.data_ptr(), DTYPES[out.dtype], _at(workspace), need)
     return out
 
 

@@ -1,0 +1,148 @@
+"""fp4_gemm against 64-bit products of the decoded operands.
+
+Products are exact in the matrix instructions; a sum of K of them in fp32 takes at most K / 8 + 16 additions (a group of
+8 or more products adds up without rounding but one at its end, then steps, K slices), each off by less than 2^-23 of
+the sum of magnitudes. bf16 results add half a step, 2^-8 of the value."""
+
+import numpy as np
+import pytest
+import torch
+
+from mxfp4_block_scaled_amd import ops
+from tests import train_exact as ex
+
+pytestmark = pytest.mark.gpu
+
+E2M1 = torch.tensor(list(ex.E2M1) + [-v for v in ex.E2M1], dtype=torch.float64)
+E4M3 = torch.tensor(np.concatenate([ex.E4M3, [np.nan]]), dtype=torch.float64)
+
+
+def _operand(rows, K, fmt, seed, wide=False):
+    g = torch.Generator().manual_seed(seed)
+    q = torch.randint(0, 256, (rows, K // 2), dtype=torch.uint8, generator=g)
+    if fmt == "nvfp4":
+        s = torch.randint(0 if wide else 40, 127 if wide else 72, (rows, K // 16), dtype=torch.uint8, generator=g)
+    else:
+        s = torch.randint(60 if wide else 119, 180 if wide else 124, (rows, K // 32), dtype=torch.uint8, generator=g)
+    return q.cuda(), s.cuda()
+
+
+def _values(q, s, fmt):
+    v = E2M1.cuda()[torch.stack((q & 15, q >> 4), -1).flatten(1).long()]
+    if fmt == "nvfp4":
+        return v * E4M3.cuda()[s.long() & 127].repeat_interleave(16, 1)
+    return v * torch.ldexp(torch.ones((), dtype=torch.float64), s.cpu().long() - 127).cuda().repeat_interleave(32, 1)
+
+
+def _check(got, a, sa, b, sb, fmt, ga=1.0, gb=1.0):
+    K = a.shape[1] * 2
+    x, y = _values(a, sa, fmt), _values(b, sb, fmt)
+    want = torch.mm(x, y.t().contiguous()) * ga * gb
+    size = torch.mm(x.abs(), y.abs().t().contiguous()) * abs(ga * gb)
+    tol = (K / 8 + 16) * 2.0 ** -23 * size + (2.0 ** -8 * want.abs() if got.dtype == torch.bfloat16 else 0)
+    assert ((got.double() - want).abs() <= tol + 1e-40).all()
+
+
+SIZES = [(1, 16, 128), (1, 4096, 7168), (5, 48, 384), (8, 512, 16384), (31, 528, 1152), (33, 64, 256), (64, 4096, 2048),
+         (100, 96, 4096), (128, 128, 512), (129, 144, 640), (300, 1040, 2048), (257, 272, 7168), (1000, 2064, 896),
+         (2048, 2048, 1024), (4000, 3344, 1408)]
+
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+@pytest.mark.parametrize("M,N,K", SIZES)
+def test_against_64_bits(M, N, K, fmt):
+    a, sa = _operand(M, K, fmt, M)
+    b, sb = _operand(N, K, fmt, N + 1)
+    nv = fmt == "nvfp4"
+    ga = torch.tensor([0.37]).cuda() if nv else None
+    gb = torch.tensor([2.0 ** -9]).cuda() if nv else None
+    for dt in (torch.float32, torch.bfloat16):
+        got = ops.fp4_gemm(a, sa, b, sb, fmt, ga, gb, out_dtype=dt)
+        _check(got, a, sa, b, sb, fmt, float(ga) if nv else 1.0, float(gb) if nv else 1.0)
+        assert torch.equal(got, ops.fp4_gemm(a, sa, b, sb, fmt, ga, gb, out_dtype=dt))
+
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+@pytest.mark.parametrize("rows", [3, 40, 200, 1000])
+def test_every_element_in_its_place(fmt, rows):
+    """b holds a one in each column: the product is a's decoded values, exactly, at the full range of scales."""
+    K = 896
+    a, sa = _operand(rows, K, fmt, 5, wide=True)
+    codes = torch.zeros((K, K), dtype=torch.uint8)
+    codes[torch.arange(K), torch.arange(K)] = 2
+    b = (codes[:, ::2] | codes[:, 1::2] << 4).cuda()
+    sb = torch.full((K, K // (16 if fmt == "nvfp4" else 32)), 0x38 if fmt == "nvfp4" else 127, dtype=torch.uint8).cuda()
+    got = ops.fp4_gemm(a, sa, b, sb, fmt, out_dtype=torch.float32)
+    assert torch.equal(got.double(), _values(a, sa, fmt))
+    a, sa = a[:rows // 16 * 16], sa[:rows // 16 * 16]
+    if rows >= 16:
+        got = ops.fp4_gemm(b, sb, a, sa, fmt, out_dtype=torch.float32)
+        assert torch.equal(got.double().t(), _values(a, sa, fmt))
+
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+@pytest.mark.parametrize("M,N", [(48, 64), (300, 272), (3000, 4112)])
+@pytest.mark.parametrize("K", [128, 384, 640])
+def test_a_nan_scale_stays_with_its_row(fmt, M, N, K):
+    """K that ends inside a stage: what lies behind a row (the next row's codes and scales) counts for nothing."""
+    a, sa = _operand(M, K, fmt, 7)
+    b, sb = _operand(N, K, fmt, 8)
+    clean = ops.fp4_gemm(a, sa, b, sb, fmt, out_dtype=torch.float32)
+    bad = 0x7F if fmt == "nvfp4" else 0xFF
+    sa[5] = bad
+    sb[9] = bad
+    got = ops.fp4_gemm(a, sa, b, sb, fmt, out_dtype=torch.float32)
+    hit = torch.zeros((M, N), dtype=torch.bool)
+    hit[5] = hit[:, 9] = True
+    assert torch.equal(got.isnan().cpu(), hit)
+    assert torch.equal(got[~hit.cuda()], clean[~hit.cuda()])
+
+
+def test_no_stray_writes_and_given_output():
+    for M, N, K in ((3, 32, 256), (130, 144, 512), (3000, 4112, 256)):
+        a, sa = _operand(M, K, "nvfp4", 1)
+        b, sb = _operand(N, K, "nvfp4", 2)
+        want = ops.fp4_gemm(a, sa, b, sb, out_dtype=torch.bfloat16)
+        room = torch.full((M + 2, N), 7.0, dtype=torch.bfloat16).cuda()
+        need = ops.load().fp4_gemm_workspace_bytes(M, N, K, 1)
+        ws = torch.full((need + 64,), 255, dtype=torch.uint8).cuda()
+        got = ops.fp4_gemm(a, sa, b, sb, out=room[1:M + 1], workspace=ws)
+        assert torch.equal(got, want) and (room[0] == 7).all() and (room[M + 1] == 7).all()
+        assert (ws[need:] == 255).all()
+
+
+def test_a_captured_product_and_other_streams():
+    a, sa = _operand(200, 2048, "nvfp4", 3)
+    b, sb = _operand(528, 2048, "nvfp4", 4)
+    c, sc = _operand(200, 2048, "nvfp4", 5)
+    first, second = ops.fp4_gemm(a, sa, b, sb), ops.fp4_gemm(c, sc, b, sb)
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        other = ops.fp4_gemm(c, sc, b, sb)
+    here = ops.fp4_gemm(a, sa, b, sb)
+    torch.cuda.synchronize()
+    assert torch.equal(other, second) and torch.equal(here, first)
+    graph = torch.cuda.CUDAGraph()
+    x, sx = a.clone(), sa.clone()
+    with torch.cuda.graph(graph):
+        held = ops.fp4_gemm(x, sx, b, sb)
+    for q, s, want in ((a, sa, first), (c, sc, second), (a, sa, first)):
+        x.copy_(q)
+        sx.copy_(s)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(held, want)
+
+
+def test_no_rows_and_refusals():
+    b, sb = _operand(32, 256, "nvfp4", 1)
+    assert ops.fp4_gemm(b[:0], sb[:0], b, sb).shape == (0, 32)
+    one = torch.ones(1).cuda()
+    for bad in (dict(b=b[:24], b_scale=sb[:24]), dict(fmt="mxfp4"), dict(a_scale=sb[:, :8].contiguous()), dict(fmt="x"),
+                dict(out=torch.empty((32, 16)).cuda()), dict(out_dtype=torch.float16)):
+        with pytest.raises(RuntimeError):
+            ops.fp4_gemm(**{**dict(a=b, a_scale=sb, b=b, b_scale=sb), **bad})
+    m, sm = _operand(32, 256, "mxfp4", 1)
+    with pytest.raises(RuntimeError):
+        ops.fp4_gemm(m, sm, m, sm, "mxfp4", one)

@@ -106,6 +106,27 @@ def test_quantise_errors():
         assert call(fn, good, **change) == want, change
 
 
+def test_fp4_gemm_errors():
+    lib = _lib()
+    fn = lib.fp4_gemm
+    M, N, K = 100, 96, 4096
+    need = lib.fp4_gemm_workspace_bytes(M, N, K, 1)
+    assert need >= 2 * M * N * 4 and lib.fp4_gemm_workspace_bytes(0, N, K, 1) == 0  # one tile: K slices
+    assert lib.fp4_gemm_workspace_bytes(8192, 8192, K, 0) == 0
+    good = dict(a=A, sa=A, M=M, b=A, sb=A, N=N, K=K, fmt=1, ga=U, gb=U, c=A, cd=1, ws=A, wb=need, stream=None)
+    assert call(fn, good, M=0) == OK
+    for change, want in [
+        (dict(fmt=2), FORMAT), (dict(cd=2), FORMAT), (dict(M=-1), SHAPE), (dict(N=0), SHAPE), (dict(N=24), SHAPE),
+        (dict(K=0), SHAPE), (dict(K=192), SHAPE), (dict(fmt=0), SHAPE), (dict(fmt=0, ga=None), SHAPE),
+        (dict(M=2 ** 31), UNSUPPORTED), (dict(N=2 ** 31), UNSUPPORTED), (dict(K=2 ** 24), UNSUPPORTED),
+        (dict(M=2 ** 20, N=2 ** 14), UNSUPPORTED), (dict(M=2 ** 30, N=16), UNSUPPORTED), (dict(a=None), NULL),
+        (dict(sa=None), NULL), (dict(b=None), NULL), (dict(sb=None), NULL), (dict(c=None), NULL), (dict(a=U), ALIGN),
+        (dict(sa=U), ALIGN), (dict(b=U), ALIGN), (dict(sb=U), ALIGN), (dict(c=U), ALIGN), (dict(ws=U), ALIGN),
+        (dict(ga=U2), ALIGN), (dict(gb=U2), ALIGN), (dict(ws=None), WORKSPACE), (dict(wb=need - 1), WORKSPACE),
+    ]:
+        assert call(fn, good, **change) == want, change
+
+
 def test_binding_refuses_host_tensors():
     z = torch.zeros
     f, i = z(4, 64), z(4, 2, dtype=torch.int32)
