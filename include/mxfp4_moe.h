@@ -512,8 +512,9 @@ int nvfp4_tensor_scale(const void* x, int x_dtype, int64_t n, float* scale, void
  *                rounded up to 128; elements past the rows are zeros (both NULL: not wanted)
  * These are the operands of fp4_gemm, and q, q_scale the weights of the calls above. Values that are
  * not finite are not handled: they spoil their own block (and a tensor scale taken from them).
- * Requires cols % 32 == 0. rows == 0 is a no-op. Errors: NULL, SHAPE (a tensor scale with MXFP4,
- * too), ALIGN, FORMAT, UNSUPPORTED.
+ * Requires cols % 32 == 0, cols < 2^22 and at most 2^23 tiles of 128 x 128 (transposed), or rows cols
+ * below 2^36. rows == 0 is a no-op. Errors: NULL, SHAPE (a tensor scale with MXFP4, too), ALIGN, FORMAT,
+ * UNSUPPORTED.
  */
 int fp4_quantize(const void* x, int x_dtype, int64_t rows, int64_t cols, int fmt, const float* tensor_scale,
                  const uint8_t* rnd, uint8_t* q, uint8_t* q_scale, uint8_t* qt, uint8_t* qt_scale, mxf_stream stream);

@@ -120,9 +120,11 @@ int fp4_quantize(const void* x, int x_dtype, int64_t rows, int64_t cols, int fmt
                  const uint8_t* rnd, uint8_t* q, uint8_t* q_scale, uint8_t* qt, uint8_t* qt_scale, mxf_stream stream) {
   if (!valid_dtype(x_dtype) || !valid_weight(fmt)) return MXF_ERR_FORMAT;
   if (rows < 0 || cols <= 0 || cols % 32 != 0 || (tensor_scale && fmt == MXF_W_MXFP4)) return MXF_ERR_SHAPE;
-  if (rows > kMaxRows || cols > kMaxRows) return MXF_ERR_UNSUPPORTED;
-  const int64_t groups = qt ? mxf::cdiv(rows, 128) * mxf::cdiv(cols, 128) : mxf::cdiv(rows * (cols / 16), 256);
-  if (groups * 256 > mxf::kMaxThreads) return MXF_ERR_UNSUPPORTED;
+  if (rows > kMaxRows || cols >= (int64_t(1) << 22)) return MXF_ERR_UNSUPPORTED;  // 32-bit offsets in 128 rows
+  // workgroups of 512 threads per 128 x 128 values, or of 256 per 4096 (fp32) or 8192 (bf16) of them
+  const int64_t threads = qt ? mxf::cdiv(mxf::cdiv(rows, 128) * mxf::cdiv(cols, 128), 8) * 8 * 512
+                             : mxf::cdiv(rows * cols, x_dtype == MXF_BF16 ? 8192 : 4096) * 256;
+  if (threads > mxf::kMaxThreads) return MXF_ERR_UNSUPPORTED;
   if (rows == 0) return MXF_OK;
   if (!x || (!q && !qt) || (q == nullptr) != (q_scale == nullptr) || (qt == nullptr) != (qt_scale == nullptr))
     return MXF_ERR_NULL;
@@ -136,7 +138,7 @@ int fp4_dequantize(const uint8_t* q, const uint8_t* q_scale, int64_t rows, int64
                    const float* tensor_scale, void* out, int out_dtype, mxf_stream stream) {
   if (!valid_weight(fmt) || !valid_dtype(out_dtype)) return MXF_ERR_FORMAT;
   if (rows < 0 || cols <= 0 || cols % 32 != 0 || (tensor_scale && fmt == MXF_W_MXFP4)) return MXF_ERR_SHAPE;
-  if (rows > kMaxRows || cols > kMaxRows || mxf::cdiv(rows * (cols / 32), 256) * 256 > mxf::kMaxThreads)
+  if (rows > kMaxRows || cols > kMaxRows || mxf::cdiv(rows * cols, 4096) * 256 > mxf::kMaxThreads)
     return MXF_ERR_UNSUPPORTED;
   if (rows == 0) return MXF_OK;
   if (!q || !q_scale || !out) return MXF_ERR_NULL;

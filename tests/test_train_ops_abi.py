@@ -88,7 +88,7 @@ def test_quantise_errors():
     for change, want in [
         (dict(xd=2), FORMAT), (dict(fmt=2), FORMAT), (dict(rows=-1), SHAPE), (dict(cols=0), SHAPE), (dict(cols=48), SHAPE),
         (dict(fmt=0), SHAPE), (dict(rows=2 ** 31), UNSUPPORTED), (dict(cols=2 ** 31), UNSUPPORTED),
-        (dict(rows=2 ** 30, cols=2 ** 14), UNSUPPORTED), (dict(rows=2 ** 26, cols=1024, qt=None, qts=None), UNSUPPORTED),
+        (dict(rows=2 ** 30, cols=2 ** 14), UNSUPPORTED), (dict(cols=2 ** 22), UNSUPPORTED), (dict(rows=2 ** 28, cols=1024, qt=None, qts=None), UNSUPPORTED),
         (dict(x=None), NULL), (dict(q=None), NULL), (dict(qs=None), NULL), (dict(qt=None), NULL), (dict(qts=None), NULL),
         (dict(q=None, qs=None, qt=None, qts=None), NULL), (dict(x=U), ALIGN), (dict(g=U2), ALIGN), (dict(rnd=U), ALIGN),
         (dict(q=U), ALIGN), (dict(qs=U), ALIGN), (dict(qt=U), ALIGN), (dict(qts=U), ALIGN),
