@@ -434,8 +434,8 @@ int moe_block_norm(const void* y, int y_dtype, int64_t y_rows, const float* expe
  *   tokens       [S+2] int32: n_s, then n, then S'
  *   lse          [T] fp32, -inf for a token that does not count (the gradient reads it)
  *   losses       [2] fp32
- *   workspace    moe_balance_loss_workspace_bytes(T, E, S) bytes, 16-byte aligned, contents
- *                irrelevant; calls that may overlap need one each
+ *   workspace    moe_balance_loss_workspace_bytes(T, E, S) bytes (0: none needed, may be NULL),
+ *                16-byte aligned, contents irrelevant; calls that may overlap need one each
  * Sums in fp32 and above in a fixed order: deterministic. NaN and +inf logits make the losses NaN.
  * Requires 1 <= topk <= min(E, 8), E <= 1024, S >= 1, T topk below 2^31, T below 2^26 and
  * S ceil(E / 64) below 2^23. T == 0 writes zeros. Errors: NULL, SHAPE, ALIGN, FORMAT, UNSUPPORTED,

@@ -35,7 +35,8 @@ int moe_balance_loss(const void* logits, int logits_dtype, const int32_t* topk_i
   if (!counts || !tokens || !prob_mean || !losses || (T > 0 && (!logits || !topk_ids || !lse))) return MXF_ERR_NULL;
   const void* ptrs[] = {logits, topk_ids, seg_offsets, counts, tokens, prob_mean, lse, losses, workspace};
   if (!all_aligned16(ptrs)) return MXF_ERR_ALIGN;
-  if (!workspace || workspace_bytes < moe_balance_loss_workspace_bytes(T, E, S)) return MXF_ERR_WORKSPACE;
+  const size_t need = moe_balance_loss_workspace_bytes(T, E, S);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return MXF_ERR_WORKSPACE;
   mxf::RouteLossArgs a{};
   a.logits = logits;
   a.topk_ids = topk_ids;

@@ -22,10 +22,23 @@ namespace {
 constexpr int kWaves = 8;        // of a forward workgroup
 constexpr int kFinishGroups = 8;  // groups of 64 threads that share a sequence's slots
 
+// Rows [row, row + U) of an [T][E] matrix as a range-checked resource: rows past T read as zeros, and the
+// row's place is a scalar, so that a load costs no address arithmetic.
+template <int U>
+__device__ __forceinline__ buf_rsrc rows_of(const void* p, int64_t row, int64_t T, int E, int bytes) {
+  const int64_t left = min((int64_t)U, T - row);
+  return make_rsrc(static_cast<const char*>(p) + (left > 0 ? row * E * bytes : 0), left > 0 ? (uint32_t)(left * E * bytes) : 0);
+}
+
+// value e (a lane's) of row u
 template <bool kBF16>
-__device__ __forceinline__ float load_logit(const void* p, int64_t i) {
-  if (kBF16) return __uint_as_float((uint32_t)static_cast<const uint16_t*>(p)[i] << 16);
-  return static_cast<const float*>(p)[i];
+__device__ __forceinline__ float load_logit(buf_rsrc r, int u, int E, int e) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  if (kBF16) return __uint_as_float((uint32_t)(uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, 2 * e, 2 * u * E, 0) << 16);
+  return __uint_as_float((uint32_t)__builtin_amdgcn_raw_buffer_load_b32(r, 4 * e, 4 * u * E, 0));
+#else
+  return 0.0f;
+#endif
 }
 
 struct Slots {  // the workspace
@@ -51,15 +64,34 @@ __host__ __device__ inline Slots slots_at(void* ws, int64_t blocks, int64_t S, i
   return s;
 }
 
-// the sequences' bounds, held to [0, T] (no offsets: one sequence of all tokens)
-__device__ __forceinline__ int64_t seg_begin(const RouteLossArgs& a, int s) {
-  return a.seg_offsets ? min(max((int64_t)a.seg_offsets[s], (int64_t)0), a.T) : (s > 0 ? a.T : 0);
-}
+// The sequences' bounds, held to [0, T] (no offsets: one sequence of all tokens). Up to 64 sequences' are
+// read once, one a lane, so that walking them needs no further loads. Used by whole waves.
+struct Bounds {
+  const int32_t* off;
+  int64_t T;
+  int S, begins, ends;
 
-// the first sequence that ends past token t, by a whole wave
-__device__ __forceinline__ int seg_of(const RouteLossArgs& a, int64_t t) {
-  return a.seg_offsets ? first_segment(a.seg_offsets, a.S, t) : 0;
-}
+  __device__ __forceinline__ explicit Bounds(const RouteLossArgs& a) : off(a.seg_offsets), T(a.T), S(a.S), begins(0), ends(0) {
+    if (off && S <= 64) {
+      const int i = min((int)(threadIdx.x & 63), S - 1);
+      begins = off[i];
+      ends = off[i + 1];
+    }
+  }
+  __device__ __forceinline__ int64_t held(int v) const { return min(max((int64_t)v, (int64_t)0), T); }
+  __device__ __forceinline__ int64_t begin(int s) const {
+    return !off ? 0 : held(S <= 64 ? __builtin_amdgcn_readlane(begins, s) : off[s]);
+  }
+  __device__ __forceinline__ int64_t end(int s) const {
+    return !off ? T : held(S <= 64 ? __builtin_amdgcn_readlane(ends, s) : off[s + 1]);
+  }
+  // the first sequence that ends past token t
+  __device__ __forceinline__ int of(int64_t t) const {
+    if (!off) return 0;
+    if (S > 64) return first_segment(off, S, t);
+    return __popcll(__ballot((int)(threadIdx.x & 63) < S && (int64_t)ends <= t));
+  }
+};
 
 __device__ __forceinline__ double wave_sum_f64(double v) {
 #pragma unroll
@@ -67,11 +99,13 @@ __device__ __forceinline__ double wave_sum_f64(double v) {
   return v;
 }
 
-// One workgroup: tokens [tb blockIdx, tb (blockIdx + 1)), sequence after sequence. With one workgroup
-// in the launch it writes the results itself.
-template <bool kBF16, int V>
+// One workgroup: tokens [tb blockIdx, tb (blockIdx + 1)), 8 TW at a time, TW a wave. All loads go out
+// first and the tokens' probabilities are formed without regard to sequences; then the workgroup walks the
+// sequences that meet its tokens and keeps each one's sums in registers until it ends. With one
+// workgroup in the launch it writes the results itself.
+template <bool kBF16, int V, int TW>
 __global__ void __launch_bounds__(64 * kWaves) balance_kernel(RouteLossArgs a, int64_t tb) {
-  constexpr int U = V <= 4 ? 4 : V <= 8 ? 2 : 1;  // tokens of a wave in flight
+  static_assert(TW <= 8, "8 lanes a token for its picks");
   __shared__ float red[kWaves][64 * V];
   __shared__ int32_t cnt[64 * V];
   __shared__ float zred[kWaves];
@@ -82,94 +116,33 @@ __global__ void __launch_bounds__(64 * kWaves) balance_kernel(RouteLossArgs a, i
   const int E = a.E, topk = a.topk;
   const bool alone = gridDim.x == 1;
   const Slots slots = slots_at(a.workspace, gridDim.x, a.S, E);
-  if (blockIdx.x == 0 && tid == 0) *slots.done = 0;
-  for (int e = tid; e < 64 * V; e += 64 * kWaves) cnt[e] = 0;
-  __syncthreads();
+  if (!alone && blockIdx.x == 0 && tid == 0) *slots.done = 0;
 
   double balance = 0.0, zsum = 0.0;  // of this thread / thread 0
   int64_t total = 0;
   int held = 0;
-  int64_t covered = t0;
-  auto uncovered = [&](int64_t to) {
-    for (int64_t t = covered + tid; t < to; t += 64 * kWaves) a.lse[t] = -INFINITY;
-    covered = max(covered, to);
-  };
+  const Bounds seg(a);
+  int s = -1;
+  float P[V] = {}, z = 0.0f;  // of this wave, for the sequence s
+  int n = 0;
 
-  for (int s = alone ? 0 : seg_of(a, t0); s < a.S; ++s) {
-    const int64_t begin = seg_begin(a, s);
-    if (begin >= t1 && !alone) break;
-    const int64_t lo = max(begin, covered), hi = min(seg_begin(a, s + 1), t1);
-    if (lo >= hi) {
-      if (alone) {
-        for (int e = tid; e < E; e += 64 * kWaves) {
-          a.counts[(int64_t)s * E + e] = 0;
-          a.prob_mean[(int64_t)s * E + e] = 0.0f;
-        }
-        if (tid == 0) a.tokens[s] = 0;
-      }
-      continue;
+  // the end of sequence s here: the waves' sums to its slot
+  auto flush = [&]() {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      red[wave][lane + 64 * v] = P[v];
+      P[v] = 0.0f;
     }
-    uncovered(lo);
-    covered = hi;
-
-    float P[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) P[v] = 0.0f;
-    float z = 0.0f;
-    int n = 0;
-    for (int64_t t = lo + wave; t < hi; t += U * kWaves) {
-      float x[U][V];
-      bool use[U];
-      int id[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int64_t tu = t + u * kWaves;
-        use[u] = tu < hi;
-        const int64_t at = use[u] ? tu : t;
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          const int e = lane + 64 * v;
-          x[u][v] = e < E ? load_logit<kBF16>(a.logits, at * E + e) : -INFINITY;
-        }
-        id[u] = lane < topk ? a.topk_ids[at * topk + lane] : -1;
-        if (a.token_mask && a.token_mask[at] == 0) use[u] = false;
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        float m = x[u][0];
-#pragma unroll
-        for (int v = 1; v < V; ++v) m = fmaxf(m, x[u][v]);
-        m = wave_max(m);
-        if (m == -INFINITY) use[u] = false;  // no expert left
-        float sum = 0.0f;
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          x[u][v] = __expf(x[u][v] - m);
-          sum += x[u][v];
-        }
-        sum = wave_sum(sum);
-        const float l = m + logf(sum);
-        const int64_t tu = t + u * kWaves;
-        if (lane == 0 && tu < hi) a.lse[tu] = use[u] ? l : -INFINITY;
-        if (use[u]) {
-          const float inv = 1.0f / sum;
-#pragma unroll
-          for (int v = 0; v < V; ++v) P[v] += x[u][v] * inv;
-          z += l * l;
-          ++n;
-          if ((uint32_t)id[u] < (uint32_t)E) atomicAdd(&cnt[id[u]], 1);
-        }
-      }
-    }
-#pragma unroll
-    for (int v = 0; v < V; ++v) red[wave][lane + 64 * v] = P[v];
     if (lane == 0) {
       zred[wave] = z;
       nred[wave] = n;
     }
+    z = 0.0f;
+    n = 0;
     __syncthreads();
     float zb = 0.0f;
     int nb = 0;
+#pragma unroll
     for (int w = 0; w < kWaves; ++w) {
       zb += zred[w];
       nb += nred[w];
@@ -203,8 +176,86 @@ __global__ void __launch_bounds__(64 * kWaves) balance_kernel(RouteLossArgs a, i
     total += nb;
     held += nb > 0;
     __syncthreads();
+  };
+
+  for (int64_t base = t0; base < t1 || (alone && base == t0); base += kWaves * TW) {
+    const int64_t tw = base + wave * TW, hi = min(base + kWaves * TW, t1);  // the wave's first token
+    float x[TW][V], l[TW];
+    int id = -1;
+    bool masked = false;
+    const buf_rsrc rx = rows_of<TW>(a.logits, tw, a.T, E, kBF16 ? 2 : 4);
+#pragma unroll
+    for (int u = 0; u < TW; ++u)
+#pragma unroll
+      for (int v = 0; v < V; ++v)  // past the experts or tokens: some value, left out below
+        x[u][v] = load_logit<kBF16>(rx, u, E, lane + 64 * v);
+    if (a.T > 0) {
+      id = a.topk_ids[min(tw + (lane >> 3), a.T - 1) * topk + min(lane & 7, topk - 1)];
+      if (a.token_mask) masked = a.token_mask[min(tw + (lane & 7), a.T - 1)] == 0;
+    }
+    if (base == t0) {
+      for (int e = tid; e < 64 * V; e += 64 * kWaves) cnt[e] = 0;
+      if (s < 0) s = alone ? 0 : seg.of(t0);
+      __syncthreads();
+    }
+    uint32_t use = 0;  // bit u: token tw + u is here and some of its experts are left
+    const uint32_t out = (uint32_t)__ballot(masked);
+#pragma unroll
+    for (int u = 0; u < TW; ++u) {
+      float m = -INFINITY;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        if (lane + 64 * v >= E) x[u][v] = -INFINITY;
+        m = fmaxf(m, x[u][v]);
+      }
+      m = wave_max(m);
+      float sum = 0.0f;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        x[u][v] = __expf(x[u][v] - m);
+        sum += x[u][v];
+      }
+      sum = wave_sum(sum);
+      l[u] = m + logf(sum);
+      const float inv = 1.0f / sum;
+#pragma unroll
+      for (int v = 0; v < V; ++v) x[u][v] *= inv;
+      if (tw + u < hi && m != -INFINITY && !(out >> u & 1)) use |= 1u << u;
+    }
+
+    uint32_t counted = 0;
+    while (s < a.S) {
+      const int64_t from = seg.begin(s), to = seg.end(s);
+      if (from >= hi && !(alone && hi >= t1)) break;  // it begins later
+#pragma unroll
+      for (int u = 0; u < TW; ++u) {
+        if ((use >> u & 1) && tw + u >= from && tw + u < to) {
+          counted |= 1u << u;
+#pragma unroll
+          for (int v = 0; v < V; ++v) P[v] += x[u][v];
+          z += l[u] * l[u];
+          ++n;
+        }
+      }
+      const int64_t mine = tw + (lane >> 3);
+      if ((lane >> 3) < TW && (lane & 7) < topk && (use >> (lane >> 3) & 1) && mine >= from && mine < to &&
+          (uint32_t)id < (uint32_t)E)
+        atomicAdd(&cnt[id], 1);
+      const bool more = to > hi;            // it goes on behind these tokens
+      if (more && hi < t1) break;           // in this workgroup
+      if (from < to || alone) {
+        __syncthreads();
+        flush();
+      }
+      if (more) break;
+      ++s;
+    }
+    float mine = -INFINITY;
+#pragma unroll
+    for (int u = 0; u < TW; ++u)
+      if (lane == u && (counted >> u & 1)) mine = l[u];
+    if (lane < TW && tw + lane < hi) a.lse[tw + lane] = mine;
   }
-  uncovered(t1);
   if (alone) {
     balance = wave_sum_f64(balance);
     if (lane == 0) bred[wave] = balance;
@@ -233,19 +284,30 @@ __global__ void __launch_bounds__(64 * kFinishGroups) balance_finish_kernel(Rout
   const int E = a.E, EB = (E + 63) / 64;
   const Slots slots = slots_at(a.workspace, blocks, a.S, E);
   const int s = blockIdx.x / EB, eb = blockIdx.x % EB, e = 64 * eb + lane;
-  const int64_t lo = seg_begin(a, s), hi = seg_begin(a, s + 1);
+  const Bounds seg(a);
+  const int64_t lo = seg.begin(s), hi = seg.end(s);
   const int64_t b0 = lo / tb, b1 = lo < hi ? (hi - 1) / tb + 1 : b0;
   float p = 0.0f, z = 0.0f;
   int32_t c = 0, n = 0;
-#pragma unroll 4
-  for (int64_t b = b0 + grp; b < b1; b += kFinishGroups) {
-    const int64_t slot = b + s;
-    if (e < E) {
-      p += slots.p[slot * E + e];
-      c += slots.c[slot * E + e];
+  for (int64_t b = b0 + grp; b < b1; b += 4 * kFinishGroups) {  // four slots' loads in flight
+    float ps[4], zs[4];
+    int32_t cs[4], ns[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t slot = min(b + i * kFinishGroups, b1 - 1) + s;
+      ps[i] = slots.p[slot * E + min(e, E - 1)];
+      cs[i] = slots.c[slot * E + min(e, E - 1)];
+      zs[i] = slots.z[slot];
+      ns[i] = slots.n[slot];
     }
-    z += slots.z[slot];
-    n += slots.n[slot];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const bool in = b + i * kFinishGroups < b1;
+      p += in ? ps[i] : 0.0f;
+      c += in ? cs[i] : 0;
+      z += in ? zs[i] : 0.0f;
+      n += in ? ns[i] : 0;
+    }
   }
   pred[grp][lane] = p;
   cred[grp][lane] = c;
@@ -322,123 +384,141 @@ __global__ void __launch_bounds__(64 * kFinishGroups) balance_finish_kernel(Rout
   }
 }
 
-// d logits: one wave per token
+// d logits: one token a wave (two or four took 14 us where this takes 11, 16384 x 256 fp32: more waves have
+// the loads' and the stores' turns beside each other). All loads that need no other go out first.
 template <bool kBF16, int V>
 __global__ void __launch_bounds__(256) route_backward_kernel(RouteLossArgs a) {
   const int lane = threadIdx.x & 63;
   const int64_t t = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if (t >= a.T) return;
   const int E = a.E, topk = a.topk;
-  float x[V];
   const bool losses = a.dlosses != nullptr;
-  float l = -INFINITY;
+  float x[V], d[V], l = -INFINITY, g = 0.0f, dg = 0.0f;
+  int id = -1;
   if (losses) {
+    const buf_rsrc rx = rows_of<1>(a.logits, t, a.T, E, kBF16 ? 2 : 4);
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int e = lane + 64 * v;
-      x[v] = e < E ? load_logit<kBF16>(a.logits, t * E + e) : -INFINITY;
-    }
+    for (int v = 0; v < V; ++v) x[v] = load_logit<kBF16>(rx, 0, E, lane + 64 * v);
     l = a.lse[t];
   }
-  float g = 0.0f, dg = 0.0f;
-  int id = -1;
-  if (a.dgates && lane < topk) {
-    g = a.gates[t * topk + lane];
-    dg = a.dgates[t * topk + lane];
-    id = a.topk_ids[t * topk + lane];
+  if (a.dgates) {  // lanes past topk: zeros, out of the row's range
+    g = load_logit<false>(rows_of<1>(a.gates, t, a.T, topk, 4), 0, 0, lane);
+    dg = load_logit<false>(rows_of<1>(a.dgates, t, a.T, topk, 4), 0, 0, lane);
+    id = (int)__float_as_uint(load_logit<false>(rows_of<1>(a.topk_ids, t, a.T, topk, 4), 0, 0, lane));
   }
-  float d[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) d[v] = 0.0f;
-  if (l != -INFINITY) {
-    const int s = seg_of(a, t);
-    if (s < a.S) {
-      const float n = (float)a.tokens[s], total = (float)a.tokens[a.S], held = (float)a.tokens[a.S + 1];
-      const float kb = a.dlosses[0] * ((float)E / ((float)topk * held)) / n, kz = a.dlosses[1] * 2.0f * l / total;
-      // p from the row itself: lse holds log(sum exp(x - max)) only as far as the maximum's size leaves it bits
-      float m = x[0];
+  if (losses) {
+    const Bounds seg(a);
+    const float gb = a.dlosses[0], gz = a.dlosses[1];
+    const float total = (float)a.tokens[a.S], held = (float)a.tokens[a.S + 1];
+    const int s = min(seg.of(t), a.S - 1);
+    const float n = (float)a.tokens[s];
+    const buf_rsrc rc = rows_of<1>(a.counts, s, a.S, E, 4);
+    float c[V], m = -INFINITY, sum = 0.0f, dot = 0.0f;
 #pragma unroll
-      for (int v = 1; v < V; ++v) m = fmaxf(m, x[v]);
-      m = wave_max(m);
-      float c[V], dot = 0.0f, sum = 0.0f;
+    for (int v = 0; v < V; ++v) c[v] = (float)(int)__float_as_uint(load_logit<false>(rc, 0, 0, lane + 64 * v));
+    // p from the row itself: lse holds log(sum exp(x - max)) only as far as the maximum's size leaves it bits
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const int e = lane + 64 * v;
-        c[v] = e < E ? (float)a.counts[(int64_t)s * E + e] / n : 0.0f;
-        x[v] = __expf(x[v] - m);
-        sum += x[v];
-        dot += x[v] * c[v];
-      }
-      const float inv = 1.0f / wave_sum(sum);
-      dot = wave_sum(dot) * inv;
+    for (int v = 0; v < V; ++v) {
+      if (lane + 64 * v >= E) x[v] = -INFINITY;
+      m = fmaxf(m, x[v]);
+    }
+    m = wave_max(m);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      x[v] = __expf(x[v] - m);
+      sum += x[v];
+    }
+    const float inv = 1.0f / wave_sum(sum);
+#pragma unroll
+    for (int v = 0; v < V; ++v) dot += x[v] * c[v];
+    dot = wave_sum(dot) * inv;
+    if (l != -INFINITY) {  // the token counts
+      const float kb = gb * ((float)E / ((float)topk * held)) / (n * n), kz = gz * 2.0f * l / total;
 #pragma unroll
       for (int v = 0; v < V; ++v) d[v] = x[v] * inv * (kb * (c[v] - dot) + kz);
     }
   }
   if (a.dgates) {
-    const float mine = g * (dg - wave_sum(g * dg));
-    for (int j = 0; j < topk; ++j) {
+    float dot = g * dg;  // over the first 8 lanes
+    dot += dpp_move<0xB1>(dot);
+    dot += dpp_move<0x4E>(dot);
+    dot += dpp_move<0x141>(dot);
+    const float mine = g * (dg - dot);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (j >= topk) break;
       const int ij = __builtin_amdgcn_readlane(id, j);
       const float dj = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(mine), j));
+      const float add = lane == (ij & 63) ? dj : 0.0f;
 #pragma unroll
       for (int v = 0; v < V; ++v)
-        if (ij == lane + 64 * v) d[v] += dj;
+        if (ij >> 6 == v) d[v] += add;  // the whole wave takes one of these
     }
   }
+  const buf_rsrc ro = rows_of<1>(a.dlogits, t, a.T, E, kBF16 ? 2 : 4);
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const int e = lane + 64 * v;
-    if (e < E) {
-      if (kBF16) static_cast<__bf16*>(a.dlogits)[t * E + e] = (__bf16)d[v];
-      else static_cast<float*>(a.dlogits)[t * E + e] = d[v];
-    }
+  for (int v = 0; v < V; ++v) {  // lanes past the experts are out of the row's range
+#if defined(__HIP_DEVICE_COMPILE__)
+    if (kBF16) __builtin_amdgcn_raw_buffer_store_b16((short)bf16x2_bits(d[v], 0.0f), ro, 2 * lane, 128 * v, 0);
+    else __builtin_amdgcn_raw_buffer_store_b32((int)__float_as_uint(d[v]), ro, 4 * lane, 256 * v, 0);
+#endif
   }
 }
 
-// Tokens of a forward workgroup: at least 64, and at most 1024 workgroups. At most 64 tokens are one
-// workgroup that writes the results itself (no second launch).
-int64_t tokens_per_block(int64_t T) { return cdiv(max(T, (int64_t)1), 1024) > 64 ? cdiv(T, 1024) : 64; }
+// How the forward pass deals out T tokens: at most 64 are one workgroup that writes the results itself;
+// else 2 a wave, so that few tokens are many workgroups, or 8, and at most 1024 workgroups.
+struct Deal {
+  int tw;
+  int64_t tb, blocks;
+};
+Deal deal_of(int64_t T) {
+  if (T <= 64) return {8, 64, 1};
+  const int tw = T < 16384 ? 2 : 8;
+  const int64_t one = kWaves * tw, tb = one * cdiv(cdiv(T, one), 1024);
+  return {tw, tb, cdiv(T, tb)};
+}
 
-template <bool kBF16>
-void launch_forward(const RouteLossArgs& a, int64_t tb, unsigned blocks, hipStream_t stream) {
-  const dim3 threads(64 * kWaves);
-  if (a.E <= 64) balance_kernel<kBF16, 1><<<blocks, threads, 0, stream>>>(a, tb);
-  else if (a.E <= 128) balance_kernel<kBF16, 2><<<blocks, threads, 0, stream>>>(a, tb);
-  else if (a.E <= 256) balance_kernel<kBF16, 4><<<blocks, threads, 0, stream>>>(a, tb);
-  else if (a.E <= 512) balance_kernel<kBF16, 8><<<blocks, threads, 0, stream>>>(a, tb);
-  else balance_kernel<kBF16, 16><<<blocks, threads, 0, stream>>>(a, tb);
+template <bool kBF16, int V>
+void launch_forward(const RouteLossArgs& a, const Deal& d, hipStream_t stream) {
+  if (d.tw == 2) balance_kernel<kBF16, V, 2><<<(unsigned)d.blocks, 64 * kWaves, 0, stream>>>(a, d.tb);
+  else balance_kernel<kBF16, V, 8><<<(unsigned)d.blocks, 64 * kWaves, 0, stream>>>(a, d.tb);
+}
+
+template <bool kBF16, int V>
+void launch_backward(const RouteLossArgs& a, hipStream_t stream) {
+  route_backward_kernel<kBF16, V><<<(unsigned)cdiv(a.T, 4), 256, 0, stream>>>(a);
 }
 
 template <bool kBF16>
-void launch_backward(const RouteLossArgs& a, hipStream_t stream) {
-  const dim3 grid((unsigned)cdiv(a.T, 4)), threads(256);
-  if (a.E <= 64) route_backward_kernel<kBF16, 1><<<grid, threads, 0, stream>>>(a);
-  else if (a.E <= 128) route_backward_kernel<kBF16, 2><<<grid, threads, 0, stream>>>(a);
-  else if (a.E <= 256) route_backward_kernel<kBF16, 4><<<grid, threads, 0, stream>>>(a);
-  else if (a.E <= 512) route_backward_kernel<kBF16, 8><<<grid, threads, 0, stream>>>(a);
-  else route_backward_kernel<kBF16, 16><<<grid, threads, 0, stream>>>(a);
+void launch_both(const RouteLossArgs& a, bool backward, hipStream_t stream) {
+  const Deal d = deal_of(a.T);
+  if (a.E <= 64) backward ? launch_backward<kBF16, 1>(a, stream) : launch_forward<kBF16, 1>(a, d, stream);
+  else if (a.E <= 128) backward ? launch_backward<kBF16, 2>(a, stream) : launch_forward<kBF16, 2>(a, d, stream);
+  else if (a.E <= 256) backward ? launch_backward<kBF16, 4>(a, stream) : launch_forward<kBF16, 4>(a, d, stream);
+  else if (a.E <= 512) backward ? launch_backward<kBF16, 8>(a, stream) : launch_forward<kBF16, 8>(a, d, stream);
+  else backward ? launch_backward<kBF16, 16>(a, stream) : launch_forward<kBF16, 16>(a, d, stream);
 }
 
 }  // namespace
 
 size_t route_loss_workspace(int64_t T, int64_t E, int64_t S) {
-  const int64_t blocks = cdiv(max(T, (int64_t)1), tokens_per_block(T));
-  const Slots s = slots_at(nullptr, blocks, S, E);
-  return reinterpret_cast<size_t>(s.done) + sizeof(uint32_t);
+  const Deal d = deal_of(T);
+  if (d.blocks == 1) return 0;
+  return reinterpret_cast<size_t>(slots_at(nullptr, d.blocks, S, E).done) + sizeof(uint32_t);
 }
 
 int launch_route_loss(const RouteLossArgs& a, bool bf16, hipStream_t stream) {
-  const int64_t tb = tokens_per_block(a.T), blocks = cdiv(max(a.T, (int64_t)1), tb);
-  if (bf16) launch_forward<true>(a, tb, (unsigned)blocks, stream);
-  else launch_forward<false>(a, tb, (unsigned)blocks, stream);
-  if (blocks > 1)
-    balance_finish_kernel<<<(unsigned)(a.S * cdiv(a.E, 64)), 64 * kFinishGroups, 0, stream>>>(a, tb, blocks);
+  bf16 ? launch_both<true>(a, false, stream) : launch_both<false>(a, false, stream);
+  const Deal d = deal_of(a.T);
+  if (d.blocks > 1)
+    balance_finish_kernel<<<(unsigned)(a.S * cdiv(a.E, 64)), 64 * kFinishGroups, 0, stream>>>(a, d.tb, d.blocks);
   return hipGetLastError() == hipSuccess ? 0 : -1;
 }
 
 int launch_route_backward(const RouteLossArgs& a, bool bf16, hipStream_t stream) {
-  if (bf16) launch_backward<true>(a, stream);
-  else launch_backward<false>(a, stream);
+  bf16 ? launch_both<true>(a, true, stream) : launch_both<false>(a, true, stream);
   return hipGetLastError() == hipSuccess ? 0 : -1;
 }
 

@@ -612,7 +612,8 @@ def moe_balance_loss(logits, topk_ids, token_mask=None, seg_offsets=None, worksp
         _is(token_mask, "token_mask", (torch.uint8, torch.bool), (T,), i)
     S = _segments(seg_offsets, i)
     need = load().moe_balance_loss_workspace_bytes(T, E, S)
-    workspace = _workspace(workspace, need, topk_ids)
+    if need or workspace is not None:
+        workspace = _workspace(workspace, need, topk_ids)
     counts = topk_ids.new_empty((S, E))
     tokens = topk_ids.new_empty((S + 2,))
     mean = torch.empty((S, E), dtype=torch.float32, device=logits.device)
@@ -620,7 +621,7 @@ def moe_balance_loss(logits, topk_ids, token_mask=None, seg_offsets=None, worksp
     losses = mean.new_empty((2,))
     _call("moe_balance_loss", i, logits.data_ptr(), dt, topk_ids.data_ptr(), _at(token_mask), _at(seg_offsets), S, T, E,
           topk, counts.data_ptr(), tokens.data_ptr(), mean.data_ptr(), lse.data_ptr(), losses.data_ptr(),
-          workspace.data_ptr(), workspace.numel())
+          _at(workspace), need)
     return dict(losses=losses, counts=counts, prob_mean=mean, tokens=tokens, lse=lse)
 
 
