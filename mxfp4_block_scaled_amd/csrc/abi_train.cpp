@@ -1,6 +1,7 @@
 // extern "C" entry points of the operators of training: the router's losses and gradient, the
 // combine's backward pass, 4-bit quantisation both ways. Validation as in abi.cpp.
 #include "abi_checks.hpp"
+#include "fp4_pair_plan.hpp"
 #include "launch.hpp"
 #include "w4a16_plan.hpp"
 
@@ -175,6 +176,15 @@ int fp4_gemm(const uint8_t* a, const uint8_t* a_scale, int64_t M, const uint8_t*
                               c_dtype == MXF_BF16, workspace, as_stream(stream))
              ? MXF_ERR_LAUNCH
              : MXF_OK;
+}
+
+// The tile and K slices of a call of these sizes, as the launcher has them (for tests and profiles)
+int mxf_fp4_pair_plan(int64_t M, int64_t N, int64_t K, int fmt, int32_t* out) {
+  const mxf::Fp4PairPlan p = mxf::fp4_pair_plan(M, N, K, fmt == MXF_W_NVFP4);
+  out[0] = p.bm;
+  out[1] = p.bn;
+  out[2] = p.slices;
+  return 3;
 }
 
 }  // extern "C"

@@ -25,6 +25,131 @@ __global__ void __launch_bounds__(256) fp4_pair_sum_kernel(const float4* part, i
   else static_cast<float4*>(out)[i] = s;
 }
 
+// Few tiles: 32 rows x 32 columns a workgroup, whose 8 waves share K. A wave copies its stages into two LDS
+// slots of its own (whole lines, no barrier among waves) and the waves' sums meet in LDS: one launch, no
+// workspace. The fixed order of the waves keeps results the same from run to run.
+constexpr int kFewWaves = 8;
+struct alignas(16) FewSlot {
+  uint8_t A[32 * 128], B[32 * 128];
+};
+
+template <bool kNV, bool kOutBF16>
+__global__ void __launch_bounds__(64 * kFewWaves) fp4_few_kernel(Fp4PairArgs a) {
+  constexpr int W = kNV ? 2 : 1;
+  __shared__ union {
+    FewSlot ring[kFewWaves][2];
+    float part[kFewWaves][16 * 65];
+  } lds;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, g = lane >> 5,
+            r32 = lane & 31;
+  const int64_t M = a.M, N = a.N, K = a.K, wrow = K / 2, srow = K / (kNV ? 16 : 32);
+  const int64_t row0 = (int64_t)blockIdx.y * 32, col0 = (int64_t)blockIdx.x * 32;
+  const int m = (int)min((int64_t)32, M - row0), n = (int)min((int64_t)32, N - col0);
+  const uint32_t stages = (uint32_t)((K + 255) / 256);
+  const int st0 = (int)w16_share(stages, wave, kFewWaves), nst = (int)w16_share(stages, wave + 1, kFewWaves);
+  const buf_rsrc ra = make_rsrc(a.a + row0 * wrow, (uint32_t)(m * wrow));
+  const buf_rsrc ras = make_rsrc(a.as + row0 * srow, (uint32_t)(m * srow));
+  const buf_rsrc rb = make_rsrc(a.b + col0 * wrow, (uint32_t)(n * wrow));
+  const buf_rsrc rbs = make_rsrc(a.bs + col0 * srow, (uint32_t)(n * srow));
+
+  uint32_t at[4];  // row 8 q + lane / 8, 16-byte chunk lane % 8 of a stage
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int r = 8 * q + (lane >> 3);
+    at[q] = (uint32_t)(r * wrow) + 16 * ((lane & 7) ^ swz_a16(r));
+  }
+  const uint32_t sat = (uint32_t)(r32 * srow) + 4 * W * g;
+  struct Scales {
+    uint32_t a[W], b[W];
+  };
+  auto issue = [&](FewSlot& slot, Scales& sc, int st) __attribute__((always_inline)) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      buf_dma16(rb, slot.B + 1024 * q, at[q], (uint32_t)st * 128);
+      buf_dma16(ra, slot.A + 1024 * q, at[q], (uint32_t)st * 128);
+    }
+#pragma unroll
+    for (int k = 0; k < W; ++k) {
+      sc.b[k] = (uint32_t)buf_load4(rbs, sat + 4 * k, (uint32_t)st * 8 * W);
+      sc.a[k] = (uint32_t)buf_load4(ras, sat + 4 * k, (uint32_t)st * 8 * W);
+    }
+  };
+  v16f acc = v16f{};
+  auto compute = [&](const FewSlot& slot, Scales sc, int st) __attribute__((always_inline)) {
+    if (g == 1 && (int64_t)st * 256 + 128 >= K) {  // the half past K, as in fp4_pair.hpp
+#pragma unroll
+      for (int k = 0; k < W; ++k) sc.a[k] = sc.b[k] = 0;
+    }
+    v4i fa[4], fb[4];
+    const int o = r32 * 128 + 16 * ((4 * g) ^ swz_a16(r32));
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      fa[s] = *reinterpret_cast<const v4i*>(slot.A + (o ^ (16 * s)));
+      fb[s] = *reinterpret_cast<const v4i*>(slot.B + (o ^ (16 * s)));
+    }
+    static_for<0, 4>([&](auto S_) __attribute__((always_inline)) {
+      constexpr int s = decltype(S_)::value;
+      if constexpr (kNV) {
+        const v2h ha = scales_to_half<(s & 1) != 0>(sc.a[s / 2]), hb = scales_to_half<(s & 1) != 0>(sc.b[s / 2]);
+        static_for<0, 4>([&](auto J_) __attribute__((always_inline)) {
+          constexpr int j = decltype(J_)::value;
+          acc = mfma32x32x16h(decode8_half((uint32_t)fb[s][j], hb[j / 2]), decode8_half((uint32_t)fa[s][j], ha[j / 2]), acc);
+        });
+      } else {
+        acc = mfma32x32x64<kFmtFP4, kFmtFP4, s>(v8i{fb[s][0], fb[s][1], fb[s][2], fb[s][3], 0, 0, 0, 0},
+                                                v8i{fa[s][0], fa[s][1], fa[s][2], fa[s][3], 0, 0, 0, 0}, acc,
+                                                (int)sc.b[0], (int)sc.a[0]);
+      }
+    });
+  };
+  FewSlot* const slot = lds.ring[wave];
+  Scales sc[2];
+  // a stage is 8 copies and 2 W loads, which return in order
+  auto step = [&](auto I, int st) __attribute__((always_inline)) {
+    constexpr int i = decltype(I)::value;
+    if (st + 1 < nst) {
+      issue(slot[i ^ 1], sc[i ^ 1], st + 1);
+      wait_vmcnt<8 + 2 * W>();
+    } else {
+      wait_vmcnt<0>();
+    }
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+    compute(slot[i], sc[i], st);
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  if (st0 < nst) issue(slot[0], sc[0], st0);
+  const float ga = a.ga ? *a.ga : 1.0f, gb = a.gb ? *a.gb : 1.0f;
+  for (int st = st0; st < nst; st += 2) {
+    step(std::integral_constant<int, 0>{}, st);
+    if (st + 1 < nst) step(std::integral_constant<int, 1>{}, st + 1);
+  }
+  __syncthreads();  // every wave is done with its slots
+#pragma unroll
+  for (int v = 0; v < 16; ++v) lds.part[wave][65 * v + lane] = acc[v];
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < 1024 / (64 * kFewWaves); ++k) {
+    const int o = (int)threadIdx.x + 64 * kFewWaves * k, r = o >> 5, c = o & 31,
+              from = 65 * (4 * (c >> 3) + (c & 3)) + r + 32 * ((c >> 2) & 1);
+    float s = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kFewWaves; ++w) s += lds.part[w][from];
+    s = s * ga * gb;
+    if (r >= m || c >= n) continue;
+    if (kOutBF16) static_cast<__bf16*>(a.out)[(row0 + r) * N + col0 + c] = (__bf16)s;
+    else static_cast<float*>(a.out)[(row0 + r) * N + col0 + c] = s;
+  }
+}
+
+template <bool kNV>
+void launch_few(const Fp4PairArgs& a, bool out_bf16, hipStream_t stream) {
+  const dim3 grid((unsigned)cdiv(a.N, 32), (unsigned)cdiv(a.M, 32));
+  if (out_bf16) fp4_few_kernel<kNV, true><<<grid, 64 * kFewWaves, 0, stream>>>(a);
+  else fp4_few_kernel<kNV, false><<<grid, 64 * kFewWaves, 0, stream>>>(a);
+}
+
 template <int BM, int BN, int WM, int WN, bool kNV>
 void launch_tile(const Fp4PairArgs& a, bool out_bf16, hipStream_t stream) {
   const dim3 grid((unsigned)(8 * cdiv(cdiv(a.M, BM) * cdiv(a.N, BN), 8)), (unsigned)a.slices), threads(64 * WM * WN);
@@ -35,7 +160,10 @@ void launch_tile(const Fp4PairArgs& a, bool out_bf16, hipStream_t stream) {
 
 template <bool kNV>
 void launch_plan(const Fp4PairPlan& p, const Fp4PairArgs& a, bool out_bf16, hipStream_t stream) {
-  if (p.bm == 256) launch_tile<256, 256, 4, 2, kNV>(a, out_bf16, stream);
+  if (p.bm == 32) launch_few<kNV>(a, out_bf16, stream);
+  else if (p.bm == 256) launch_tile<256, 256, 4, 2, kNV>(a, out_bf16, stream);
+  else if (p.bm == 64 && p.bn == 64) launch_tile<64, 64, 2, 2, kNV>(a, out_bf16, stream);
+  else if (p.bm == 64) launch_tile<64, 128, 2, 2, kNV>(a, out_bf16, stream);
   else launch_tile<128, 128, 2, 2, kNV>(a, out_bf16, stream);
 }
 

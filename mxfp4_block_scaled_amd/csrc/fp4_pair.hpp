@@ -79,9 +79,10 @@ __global__ void __launch_bounds__(64 * WM * WN) fp4_pair_kernel(Fp4PairArgs a) {
   constexpr int IA = BM * 8 / 64 / NW, IB = BN * 8 / 64 / NW;  // 16-byte copies a lane and stage
   constexpr int ISA = BM * 2 / 64, ISB = BN * 2 / 64;          // of a scale group, in all
   constexpr int G = kNV ? 2 : 4, SB = 32 / G;                  // stages and scale bytes a row of a group, a stage
-  static_assert(IA >= 1 && IB >= 1 && ISA % NW == 0 && ISB % NW == 0, "tile shape");
+  constexpr int IS = (ISA + ISB + NW - 1) / NW;                // of them a wave: A's, then B's
+  static_assert(IA >= 1 && IB >= 1, "tile shape");
   __shared__ Fp4PairRing<BM, BN> ring;
-  static_assert(sizeof(ring) <= 160 * 1024 && 2 * BM * 128 + 2 * BN * 128 >= NW * 8192, "LDS");
+  static_assert(sizeof(ring) <= 160 * 1024 && sizeof(ring) >= NW * 8192, "LDS");
 
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, g = lane >> 5,
             r32 = lane & 31;
@@ -102,7 +103,7 @@ __global__ void __launch_bounds__(64 * WM * WN) fp4_pair_kernel(Fp4PairArgs a) {
   const buf_rsrc ras = make_rsrc(a.as + row0 * srow, (uint32_t)(m * srow));
   const buf_rsrc rb = make_rsrc(a.b + col0 * wrow, (uint32_t)(n * wrow));
   const buf_rsrc rbs = make_rsrc(a.bs + col0 * srow, (uint32_t)(n * srow));
-  uint32_t va[IA], vb[IB], vsa[ISA / NW], vsb[ISB / NW];
+  uint32_t va[IA], vb[IB], vs[IS];
 #pragma unroll
   for (int q = 0; q < IA; ++q) {
     const int chunk = (wave * IA + q) * 64 + lane, r = chunk >> 3;
@@ -114,14 +115,9 @@ __global__ void __launch_bounds__(64 * WM * WN) fp4_pair_kernel(Fp4PairArgs a) {
     vb[q] = (uint32_t)(r * wrow + 16 * ((chunk & 7) ^ swz_a16(r)));
   }
 #pragma unroll
-  for (int q = 0; q < ISA / NW; ++q) {
-    const int piece = (wave * (ISA / NW) + q) * 64 + lane;
-    vsa[q] = (uint32_t)((piece >> 1) * srow + 16 * (piece & 1));
-  }
-#pragma unroll
-  for (int q = 0; q < ISB / NW; ++q) {
-    const int piece = (wave * (ISB / NW) + q) * 64 + lane;
-    vsb[q] = (uint32_t)((piece >> 1) * srow + 16 * (piece & 1));
+  for (int q = 0; q < IS; ++q) {
+    const int p = wave + NW * q, piece = (p < ISA ? p : p - ISA) * 64 + lane;
+    vs[q] = (uint32_t)((piece >> 1) * srow + 16 * (piece & 1));
   }
   auto issue = [&](int slot, int st) {
 #pragma unroll
@@ -131,11 +127,11 @@ __global__ void __launch_bounds__(64 * WM * WN) fp4_pair_kernel(Fp4PairArgs a) {
   };
   auto issue_scales = [&](int grp) {
 #pragma unroll
-    for (int q = 0; q < ISA / NW; ++q)
-      buf_dma16(ras, &ring.SA[grp & 1][(wave * (ISA / NW) + q) * 1024], vsa[q], (uint32_t)grp * 32);
-#pragma unroll
-    for (int q = 0; q < ISB / NW; ++q)
-      buf_dma16(rbs, &ring.SB[grp & 1][(wave * (ISB / NW) + q) * 1024], vsb[q], (uint32_t)grp * 32);
+    for (int q = 0; q < IS; ++q) {
+      const int p = wave + NW * q;
+      if (p < ISA) buf_dma16(ras, &ring.SA[grp & 1][p * 1024], vs[q], (uint32_t)grp * 32);
+      else if (p < ISA + ISB) buf_dma16(rbs, &ring.SB[grp & 1][(p - ISA) * 1024], vs[q], (uint32_t)grp * 32);
+    }
   };
   issue_scales(st0 / G);
   issue(0, st0);
@@ -259,7 +255,7 @@ static_for<0, 4>([&](auto J_) __attribute__((always_inline)) {
   constexpr int ES = kOutBF16 ? 2 : 4, PF = FN * 32 * ES > 256 ? 256 / (32 * ES) : FN;
   constexpr int RB = PF * 32 * ES, NCH = RB / 16;
   static_assert(FN % PF == 0, "passes");
-  uint8_t* const stg = &ring.A[0][0] + wave * 8192;
+  uint8_t* const stg = reinterpret_cast<uint8_t*>(&ring) + wave * 8192;
   uint8_t* const out = static_cast<uint8_t*>(a.out) + (kSlices ? (int64_t)blockIdx.y * M * N * 4 : 0);
 #pragma unroll
   for (int i = 0; i < FM; ++i)

@@ -5,20 +5,55 @@
 
 namespace mxf {
 
+// bm == 32: the kernel of few tiles (32 x 32); slices > 1: sums of K slices through the workspace
 struct Fp4PairPlan {
   int bm, bn, slices;
 };
 
+// The shape with the least estimated time: a launch, then for each 256-k stage the length of one
+// workgroup's stage (copy, barrier, decoding and MFMAs after each other) or, with k workgroups for each
+// compute unit, their k shares of its work, whichever is longer; K slices add their sum's launch and
+// traffic. Below the constants (us), fitted to these times (us: 32 x 32 | 64 x 64 | 64 x 128 | 128 x 128 |
+// 256 x 256; 4s: 64 x 128 in 4 slices):
+//                      NVFP4                               MXFP4
+//   128 x 7168 x 4096    24 | 20 | 25 | 34 | 54              16 | 11 | 12 | 16 | 21
+//   256 x 2048 x 2048    7.9 | 11 | 14 | 19 | 46             6.1 | 6.1 | 7.0 | 9.5 | 18
+//   256 x 4096 x 7168    37 | 31 | 40 | 57 | 149  4s 28      23 | 17 | 20 | 25 | 49  4s 18
+//   512 x 1024 x 16384   38 | 67 | 88 | 126 | 333  4s 30     23 | 34 | 39 | 51 | 103  4s 18
+//   512 x 4096 x 7168    73 | 51 | 43 | 57 | 149             42 | 18 | 21 | 25 | 49
+//   1024 x 2048 x 2048   28 | 16 | 15 | 20 | 46              21 | 7.4 | 7.6 | 10 | 18
+//   1024 x 4096 x 7168   136 | 84 | 71 | 62 | 149            80 | 31 | 24 | 26 | 48
+//   2000 x 4096 x 2048   98 | 53 | 42 | 34 | 48              73 | 20 | 17 | 14 | 19
+//   3000 x 3008 x 4096   182 | 103 | 92 | 86 | 89            119 | 40 | 38 | 35 | 31
+//   4096 x 4096 x 7168   513 | 316 | 268 | 215 | 187         311 | 116 | 99 | 77 | 64
 inline Fp4PairPlan fp4_pair_plan(int64_t M, int64_t N, int64_t K, bool nv) {
-  const int64_t t256 = cdiv(M, 256) * cdiv(N, 256), stages = cdiv(K, 256);
-  if (t256 >= 192) return {256, 256, 1};
-  const int64_t t128 = cdiv(M, 128) * cdiv(N, 128);
-  int64_t s = t128 >= 256 ? 1 : 512 / t128;
-  if (s > stages / 2) s = stages / 2;
-  if (s > 16) s = 16;
-  if (s < 1) s = 1;
-  (void)nv;
-  return {128, 128, (int)s};
+  struct Shape {
+    int bm, bn;
+    float stage[2], work[2];  // MXFP4, NVFP4
+  };
+  constexpr Shape kShapes[] = {{32, 32, {0.14f, 0.27f}, {0.165f, 0.29f}},
+                               {64, 64, {0.48f, 0.98f}, {0.245f, 0.68f}},
+                               {64, 128, {0.58f, 1.35f}, {0.40f, 1.1f}},
+                               {128, 128, {0.75f, 1.9f}, {0.65f, 1.88f}},
+                               {256, 256, {1.6f, 5.2f}, {2.1f, 6.4f}}};
+  const int64_t stages = cdiv(K, 256);
+  Fp4PairPlan best{256, 256, 1};
+  float least = 3.0e38f;
+  for (const Shape& t : kShapes) {
+    const int64_t tiles = cdiv(M, t.bm) * cdiv(N, t.bn);
+    for (int s = 1; s <= 8 && s <= stages; s *= 2) {
+      if (s > 1 && (t.bm == 32 || tiles * s > 512)) break;
+      const float units = (float)(tiles * s) / 256.0f, k = units > 1.0f ? (float)cdiv(tiles * s, 256) : units;
+      const float stage = t.stage[nv] > k * t.work[nv] ? t.stage[nv] : k * t.work[nv];
+      float us = 3.0f + (float)cdiv(stages, s) * stage;
+      if (s > 1) us += 4.5f + (float)s * (float)M * (float)N * 8.0f / 5.0e6f;
+      if (us < least) {
+        least = us;
+        best = {t.bm, t.bn, s};
+      }
+    }
+  }
+  return best;
 }
 
 }  // namespace mxf

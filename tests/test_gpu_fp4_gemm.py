@@ -4,6 +4,8 @@ Products are exact in the matrix instructions; a sum of K of them in fp32 takes 
 8 or more products adds up without rounding but one at its end, then steps, K slices), each off by less than 2^-23 of
 the sum of magnitudes. bf16 results add half a step, 2^-8 of the value."""
 
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -43,9 +45,28 @@ def _check(got, a, sa, b, sb, fmt, ga=1.0, gb=1.0):
     assert ((got.double() - want).abs() <= tol + 1e-40).all()
 
 
+def _plan(M, N, K, fmt):
+    out = (ctypes.c_int32 * 3)()
+    fn = ops.load().mxf_fp4_pair_plan
+    fn.argtypes = [ctypes.c_int64] * 3 + [ctypes.c_int, ctypes.c_void_p]
+    fn(M, N, K, ops.WEIGHT_FMTS[fmt], out)
+    return f"{out[0]} x {out[1]}" + (", sliced" if out[2] > 1 else "")
+
+
 SIZES = [(1, 16, 128), (1, 4096, 7168), (5, 48, 384), (8, 512, 16384), (31, 528, 1152), (33, 64, 256), (64, 4096, 2048),
          (100, 96, 4096), (128, 128, 512), (129, 144, 640), (300, 1040, 2048), (257, 272, 7168), (1000, 2064, 896),
-         (2048, 2048, 1024), (4000, 3344, 1408)]
+         (2048, 2048, 1024), (4000, 3344, 1408), (96, 4096, 7168), (200, 4096, 7168), (500, 4112, 7040), (500, 1040, 16256),
+         (129, 7184, 4096), (1000, 4080, 1920), (2000, 4112, 2176), (100, 272, 16256),
+         (300, 4816, 128), (800, 4816, 128), (1000, 2064, 2048), (5600, 144, 16256),
+         (310, 2720, 1024), (54, 5680, 8192)]
+
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+def test_every_kernel_is_among_the_sizes(fmt):
+    plans = {_plan(*s, fmt) for s in SIZES}
+    assert {"32 x 32", "64 x 64", "64 x 128", "128 x 128", "256 x 256"} <= plans
+    assert {"64 x 64, sliced", "128 x 128, sliced", "256 x 256, sliced"} <= plans
+    assert fmt == "mxfp4" or "64 x 128, sliced" in plans
 
 
 @pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
