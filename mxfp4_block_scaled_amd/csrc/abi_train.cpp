@@ -93,7 +93,7 @@ int moe_combine_backward(const void* dout, int dout_dtype, const void* y, int y_
   if (T < 0 || y_rows < 0 || topk < 1 || topk > 8 || H <= 0 || H % 8 != 0) return MXF_ERR_SHAPE;
   if (T * (int64_t)topk > kMaxRows || y_rows > kMaxRows || H > kMaxRows) return MXF_ERR_UNSUPPORTED;
   const int64_t groups = T * mxf::cdiv(topk, mxf::combine_backward_pairs(T, topk));
-  if (groups * mxf::combine_backward_threads(H) > mxf::kMaxThreads) return MXF_ERR_UNSUPPORTED;
+  if (groups * mxf::combine_backward_threads(H, dout_dtype == MXF_BF16 && y_dtype == MXF_BF16) > mxf::kMaxThreads) return MXF_ERR_UNSUPPORTED;
   if (T == 0) return MXF_OK;
   if (!dout || !gates || !pair_row || (!dy && !dgates) || (dgates && !y && y_rows > 0)) return MXF_ERR_NULL;
   const void* ptrs[] = {dout, y, gates, pair_row, dy, dgates};

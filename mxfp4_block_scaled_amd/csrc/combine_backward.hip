@@ -10,39 +10,34 @@ namespace mxf {
 
 namespace {
 
-typedef unsigned int u4v __attribute__((ext_vector_type(4)));
-
-template <bool kBF16>
-struct Eight {  // 8 consecutive values as they lie in memory
-  u4v w[kBF16 ? 1 : 2];
+// P consecutive values as they lie in memory: 16 bytes of the wider type, so that a wave's loads and
+// stores are whole lines (4 fp32 values beside 4 bf16 ones of 8 bytes, or 8 bf16 ones)
+template <bool kBF16, int P>
+struct Part {
+  static constexpr int W = kBF16 ? P / 2 : P;  // words
+  typedef unsigned int Words __attribute__((ext_vector_type(W)));
+  Words w;
   __device__ __forceinline__ void load(const void* p, int64_t at) {
-    const u4v* src = reinterpret_cast<const u4v*>(static_cast<const char*>(p) + at * (kBF16 ? 2 : 4));
-#pragma unroll
-    for (int i = 0; i < (kBF16 ? 1 : 2); ++i) w[i] = __builtin_nontemporal_load(src + i);
+    w = __builtin_nontemporal_load(reinterpret_cast<const Words*>(static_cast<const char*>(p) + at * (kBF16 ? 2 : 4)));
   }
   __device__ __forceinline__ float get(int i) const {
-    if (kBF16) return __uint_as_float(i & 1 ? w[0][i / 2] & 0xFFFF0000u : w[0][i / 2] << 16);
-    return __uint_as_float(w[i / 4][i % 4]);
+    if (kBF16) return __uint_as_float(i & 1 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
+    return __uint_as_float(w[i]);
+  }
+  __device__ static __forceinline__ void store(void* p, int64_t at, const float (&v)[P]) {
+    Words d;
+#pragma unroll
+    for (int i = 0; i < W; ++i) d[i] = kBF16 ? bf16x2_bits(v[(2 * i) % P], v[(2 * i + 1) % P]) : __float_as_uint(v[i % P]);
+    __builtin_nontemporal_store(d, reinterpret_cast<Words*>(static_cast<char*>(p) + at * (kBF16 ? 2 : 4)));
   }
 };
 
-template <bool kBF16>
-__device__ __forceinline__ void store8(void* p, int64_t at, const float (&v)[8]) {
-  u4v* dst = reinterpret_cast<u4v*>(static_cast<char*>(p) + at * (kBF16 ? 2 : 4));
-  if (kBF16) {
-    __builtin_nontemporal_store(u4v{bf16x2_bits(v[0], v[1]), bf16x2_bits(v[2], v[3]), bf16x2_bits(v[4], v[5]),
-                                    bf16x2_bits(v[6], v[7])}, dst);
-  } else {
-    __builtin_nontemporal_store(u4v{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])}, dst);
-    __builtin_nontemporal_store(u4v{__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7])}, dst + 1);
-  }
-}
-
-constexpr int kChunks = 2;  // 8-column pieces of a thread per pass
+constexpr int kChunks = 2;  // parts of a thread in a pass
 
 // One workgroup per token and KJ of its pairs.
 template <bool kYBF16, bool kDBF16, int KJ>
 __global__ void __launch_bounds__(512) combine_backward_kernel(CombineBackwardArgs a) {
+  constexpr int P = kYBF16 && kDBF16 ? 8 : 4;
   __shared__ float red[8][KJ];
   const int tid = threadIdx.x, nthr = blockDim.x, wave = tid >> 6, lane = tid & 63;
   const int parts = (a.topk + KJ - 1) / KJ;
@@ -59,13 +54,13 @@ __global__ void __launch_bounds__(512) combine_backward_kernel(CombineBackwardAr
     g[j] = a.gates[p];
     dot[j] = 0.0f;
   }
-  for (int64_t c0 = 0; c0 < a.H; c0 += (int64_t)nthr * 8 * kChunks) {
-    Eight<kDBF16> d[kChunks];
-    Eight<kYBF16> y[KJ][kChunks];
+  for (int64_t c0 = 0; c0 < a.H; c0 += (int64_t)nthr * P * kChunks) {
+    Part<kDBF16, P> d[kChunks];
+    Part<kYBF16, P> y[KJ][kChunks];
     bool ok[kChunks];
 #pragma unroll
     for (int k = 0; k < kChunks; ++k) {
-      const int64_t col = c0 + ((int64_t)k * nthr + tid) * 8;
+      const int64_t col = c0 + ((int64_t)k * nthr + tid) * P;
       ok[k] = col < a.H;
       if (!ok[k]) continue;
       d[k].load(a.dout, t * a.H + col);
@@ -78,22 +73,22 @@ __global__ void __launch_bounds__(512) combine_backward_kernel(CombineBackwardAr
 #pragma unroll
     for (int k = 0; k < kChunks; ++k) {
       if (!ok[k]) continue;
-      const int64_t col = c0 + ((int64_t)k * nthr + tid) * 8;
-      float dv[8];
+      const int64_t col = c0 + ((int64_t)k * nthr + tid) * P;
+      float dv[P];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) dv[i] = d[k].get(i);
+      for (int i = 0; i < P; ++i) dv[i] = d[k].get(i);
 #pragma unroll
       for (int j = 0; j < KJ; ++j) {
         if (row[j] < 0) continue;
         if (a.dgates) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) dot[j] = fmaf(dv[i], y[j][k].get(i), dot[j]);
+          for (int i = 0; i < P; ++i) dot[j] = fmaf(dv[i], y[j][k].get(i), dot[j]);
         }
         if (a.dy) {
-          float v[8];
+          float v[P];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] = g[j] * dv[i];
-          store8<kYBF16>(a.dy, row[j] * a.H + col, v);
+          for (int i = 0; i < P; ++i) v[i] = g[j] * dv[i];
+          Part<kYBF16, P>::store(a.dy, row[j] * a.H + col, v);
         }
       }
     }
@@ -134,10 +129,12 @@ int combine_backward_pairs(int64_t T, int topk) {
   return topk <= 2 ? topk : topk <= 4 ? 4 : topk <= 6 ? 6 : 8;
 }
 
-int combine_backward_threads(int64_t H) { return (int)min(cdiv(H, 8 * kChunks * 64), (int64_t)8) * 64; }
+int combine_backward_threads(int64_t H, bool bf16) {
+  return (int)min(cdiv(H, (bf16 ? 8 : 4) * kChunks * 64), (int64_t)8) * 64;
+}
 
 int launch_combine_backward(const CombineBackwardArgs& a, bool y_bf16, bool dout_bf16, hipStream_t stream) {
-  const int threads = combine_backward_threads(a.H);
+  const int threads = combine_backward_threads(a.H, y_bf16 && dout_bf16);
   if (y_bf16) {
     if (dout_bf16) launch_t<true, true>(a, threads, stream);
     else launch_t<true, false>(a, threads, stream);

@@ -119,7 +119,7 @@ struct CombineBackwardArgs {
   float* dgates;
 };
 int combine_backward_pairs(int64_t T, int topk);
-int combine_backward_threads(int64_t H);
+int combine_backward_threads(int64_t H, bool bf16);  // bf16: y and dout
 int launch_combine_backward(const CombineBackwardArgs& a, bool y_bf16, bool dout_bf16, hipStream_t stream);
 
 // quantisation to MXFP4 / NVFP4 along rows and columns, and back (fp4_quant.hip)
