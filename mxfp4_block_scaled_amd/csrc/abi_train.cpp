@@ -94,7 +94,7 @@ int moe_combine_backward(const void* dout, int dout_dtype, const void* y, int y_
   if (T * (int64_t)topk > kMaxRows || y_rows > kMaxRows || H > kMaxRows) return MXF_ERR_UNSUPPORTED;
   const int64_t groups = T * mxf::cdiv(topk, mxf::combine_backward_pairs(T, topk));
   if (groups * mxf::combine_backward_threads(H, dout_dtype == MXF_BF16 && y_dtype == MXF_BF16) > mxf::kMaxThreads) return MXF_ERR_UNSUPPORTED;
-  if (T == 0) return MXF_OK;
+  if (T == 0 || (y_rows == 0 && !dgates)) return MXF_OK;  // (a dy of no rows has no address)
   if (!dout || !gates || !pair_row || (!dy && !dgates) || (dgates && !y && y_rows > 0)) return MXF_ERR_NULL;
   const void* ptrs[] = {dout, y, gates, pair_row, dy, dgates};
   if (!all_aligned16(ptrs)) return MXF_ERR_ALIGN;

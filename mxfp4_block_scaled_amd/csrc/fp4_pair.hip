@@ -33,6 +33,20 @@ struct alignas(16) FewSlot {
   uint8_t A[32 * 128], B[32 * 128];
 };
 
+// a lane's scales of a stage, one load: 4 UE8M0 or 8 UE4M3 bytes
+template <int W>
+__device__ __forceinline__ void load_scales(buf_rsrc r, uint32_t voff, uint32_t soff, uint32_t (&s)[W]) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  if constexpr (W == 2) {
+    const auto w = __builtin_amdgcn_raw_buffer_load_b64(r, (int)voff, (int)soff, 0);
+    s[0] = w[0];
+    s[1] = w[1];
+  } else {
+    s[0] = __builtin_amdgcn_raw_buffer_load_b32(r, (int)voff, (int)soff, 0);
+  }
+#endif
+}
+
 template <bool kNV, bool kOutBF16>
 __global__ void __launch_bounds__(64 * kFewWaves) fp4_few_kernel(Fp4PairArgs a) {
   constexpr int W = kNV ? 2 : 1;
@@ -68,11 +82,10 @@ __global__ void __launch_bounds__(64 * kFewWaves) fp4_few_kernel(Fp4PairArgs a) 
       buf_dma16(rb, slot.B + 1024 * q, at[q], (uint32_t)st * 128);
       buf_dma16(ra, slot.A + 1024 * q, at[q], (uint32_t)st * 128);
     }
-#pragma unroll
-    for (int k = 0; k < W; ++k) {
-      sc.b[k] = (uint32_t)buf_load4(rbs, sat + 4 * k, (uint32_t)st * 8 * W);
-      sc.a[k] = (uint32_t)buf_load4(ras, sat + 4 * k, (uint32_t)st * 8 * W);
-    }
+    __builtin_amdgcn_sched_barrier(0);  // the copies first: step() counts on it
+    load_scales(rbs, sat, (uint32_t)st * 8 * W, sc.b);
+    load_scales(ras, sat, (uint32_t)st * 8 * W, sc.a);
+    __builtin_amdgcn_sched_barrier(0);
   };
   v16f acc = v16f{};
   auto compute = [&](const FewSlot& slot, Scales sc, int st) __attribute__((always_inline)) {
@@ -104,12 +117,13 @@ __global__ void __launch_bounds__(64 * kFewWaves) fp4_few_kernel(Fp4PairArgs a) 
   };
   FewSlot* const slot = lds.ring[wave];
   Scales sc[2];
-  // a stage is 8 copies and 2 W loads, which return in order
+  // A stage is 8 copies, then 2 loads; they return in order, so once at most the 10 of the next stage are
+  // outstanding the copies of this one have landed. No barrier: the slots are the wave's own.
   auto step = [&](auto I, int st) __attribute__((always_inline)) {
     constexpr int i = decltype(I)::value;
     if (st + 1 < nst) {
       issue(slot[i ^ 1], sc[i ^ 1], st + 1);
-      wait_vmcnt<8 + 2 * W>();
+      wait_vmcnt<10>();
     } else {
       wait_vmcnt<0>();
     }

@@ -381,11 +381,16 @@ __global__ void __launch_bounds__(512) amax_kernel(const u4v* x, int64_t n, uint
   }
 }
 
-__global__ void __launch_bounds__(512) amax_finish_kernel(const uint32_t* partial, int n, float* scale) {
-  uint32_t m = 0;
-  for (int i = threadIdx.x; i < n; i += 512) m = max(m, partial[i]);
-  m = block_max(m);
-  if (threadIdx.x == 0) *scale = scale_of_amax(m);
+// one wave, all of its loads in flight together
+__global__ void __launch_bounds__(64) amax_finish_kernel(const uint32_t* partial, int n, float* scale) {
+  uint32_t m[kAmaxBlocks / 64];
+#pragma unroll
+  for (int i = 0; i < kAmaxBlocks / 64; ++i) m[i] = partial[min((int)threadIdx.x + 64 * i, n - 1)];
+#pragma unroll
+  for (int i = 1; i < kAmaxBlocks / 64; ++i) m[0] = max(m[0], m[i]);
+#pragma unroll
+  for (int d = 32; d >= 1; d >>= 1) m[0] = max(m[0], (uint32_t)__shfl_xor((int)m[0], d));
+  if (threadIdx.x == 0) *scale = scale_of_amax(m[0]);
 }
 
 template <bool kBF16, bool kNV, bool kSR>
@@ -429,7 +434,7 @@ int launch_nvfp4_tensor_scale(const void* x, bool bf16, int64_t n16, float* scal
   const u4v* p = static_cast<const u4v*>(x);
   if (bf16) amax_kernel<true><<<blocks, 512, 0, stream>>>(p, n16, partial, scale);
   else amax_kernel<false><<<blocks, 512, 0, stream>>>(p, n16, partial, scale);
-  if (blocks > 1) amax_finish_kernel<<<1, 512, 0, stream>>>(partial, blocks, scale);
+  if (blocks > 1) amax_finish_kernel<<<1, 64, 0, stream>>>(partial, blocks, scale);
   return hipGetLastError() == hipSuccess ? 0 : -1;
 }
 

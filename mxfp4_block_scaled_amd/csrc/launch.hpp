@@ -130,7 +130,7 @@ struct Fp4QuantArgs {
   const uint8_t* rnd;
   uint8_t *q, *q_scale, *qt, *qt_scale;
 };
-constexpr int kAmaxBlocks = 1024;
+constexpr int kAmaxBlocks = 512;
 int launch_fp4_quantize(const Fp4QuantArgs& a, bool x_bf16, bool nvfp4, hipStream_t stream);
 int launch_fp4_dequantize(const uint8_t* q, const uint8_t* q_scale, int64_t blocks32, bool nvfp4,
                           const float* tensor_scale, void* out, bool out_bf16, hipStream_t stream);
