@@ -541,7 +541,7 @@ int fp4_dequantize(const uint8_t* q, const uint8_t* q_scale, int64_t rows, int64
  * A linear layer y = x W^T of [T][I] by [O][I] and its gradients: y = fp4_gemm(q(x), q(W)), dx =
  * fp4_gemm(q(dy), qt(W)), dW = fp4_gemm(qt(dy), qt(x)), q and qt as fp4_quantize's.
  * Every product is exact (NVFP4: code x scale is exact in the fp16 operands), accumulation in fp32.
- * Requires K % 128 == 0, N % 16 == 0, K < 2^24, M N < 2^34 and at most 2^22 tiles of 128 x 128. The
+ * Requires K % 128 == 0, N % 16 == 0, K < 2^24, M N < 2^34 and at most 2^21 tiles of 128 x 128. The
  * UE8M0 byte 255 and the UE4M3 byte 0x7F (NaN) are not valid scales. M == 0 is a no-op.
  * Errors: NULL, SHAPE (a tensor scale with MXFP4, too), ALIGN, FORMAT, UNSUPPORTED, WORKSPACE.
  */

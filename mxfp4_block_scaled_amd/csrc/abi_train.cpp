@@ -165,7 +165,7 @@ int fp4_gemm(const uint8_t* a, const uint8_t* a_scale, int64_t M, const uint8_t*
   if (fmt == MXF_W_MXFP4 && (a_tensor_scale || b_tensor_scale)) return MXF_ERR_SHAPE;
   // 32-bit byte offsets inside a tile of 256 rows; items and threads of a launch counted in 32 bits
   if (M > kMaxRows || N > kMaxRows || K >= (int64_t(1) << 24)) return MXF_ERR_UNSUPPORTED;
-  if (mxf::cdiv(M, 128) * mxf::cdiv(N, 128) > (int64_t(1) << 22) || M * N >= (int64_t(1) << 34)) return MXF_ERR_UNSUPPORTED;
+  if (mxf::cdiv(M, 128) * mxf::cdiv(N, 128) > mxf::kMostTiles || M * N >= (int64_t(1) << 34)) return MXF_ERR_UNSUPPORTED;
   if (M == 0) return MXF_OK;
   if (!a || !a_scale || !b || !b_scale || !c) return MXF_ERR_NULL;
   const void* ptrs[] = {a, a_scale, b, b_scale, c, workspace};

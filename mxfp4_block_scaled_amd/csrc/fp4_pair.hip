@@ -57,7 +57,8 @@ __global__ void __launch_bounds__(64 * kFewWaves) fp4_few_kernel(Fp4PairArgs a) 
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, g = lane >> 5,
             r32 = lane & 31;
   const int64_t M = a.M, N = a.N, K = a.K, wrow = K / 2, srow = K / (kNV ? 16 : 32);
-  const int64_t row0 = (int64_t)blockIdx.y * 32, col0 = (int64_t)blockIdx.x * 32;
+  const uint32_t ntiles = (uint32_t)((N + 31) / 32);
+  const int64_t row0 = (int64_t)(blockIdx.x / ntiles) * 32, col0 = (int64_t)(blockIdx.x % ntiles) * 32;
   const int m = (int)min((int64_t)32, M - row0), n = (int)min((int64_t)32, N - col0);
   const uint32_t stages = (uint32_t)((K + 255) / 256);
   const int st0 = (int)w16_share(stages, wave, kFewWaves), nst = (int)w16_share(stages, wave + 1, kFewWaves);
@@ -159,7 +160,7 @@ __global__ void __launch_bounds__(64 * kFewWaves) fp4_few_kernel(Fp4PairArgs a) 
 
 template <bool kNV>
 void launch_few(const Fp4PairArgs& a, bool out_bf16, hipStream_t stream) {
-  const dim3 grid((unsigned)cdiv(a.N, 32), (unsigned)cdiv(a.M, 32));
+  const unsigned grid = (unsigned)(cdiv(a.N, 32) * cdiv(a.M, 32));  // at most kMostFewTiles
   if (out_bf16) fp4_few_kernel<kNV, true><<<grid, 64 * kFewWaves, 0, stream>>>(a);
   else fp4_few_kernel<kNV, false><<<grid, 64 * kFewWaves, 0, stream>>>(a);
 }

@@ -10,6 +10,10 @@ struct Fp4PairPlan {
   int bm, bn, slices;
 };
 
+// What the launches are held to: fp4_gemm takes at most kMostTiles tiles of 128 x 128 (four times as many
+// of 64 x 64, of 256 threads each: 2^31), and the kernel of 32 x 32 tiles never wins with more than a few rounds of the chip
+constexpr int64_t kMostTiles = int64_t(1) << 21, kMostFewTiles = 4096;
+
 // The shape with the least estimated time: a launch, then for each 256-k stage the length of one
 // workgroup's stage (copy, barrier, decoding and MFMAs after each other) or, with k workgroups for each
 // compute unit, their k shares of its work, whichever is longer; K slices add their sum's launch and
@@ -41,6 +45,7 @@ inline Fp4PairPlan fp4_pair_plan(int64_t M, int64_t N, int64_t K, bool nv) {
   float least = 3.0e38f;
   for (const Shape& t : kShapes) {
     const int64_t tiles = cdiv(M, t.bm) * cdiv(N, t.bn);
+    if (t.bm == 32 && tiles > kMostFewTiles) continue;
     for (int s = 1; s <= 8 && s <= stages; s *= 2) {
       if (s > 1 && (t.bm == 32 || tiles * s > 512)) break;
       const float units = (float)(tiles * s) / 256.0f, k = units > 1.0f ? (float)cdiv(tiles * s, 256) : units;

@@ -156,6 +156,17 @@ def test_a_captured_product_and_other_streams():
         assert torch.equal(held, want)
 
 
+def test_scales_of_the_tensors_as_views_and_long_thin_products():
+    a, sa = _operand(40, 256, "nvfp4", 1)
+    b, sb = _operand(64, 256, "nvfp4", 2)
+    g = torch.tensor([3.0, 0.5, 2.0]).cuda()
+    assert torch.equal(ops.fp4_gemm(a, sa, b, sb, "nvfp4", g[1:2], g[2:3]), ops.fp4_gemm(a, sa, b, sb))
+    for M, N in ((1, 200_000), (150_001, 16)):
+        a, sa = _operand(M, 128, "mxfp4", 3)
+        b, sb = _operand(N, 128, "mxfp4", 4)
+        _check(ops.fp4_gemm(a, sa, b, sb, "mxfp4", out_dtype=torch.float32), a, sa, b, sb, "mxfp4")
+
+
 def test_no_rows_and_refusals():
     b, sb = _operand(32, 256, "nvfp4", 1)
     assert ops.fp4_gemm(b[:0], sb[:0], b, sb).shape == (0, 32)

@@ -69,6 +69,29 @@ def test_sequences(T, offsets):
     _check(*_case(T, 33, 2, T, True), mask.bool(), offsets)
 
 
+@pytest.mark.parametrize("T,offsets", [(64, sorted([i // 2 for i in range(129)])), (20000, [0, 17, 16000, 19990]),
+                                       (70000, [3, 100, 40000, 40001, 69990, 70000])])
+def test_many_tokens_and_more_sequences_than_lanes(T, offsets):
+    """Workgroups that take their tokens in several turns; 128 sequences in one workgroup, half of them empty."""
+    _check(*_case(T, 24, 2, T), None, offsets)
+
+
+def test_views_of_larger_tensors():
+    logits, ids, gates, dgates = (t.cuda() for t in _case(130, 64, 4, 8))
+    mask = torch.ones(200, dtype=torch.uint8).cuda()
+    mask[40] = 0
+    a = ops.moe_balance_loss(logits, ids, mask[1:131])
+    b = ops.moe_balance_loss(logits, ids, mask[1:131].clone())
+    assert torch.equal(a["losses"], b["losses"]) and int(a["tokens"][0]) == 129
+    dl = torch.tensor([9.0, 0.3, 0.2]).cuda()
+    x = ops.moe_route_backward(logits, ids, gates, dgates, a, dl[1:])
+    assert torch.equal(x, ops.moe_route_backward(logits, ids, gates, dgates, a, dl[1:].clone()))
+    with pytest.raises(RuntimeError, match="contiguous"):
+        ops.moe_balance_loss(logits.t().contiguous().t(), ids)
+    with pytest.raises(RuntimeError, match="seg_offsets"):
+        ops.moe_balance_loss(logits, ids, seg_offsets=torch.zeros(1, dtype=torch.int32).cuda())
+
+
 @pytest.mark.parametrize("T", [30, 400])
 def test_nothing_counts(T):
     logits, ids, gates, dgates = _case(T, 48, 3, 1)

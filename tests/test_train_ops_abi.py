@@ -127,6 +127,29 @@ def test_fp4_gemm_errors():
         assert call(fn, good, **change) == want, change
 
 
+def test_every_launch_of_the_product_fits():
+    """Sizes at the call's limits: fewer than 2^32 threads whatever tile is chosen, no more K slices than stages."""
+    lib = _lib()
+    plan, out = lib.mxf_fp4_pair_plan, (ctypes.c_int32 * 3)()
+    plan.argtypes = [ctypes.c_int64] * 3 + [ctypes.c_int, ctypes.c_void_p]
+    good = dict(a=None, sa=A, M=1, b=A, sb=A, N=16, K=128, fmt=1, ga=None, gb=None, c=A, cd=1, ws=A, wb=2 ** 62, stream=None)
+    edge = 2 ** 21 * 128
+    for M, N in [(1, edge), (edge, 16), (edge, 128), (2 ** 17, 2 ** 17 - 16), (128, edge), (4096 * 32, 32), (4096 * 32 + 1, 32),
+                 (1, 2 ** 30), (2 ** 18, 2 ** 15)]:
+        for K in (128, 256, 7168, 2 ** 24 - 128):
+            for fmt in (0, 1):
+                rc = call(lib.fp4_gemm, good, M=M, N=N, K=K, fmt=fmt)
+                tiles = -(-M // 128) * -(-N // 128)
+                assert rc == (UNSUPPORTED if tiles > 2 ** 21 or M * N >= 2 ** 34 else NULL)
+                if rc == UNSUPPORTED:
+                    continue
+                plan(M, N, K, fmt, out)
+                bm, bn, slices = out
+                groups = -(-M // bm) * -(-N // bn)
+                assert 8 * -(-groups // 8) * slices * (512 if bm in (32, 256) else 256) < 2 ** 32
+                assert slices == 1 or (slices <= -(-K // 256) and M * N < 2 ** 30)
+
+
 def test_binding_refuses_host_tensors():
     z = torch.zeros
     f, i = z(4, 64), z(4, 2, dtype=torch.int32)
