@@ -489,10 +489,11 @@ int moe_combine_backward(const void* dout, int dout_dtype, const void* y, int y_
  * 2^-126) with max |x| <= 6 * 448 * g, and 1 for a tensor of zeros. A power of two, so that block scale
  * times g, and with it every quantised value, is exact.
  *   x  n values, fp32 or bf16 (n % 32 == 0);  scale [1] fp32 on the device (4-byte aligned)
- *   workspace    nvfp4_tensor_scale_workspace_bytes() bytes, 16-byte aligned, contents irrelevant
+ *   workspace    nvfp4_tensor_scale_workspace_bytes(n, x_dtype) bytes (0: none needed, may be NULL),
+ *                16-byte aligned, contents irrelevant; calls that may overlap need one each
  * Errors: NULL, SHAPE, ALIGN, FORMAT, WORKSPACE.
  */
-size_t nvfp4_tensor_scale_workspace_bytes(void);
+size_t nvfp4_tensor_scale_workspace_bytes(int64_t n, int x_dtype);
 int nvfp4_tensor_scale(const void* x, int x_dtype, int64_t n, float* scale, void* workspace, size_t workspace_bytes,
                        mxf_stream stream);
 

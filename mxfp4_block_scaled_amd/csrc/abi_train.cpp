@@ -103,7 +103,10 @@ int moe_combine_backward(const void* dout, int dout_dtype, const void* y, int y_
                                                                                                          : MXF_OK;
 }
 
-size_t nvfp4_tensor_scale_workspace_bytes(void) { return mxf::kAmaxBlocks * sizeof(uint32_t); }
+size_t nvfp4_tensor_scale_workspace_bytes(int64_t n, int x_dtype) {
+  if (n <= 0 || !valid_dtype(x_dtype)) return 0;
+  return mxf::amax_blocks(n / (x_dtype == MXF_BF16 ? 8 : 4)) > 1 ? mxf::kAmaxBlocks * sizeof(uint32_t) : 0;
+}
 
 int nvfp4_tensor_scale(const void* x, int x_dtype, int64_t n, float* scale, void* workspace, size_t workspace_bytes,
                        mxf_stream stream) {
@@ -111,7 +114,8 @@ int nvfp4_tensor_scale(const void* x, int x_dtype, int64_t n, float* scale, void
   if (n <= 0 || n % 32 != 0) return MXF_ERR_SHAPE;
   if (!x || !scale) return MXF_ERR_NULL;
   if (!aligned16(x) || !aligned4(scale) || !aligned16(workspace)) return MXF_ERR_ALIGN;
-  if (!workspace || workspace_bytes < nvfp4_tensor_scale_workspace_bytes()) return MXF_ERR_WORKSPACE;
+  const size_t need = nvfp4_tensor_scale_workspace_bytes(n, x_dtype);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return MXF_ERR_WORKSPACE;
   return mxf::launch_nvfp4_tensor_scale(x, x_dtype == MXF_BF16, n / (x_dtype == MXF_BF16 ? 8 : 4), scale,
                                         static_cast<uint32_t*>(workspace), as_stream(stream))
              ? MXF_ERR_LAUNCH

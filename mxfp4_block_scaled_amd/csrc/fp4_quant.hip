@@ -429,8 +429,14 @@ int launch_fp4_dequantize(const uint8_t* q, const uint8_t* q_scale, int64_t bloc
   return hipGetLastError() == hipSuccess ? 0 : -1;
 }
 
+// Workgroups of the maximum of n16 16-byte pieces. One alone up to 256 KB: us a call, one launch | two,
+// 64 KB 6.4 | 10.4, 256 KB 6.3 | 10.4; in a graph 3.0 | 4.3 and 5.5 | 4.3.
+int amax_blocks(int64_t n16) {
+  return n16 <= 16384 ? 1 : (int)min(cdiv(n16, 512 * 4), (int64_t)kAmaxBlocks);
+}
+
 int launch_nvfp4_tensor_scale(const void* x, bool bf16, int64_t n16, float* scale, uint32_t* partial, hipStream_t stream) {
-  const int blocks = (int)min(cdiv(n16, 512 * 4), (int64_t)kAmaxBlocks);
+  const int blocks = amax_blocks(n16);
   const u4v* p = static_cast<const u4v*>(x);
   if (bf16) amax_kernel<true><<<blocks, 512, 0, stream>>>(p, n16, partial, scale);
   else amax_kernel<false><<<blocks, 512, 0, stream>>>(p, n16, partial, scale);

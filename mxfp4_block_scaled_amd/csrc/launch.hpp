@@ -131,6 +131,7 @@ struct Fp4QuantArgs {
   uint8_t *q, *q_scale, *qt, *qt_scale;
 };
 constexpr int kAmaxBlocks = 512;
+int amax_blocks(int64_t n16);
 int launch_fp4_quantize(const Fp4QuantArgs& a, bool x_bf16, bool nvfp4, hipStream_t stream);
 int launch_fp4_dequantize(const uint8_t* q, const uint8_t* q_scale, int64_t blocks32, bool nvfp4,
                           const float* tensor_scale, void* out, bool out_bf16, hipStream_t stream);

@@ -62,7 +62,7 @@ SIGNATURES = {
                                   _p]),
     "moe_route_backward": (_c_int, [_p, _c_int, _p, _p, _p, _p, _p, _p, _p, _p, _c_i32, _c_i64, _c_i32, _c_i32, _p, _p]),
     "moe_combine_backward": (_c_int, [_p, _c_int, _p, _c_int, _c_i64, _p, _p, _c_i64, _c_i32, _c_i64, _p, _p, _p]),
-    "nvfp4_tensor_scale_workspace_bytes": (_sz, []),
+    "nvfp4_tensor_scale_workspace_bytes": (_sz, [_c_i64, _c_int]),
     "nvfp4_tensor_scale": (_c_int, [_p, _c_int, _c_i64, _p, _p, _sz, _p]),
     "fp4_quantize": (_c_int, [_p, _c_int, _c_i64, _c_i64, _c_int, _p, _p, _p, _p, _p, _p, _p]),
     "fp4_dequantize": (_c_int, [_p, _p, _c_i64, _c_i64, _c_int, _p, _p, _c_int, _p]),
@@ -716,8 +716,11 @@ def nvfp4_tensor_scale(x, workspace=None):
     i = _gpu(x)
     dt = _one_of(x.dtype, DTYPES, "x")
     out = x.new_empty((1,), dtype=torch.float32)
-    workspace = _workspace(workspace, (_lib or load()).nvfp4_tensor_scale_workspace_bytes(), x)
-    _call("nvfp4_tensor_scale", i, x.data_ptr(), dt, x.numel(), out.data_ptr(), workspace.data_ptr(), workspace.numel())
+    n = x.numel()
+    need = (_lib or load()).nvfp4_tensor_scale_workspace_bytes(n, dt)
+    if need or workspace is not None:
+        workspace = _workspace(workspace, need, x)
+    _call("nvfp4_tensor_scale", i, x.data_ptr(), dt, n, out.data_ptr(), _at(workspace), need)
     return out
 
 

@@ -118,7 +118,7 @@ def test_ties_of_codes_and_scales():
     _compare(d["q"], d["q_scale"], t.double().numpy(), "nvfp4", 1.0, None, False)
 
 
-@pytest.mark.parametrize("n", [32, 2048 * 16, 4_000_000 // 32 * 32])
+@pytest.mark.parametrize("n", [32, 2048 * 16, 65_536, 65_568, 131_072, 131_104, 4_000_000])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 def test_tensor_scale(n, dtype):
     for amax in (0.0, 1e-44, 2.0 ** -126, 2688.0, 2688.0 * 2 ** 7, 2704.0, 5e-7, 3e38):

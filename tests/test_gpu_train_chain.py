@@ -51,7 +51,7 @@ def test_router_and_combine_of_an_expert_layer(T):
             parts.append(E / (k * len(use)) * (c * p[use].mean(0)).sum())
     if parts:
         loss = loss + 0.02 * sum(parts) / len(parts) + 0.003 * (lse[mask.bool()] ** 2).mean()
-        assert abs(float(bal["losses"][0]) - float(sum(parts) / len(parts))) < 1e-5 * E
+        assert abs(float(bal["losses"][0]) - float(sum(parts).detach() / len(parts))) < 1e-5 * E
     loss.backward()
     # dgates: 512 products added in fp32, |terms| in all at most `size`; dlogits adds k of them weighted by gates
     size = (dout.double()[:, None] * y).abs().sum(2).max(1, keepdim=True).values

@@ -75,8 +75,10 @@ def test_combine_backward_errors():
 def test_quantise_errors():
     lib = _lib()
     fn = lib.nvfp4_tensor_scale
-    need = lib.nvfp4_tensor_scale_workspace_bytes()
-    good = dict(x=A, xd=1, n=64, out=A, ws=A, wb=need, stream=None)
+    n = 2 ** 20
+    need = lib.nvfp4_tensor_scale_workspace_bytes(n, 1)
+    assert need > 0 and lib.nvfp4_tensor_scale_workspace_bytes(64, 1) == 0  # small: one workgroup
+    good = dict(x=A, xd=1, n=n, out=A, ws=A, wb=need, stream=None)
     for change, want in [
         (dict(xd=2), FORMAT), (dict(n=0), SHAPE), (dict(n=48), SHAPE), (dict(x=None), NULL), (dict(out=None), NULL),
         (dict(x=U), ALIGN), (dict(out=U2), ALIGN), (dict(ws=U), ALIGN), (dict(ws=None), WORKSPACE), (dict(wb=need - 1), WORKSPACE),
