@@ -116,8 +116,8 @@ __global__ void __launch_bounds__(64 * WM * WN) fp4_pair_kernel(Fp4PairArgs a) {
   }
 #pragma unroll
   for (int q = 0; q < IS; ++q) {
-    const int p = wave + NW * q, piece = (p < ISA ? p : p - ISA) * 64 + lane;
-    vs[q] = (uint32_t)((piece >> 1) * srow + 16 * (piece & 1));
+    const int p = wave + NW * q;
+    vs[q] = (uint32_t)((32 * (p < ISA ? p : p - ISA) + r32) * srow + 16 * g);
   }
   auto issue = [&](int slot, int st) {
 #pragma unroll
@@ -164,20 +164,22 @@ __global__ void __launch_bounds__(64 * WM * WN) fp4_pair_kernel(Fp4PairArgs a) {
   auto compute = [&](const uint8_t* As, const uint8_t* Bs, int st) __attribute__((always_inline)) {
     constexpr int W = kNV ? 2 : 1;  // dwords of scales a lane and row
     uint32_t sa[FM][W], sb[FN][W];
-    const uint8_t* const SAs = &ring.SA[(st / G) & 1][SB * (st % G) + 4 * W * g];
-    const uint8_t* const SBs = &ring.SB[(st / G) & 1][SB * (st % G) + 4 * W * g];
+    // 32 rows' first 16 bytes, then their second: neighbouring rows on other banks
+    const int off = SB * (st % G) + 4 * W * g, part = 512 * (off >> 4) + (off & 15);
+    const uint8_t* const SAs = &ring.SA[(st / G) & 1][part];
+    const uint8_t* const SBs = &ring.SB[(st / G) & 1][part];
     // the half of the last stage past K: lane group 1's blocks count for nothing
     const bool past = g == 1 && ((int64_t)st * 256 + 128 >= K);
 #pragma unroll
     for (int i = 0; i < W; ++i) {
 #pragma unroll
       for (int f = 0; f < FM; ++f) {
-        sa[f][i] = *reinterpret_cast<const uint32_t*>(SAs + 32 * arow[f] + 4 * i);
+        sa[f][i] = *reinterpret_cast<const uint32_t*>(SAs + 1024 * (FM * wm + f) + 16 * r32 + 4 * i);
         if (past) sa[f][i] = 0;
       }
 #pragma unroll
       for (int f = 0; f < FN; ++f) {
-        sb[f][i] = *reinterpret_cast<const uint32_t*>(SBs + 32 * brow[f] + 4 * i);
+        sb[f][i] = *reinterpret_cast<const uint32_t*>(SBs + 1024 * (FN * wn + f) + 16 * r32 + 4 * i);
         if (past) sb[f][i] = 0;
       }
     }

@@ -66,7 +66,7 @@ def test_each_lane_reads_its_rows_blocks(rows, waves):
 @pytest.mark.parametrize("nv", [False, True])
 @pytest.mark.parametrize("bm,bn,wm,wn", SHAPES)
 def test_scales_of_a_group(bm, bn, wm, wn, nv):
-    """A group is 32 scale bytes a row; the lane of row r and group g finds those of its blocks 4 g .. 4 g + 3."""
+    """A group is 32 scale bytes a row, the first 16 of 32 rows, then their second; the lane of row r and group g finds those of its blocks 4 g .. 4 g + 3."""
     NW, G, W = wm * wn, 2 if nv else 4, 2 if nv else 1
     SB = 32 // G
     ISA, ISB = bm * 2 // 64, bn * 2 // 64
@@ -81,15 +81,15 @@ def test_scales_of_a_group(bm, bn, wm, wn, nv):
                     continue
                 into, part = (sa, p) if p < ISA else (sb, p - ISA)
                 for lane in range(64):
-                    piece = part * 64 + lane
                     lds = part * 1024 + 16 * lane
                     assert (into[lds:lds + 16] == -1).all() and lds + 16 <= into.size
-                    into[lds:lds + 16] = (piece >> 1) * srow + 16 * (piece & 1) + grp * 32 + np.arange(16)
+                    into[lds:lds + 16] = (32 * part + lane % 32) * srow + 16 * (lane // 32) + grp * 32 + np.arange(16)
         for rows, held in ((bm, sa), (bn, sb)):
             for r in range(rows):
                 for st in range(grp * G, grp * G + G):
                     for g in range(2):
-                        at = SB * (st % G) + 4 * W * g + 32 * r
+                        off = SB * (st % G) + 4 * W * g
+                        at = 1024 * (r // 32) + 512 * (off >> 4) + 16 * (r % 32) + (off & 15)
                         for s in range(4):  # block 4 g + s of the stage: one byte, or two of 16 elements each
                             block = (st * 8 + 4 * g + s) * W
                             got = held[at + s * W:at + s * W + W]
