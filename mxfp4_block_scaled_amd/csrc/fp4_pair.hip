@@ -27,7 +27,10 @@ __global__ void __launch_bounds__(256) fp4_pair_sum_kernel(const float4* part, i
 
 // Few tiles: 32 rows x 32 columns a workgroup, whose 8 waves share K. A wave copies its stages into two LDS
 // slots of its own (whole lines, no barrier among waves) and the waves' sums meet in LDS: one launch, no
-// workspace. The fixed order of the waves keeps results the same from run to run.
+// workspace. The fixed order of the waves keeps results the same from run to run. 64 x 4096 x 7168: MXFP4
+// 7.4 us, NVFP4 11 (its decoding takes the vector unit 3 us: 32 rows of A beside 32 of B). Loads straight
+// into registers, a lane a row, cost the address unit 32 lines an instruction: 11 and 13 us, and the tiled
+// kernel with K slices 19 and 22.
 constexpr int kFewWaves = 8;
 struct alignas(16) FewSlot {
   uint8_t A[32 * 128], B[32 * 128];

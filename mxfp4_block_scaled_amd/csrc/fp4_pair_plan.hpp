@@ -20,16 +20,16 @@ constexpr int64_t kMostTiles = int64_t(1) << 21, kMostFewTiles = 4096;
 // traffic. Below the constants (us), fitted to these times (us: 32 x 32 | 64 x 64 | 64 x 128 | 128 x 128 |
 // 256 x 256; 4s: 64 x 128 in 4 slices):
 //                      NVFP4                               MXFP4
-//   128 x 7168 x 4096    24 | 20 | 25 | 34 | 54              16 | 11 | 12 | 16 | 21
-//   256 x 2048 x 2048    7.9 | 11 | 14 | 19 | 46             6.1 | 6.1 | 7.0 | 9.5 | 18
-//   256 x 4096 x 7168    37 | 31 | 40 | 57 | 149  4s 28      23 | 17 | 20 | 25 | 49  4s 18
-//   512 x 1024 x 16384   38 | 67 | 88 | 126 | 333  4s 30     23 | 34 | 39 | 51 | 103  4s 18
-//   512 x 4096 x 7168    73 | 51 | 43 | 57 | 149             42 | 18 | 21 | 25 | 49
-//   1024 x 2048 x 2048   28 | 16 | 15 | 20 | 46              21 | 7.4 | 7.6 | 10 | 18
-//   1024 x 4096 x 7168   136 | 84 | 71 | 62 | 149            80 | 31 | 24 | 26 | 48
-//   2000 x 4096 x 2048   98 | 53 | 42 | 34 | 48              73 | 20 | 17 | 14 | 19
-//   3000 x 3008 x 4096   182 | 103 | 92 | 86 | 89            119 | 40 | 38 | 35 | 31
-//   4096 x 4096 x 7168   513 | 316 | 268 | 215 | 187         311 | 116 | 99 | 77 | 64
+//   128 x 7168 x 4096    24 | 20 | 25 | 35 | 54              16 | 11 | 13 | 15 | 20
+//   256 x 2048 x 2048    7.8 | 11 | 13 | 19 | 46             6.2 | 5.9 | 6.8 | 9.0 | 17
+//   256 x 4096 x 7168    38 | 34 | 41 | 57 | 149  4s 31      23 | 17 | 20 | 23 | 45  4s 18
+//   512 x 1024 x 16384   36 | 66 | 85 | 126 | 333  4s 33     24 | 34 | 40 | 49 | 95  4s 18
+//   512 x 4096 x 7168    72 | 50 | 43 | 58 | 149             44 | 18 | 21 | 24 | 45
+//   1024 x 2048 x 2048   28 | 16 | 15 | 20 | 46              21 | 7.4 | 7.4 | 9.7 | 17
+//   1024 x 4096 x 7168   129 | 87 | 72 | 64 | 150            81 | 31 | 25 | 27 | 45
+//   2000 x 4096 x 2048   98 | 53 | 45 | 36 | 50              75 | 20 | 17 | 14 | 18
+//   3000 x 3008 x 4096   175 | 107 | 97 | 90 | 90            122 | 39 | 38 | 35 | 30
+//   4096 x 4096 x 7168   489 | 329 | 280 | 225 | 199         312 | 116 | 94 | 78 | 65
 inline Fp4PairPlan fp4_pair_plan(int64_t M, int64_t N, int64_t K, bool nv) {
   struct Shape {
     int bm, bn;

@@ -10,7 +10,9 @@
 // q + (x - q d) (1/d). With the reciprocal alone a value halfway between two codes (often: x has 8
 // bits and s 4) could land on either side of the tie.
 //
-// HBM-bound: x once, the codes and scales once. Where columns are wanted a workgroup holds a
+// x once, the codes and scales once. To nearest and along rows HBM bounds it; the stochastic choice in both
+// directions the vector unit (4096 x 7168 bf16: 41 us, 1339 instructions for a lane's 32 values both ways are 31 of
+// them; 53 with the choice by comparisons and the compiler's division). Where columns are wanted a workgroup holds a
 // 128 x 128 tile of x in LDS; the codes along columns go back through LDS so that they leave as whole
 // 64-byte pieces of a row of x^T.
 #include "mx_codec.hpp"
