@@ -11,7 +11,7 @@
 // bits and s 4) could land on either side of the tie.
 //
 // x once, the codes and scales once. To nearest and along rows HBM bounds it; the stochastic choice in both
-// directions the vector unit (4096 x 7168 bf16: 41 us, 1339 instructions for a lane's 32 values both ways are 31 of
+// directions the vector unit (4096 x 7168 bf16: 40 us, 1275 instructions for a lane's 32 values both ways are 30 of
 // them; 53 with the choice by comparisons and the compiler's division). Where columns are wanted a workgroup holds a
 // 128 x 128 tile of x in LDS; the codes along columns go back through LDS so that they leave as whole
 // 64-byte pieces of a row of x^T.
@@ -132,10 +132,10 @@ __device__ __forceinline__ uint32_t codes_of(const float (&x)[P], const uint32_t
 
 template <int P>
 __device__ __forceinline__ uint32_t amax_of(const float (&x)[P]) {
-  uint32_t m = 0;
+  float m = 0.0f;  // as floats: the magnitude is an operand's modifier, as integers an instruction
 #pragma unroll
-  for (int i = 0; i < P; ++i) m = max(m, __float_as_uint(x[i]) & 0x7FFFFFFFu);
-  return m;
+  for (int i = 0; i < P; ++i) m = fmaxf(m, fabsf(x[i]));
+  return __float_as_uint(m);
 }
 
 template <int kCtrl>
