@@ -12,7 +12,7 @@ inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3
 
 int route_sizes(int64_t T, int32_t E, int32_t topk, int32_t S) {
   if (T < 0 || E < 1 || topk < 1 || topk > 8 || topk > E || S < 1) return MXF_ERR_SHAPE;
-  if (E > 1024 || T * (int64_t)topk > kMaxRows) return MXF_ERR_UNSUPPORTED;
+  if (E > 1024 || T > kMaxRows || T * (int64_t)topk > kMaxRows) return MXF_ERR_UNSUPPORTED;
   // one wave per token; one workgroup of 512 threads per sequence and 64 experts
   if (mxf::cdiv(T, 4) * 256 > mxf::kMaxThreads || S * mxf::cdiv(E, 64) * 512 > mxf::kMaxThreads) return MXF_ERR_UNSUPPORTED;
   return MXF_OK;
@@ -91,7 +91,7 @@ int moe_combine_backward(const void* dout, int dout_dtype, const void* y, int y_
                          float* dgates, mxf_stream stream) {
   if (!valid_dtype(dout_dtype) || !valid_dtype(y_dtype)) return MXF_ERR_FORMAT;
   if (T < 0 || y_rows < 0 || topk < 1 || topk > 8 || H <= 0 || H % 8 != 0) return MXF_ERR_SHAPE;
-  if (T * (int64_t)topk > kMaxRows || y_rows > kMaxRows || H > kMaxRows) return MXF_ERR_UNSUPPORTED;
+  if (T > kMaxRows || T * (int64_t)topk > kMaxRows || y_rows > kMaxRows || H > kMaxRows) return MXF_ERR_UNSUPPORTED;
   const int64_t groups = T * mxf::cdiv(topk, mxf::combine_backward_pairs(T, topk));
   if (groups * mxf::combine_backward_threads(H, dout_dtype == MXF_BF16 && y_dtype == MXF_BF16) > mxf::kMaxThreads) return MXF_ERR_UNSUPPORTED;
   if (T == 0 || (y_rows == 0 && !dgates)) return MXF_OK;  // (a dy of no rows has no address)

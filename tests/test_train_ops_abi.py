@@ -72,6 +72,15 @@ def test_combine_backward_errors():
         assert call(fn, good, **change) == want, change
 
 
+def test_token_counts_whose_products_pass_64_bits():
+    """T * topk of 2^64 is 0 in 64 bits; so are the threads of such a call."""
+    lib = _lib()
+    for T in (2 ** 61, 2 ** 62, 2 ** 63 - 1):
+        assert lib.moe_balance_loss(A, 0, A, None, None, 1, T, 60, 8, A, A, A, A, A, A, 2 ** 62, None) == UNSUPPORTED
+        assert lib.moe_route_backward(A, 0, A, A, A, A, A, A, A, None, 1, T, 60, 8, A, None) == UNSUPPORTED
+        assert lib.moe_combine_backward(A, 0, A, 0, 64, A, A, T, 8, 64, A, A, None) == UNSUPPORTED
+
+
 def test_quantise_errors():
     lib = _lib()
     fn = lib.nvfp4_tensor_scale
