@@ -22,9 +22,9 @@ namespace mxf {
 
 namespace {
 
-constexpr int kWaves = 8;        // of a forward workgroup
-constexpr int kFinishGroups = 8;   // groups of 64 threads that share a sequence's slots
-constexpr int kFinishLoads = 8;    // slots of a group in flight
+constexpr int kWaves = 8;         // of a forward workgroup
+constexpr int kFinishGroups = 8;  // groups of 64 threads that share a sequence's slots
+constexpr int kFinishLoads = 8;   // slots of a group in flight
 
 // Rows [row, row + U) of an [T][E] matrix as a range-checked resource: rows past T read as zeros, and the
 // row's place is a scalar, so that a load costs no address arithmetic.
@@ -212,7 +212,7 @@ __global__ void __launch_bounds__(64 * kWaves) balance_kernel(RouteLossArgs a, i
         if (lane + 64 * v >= E) x[u][v] = -INFINITY;
         m = fmaxf(m, x[u][v]);
       }
-      m = wave_max(m);
+      m = fmaxf(wave_max(m), -3.402823466e38f);  // so that a row of -inf alone has the sum 0, one with NaN the sum NaN
       float sum = 0.0f;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
@@ -224,7 +224,7 @@ __global__ void __launch_bounds__(64 * kWaves) balance_kernel(RouteLossArgs a, i
       const float inv = 1.0f / sum;
 #pragma unroll
       for (int v = 0; v < V; ++v) x[u][v] *= inv;
-      if (tw + u < hi && m != -INFINITY && !(out >> u & 1)) use |= 1u << u;
+      if (tw + u < hi && sum != 0.0f && !(out >> u & 1)) use |= 1u << u;
     }
 
     uint32_t counted = 0;

@@ -139,6 +139,21 @@ def test_a_nan_row_spoils_the_losses_and_its_own_gradient_only():
     assert bad == [17, 18]
 
 
+@pytest.mark.parametrize("T", [60, 200])
+def test_a_row_of_nothing_but_nan_counts(T):
+    """NaN is not -inf: such a row, alone or beside -inf, is no row ruled out; it spoils the losses."""
+    logits, ids, gates, dgates = _case(T, 40, 2, 4)
+    logits[17] = torch.nan
+    logits[18] = -torch.inf
+    logits[19, 1:], logits[19, 0] = -torch.inf, torch.nan
+    d = ops.moe_balance_loss(logits.cuda(), ids.cuda())
+    assert d["losses"].isnan().all()
+    assert d["tokens"].tolist() == [T - 1, T - 1, 1] and int(d["counts"].sum()) == 2 * (T - 1)
+    assert d["lse"].isnan().nonzero().flatten().tolist() == [17, 19]
+    got = ops.moe_route_backward(logits.cuda(), ids.cuda(), gates.cuda(), dgates.cuda(), d, torch.ones(2).cuda())
+    assert got.isnan().any(1).nonzero().flatten().tolist() == [17, 19]
+
+
 def test_no_tokens():
     d = ops.moe_balance_loss(torch.empty((0, 32)).cuda(), torch.empty((0, 2), dtype=torch.int32).cuda(),
                              seg_offsets=torch.zeros(4, dtype=torch.int32).cuda())
