@@ -61,7 +61,7 @@ template <bool kNV>
 __device__ __forceinline__ Divisor divisor_of(uint32_t amax_bits, const Top& top) {
   Divisor v;
   if (kNV) {
-    v.byte = e4m3_mag_code(divide(__uint_as_float(amax_bits), top.six, top.inv));
+    v.byte = e4m3_mag_code(fminf(divide(__uint_as_float(amax_bits), top.six, top.inv), 448.0f));  // infinity gives NaN
     v.d = ue4m3_to_f32(v.byte) * top.g;
     const bool ok = v.d >= kTiny && v.d <= 3.0e38f;  // else the block is stored as zeros (g of no use, too)
     v.byte = ok ? v.byte : 0;
@@ -75,8 +75,8 @@ __device__ __forceinline__ Divisor divisor_of(uint32_t amax_bits, const Top& top
   return v;
 }
 
-// x / d, for the code nearest to it or, with a random byte r, the one of its two neighbours that r
-// picks, as twice its value. With step the distance of the neighbours, u = |x / d| / step and t = (r + 1/2) / 256 the code is
+// x / d, for the code nearest to it; or with a random byte r twice the value of the one of its two neighbours
+// that r picks. With step the distance of the neighbours, u = |x / d| / step and t = (r + 1/2) / 256 that is
 // ceil(u - t) steps: above floor(u) exactly if the part of u above it exceeds t. u - t is exact (t and u are
 // multiples of u's last bit, or u < 1 and they are near each other or far from 0). Past 6 the conversion saturates.
 template <bool kNV, bool kSR>

@@ -144,6 +144,7 @@ def test_extremes():
     clean = ops.fp4_quantize(y.cuda(), "nvfp4", transposed=True)
     y[1, 2], y[2, 40] = torch.nan, torch.inf
     d = ops.fp4_quantize(y.cuda(), "nvfp4", transposed=True)
+    assert int(d["q_scale"][2, 2]) == 0x7E and (d["q_scale"] < 0x7F).all()
     keep = torch.ones(3, 32, dtype=torch.bool)
     keep[1, :8] = keep[2, 16:24] = False
     assert torch.equal(d["q"].cpu()[keep], clean["q"].cpu()[keep])
