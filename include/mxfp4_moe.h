@@ -456,8 +456,9 @@ int moe_balance_loss(const void* logits, int logits_dtype, const int32_t* topk_i
  *   gates, dgates [T][topk] fp32; dgates NULL: no such term (gates and topk_ids are ignored)
  *   dlosses      [2] fp32 on the device (4-byte aligned); NULL: no such terms (logits, lse, counts,
  *                tokens and seg_offsets are ignored)
- *   lse, counts, tokens  as moe_balance_loss wrote them for these sequences (counts and tokens may be
- *                those of several GPUs added up)
+ *   lse, counts, tokens  as moe_balance_loss wrote them for these sequences. Where each sequence's tokens lie
+ *                on several GPUs, the losses of them all take counts, n_s and n added up over the GPUs;
+ *                S' (the last of tokens) is then the number of n_s > 0 after that, not a sum
  *   dlogits      [T][E], of logits_dtype; every value is written
  * Sizes as for moe_balance_loss. T == 0 is a no-op. Errors: NULL (neither term wanted, too), SHAPE,
  * ALIGN, FORMAT, UNSUPPORTED.

@@ -654,7 +654,9 @@ def _workspace(workspace, need, like):
 def moe_route_backward(logits, topk_ids, gates=None, dgates=None, balance=None, dlosses=None, seg_offsets=None):
     """The gradient of the router's logits [T][E]: of the gates (the softmax over the selected logits) with gates and
     dgates [T][topk] fp32, and of the losses with `balance`, moe_balance_loss's dict for these seg_offsets, and dlosses
-    [2] fp32 (the losses' own gradients, on the GPU). Either part may be left out. Returns dlogits, of logits' dtype."""
+    [2] fp32 (the losses' own gradients, on the GPU). Either part may be left out. Returns dlogits, of logits' dtype.
+    Where each sequence's tokens lie on several GPUs, `balance` holds counts and tokens added up over them, except its
+    last, the number of sequences that then hold a token."""
     i = _gpu(logits)
     if logits.dim() != 2 or topk_ids.dim() != 2:
         raise RuntimeError("logits must be [T][E] and topk_ids [T][topk]")

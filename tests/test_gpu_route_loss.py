@@ -177,6 +177,27 @@ def test_each_part_alone():
             ops.moe_route_backward(logits.cuda(), ids.cuda(), **bad)
 
 
+def test_sequences_spread_over_several_devices():
+    """Counts and tokens of the parts added up (the sequences that hold any counted again): each part's gradient is its
+    piece of the whole's. Every term of a token is formed from the same values in the same order, so bit for bit."""
+    logits, ids, gates, dgates = (t.cuda() for t in _case(400, 96, 4, 9))
+    dl = torch.tensor([0.6, 0.2]).cuda()
+    offs = [torch.tensor(o, dtype=torch.int32).cuda() for o in ([0, 150, 150, 400], [0, 100, 100, 220], [0, 50, 50, 180])]
+    # the first part: tokens 0..99 of sequence 0 and 150..269 of sequence 2
+    own = [torch.cat((torch.arange(0, 100), torch.arange(150, 270))), torch.cat((torch.arange(100, 150), torch.arange(270, 400)))]
+    whole = ops.moe_balance_loss(logits, ids, seg_offsets=offs[0])
+    want = ops.moe_route_backward(logits, ids, gates, dgates, whole, dl, offs[0])
+    part = [ops.moe_balance_loss(logits[o], ids[o], seg_offsets=f) for o, f in zip(own, offs[1:])]
+    counts = part[0]["counts"] + part[1]["counts"]
+    tokens = part[0]["tokens"] + part[1]["tokens"]
+    tokens[-1] = (tokens[:-2] > 0).sum()
+    assert torch.equal(counts, whole["counts"]) and torch.equal(tokens, whole["tokens"])
+    for o, f, d in zip(own, offs[1:], part):
+        d = dict(d, counts=counts, tokens=tokens)
+        got = ops.moe_route_backward(logits[o], ids[o], gates[o], dgates[o], d, dl, f)
+        assert torch.equal(got, want[o.cuda()])
+
+
 def test_against_differences():
     """dlogits is the derivative of dlosses . losses + dgates . gates (counts held): differences of the 64-bit forms."""
     T, E, k = 9, 12, 3
