@@ -105,10 +105,10 @@ __device__ __forceinline__ double wave_sum_f64(double v) {
 
 // One workgroup: tokens [tb blockIdx, tb (blockIdx + 1)), 8 TW at a time, TW a wave. All loads go out
 // first and the tokens' probabilities are formed without regard to sequences; then the workgroup walks the
-// sequences that meet its tokens and keeps each one's sums in registers until it ends. With one
-// workgroup in the launch it writes the results itself.
+// sequences that meet its tokens and keeps each one's sums in registers until it ends. Alone
+// it writes the results itself.
 template <bool kBF16, int V, int TW>
-__global__ void __launch_bounds__(64 * kWaves) balance_kernel(RouteLossArgs a, int64_t tb) {
+__global__ void __launch_bounds__(64 * kWaves) balance_kernel(RouteLossArgs a, int64_t tb, bool alone) {
   static_assert(TW <= 8, "8 lanes a token for its picks");
   __shared__ float red[kWaves][64 * V];
   __shared__ int32_t cnt[64 * V];
@@ -118,7 +118,6 @@ __global__ void __launch_bounds__(64 * kWaves) balance_kernel(RouteLossArgs a, i
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   const int64_t t0 = (int64_t)blockIdx.x * tb, t1 = min(t0 + tb, a.T);
   const int E = a.E, topk = a.topk;
-  const bool alone = gridDim.x == 1;
   const Slots slots = slots_at(a.workspace, gridDim.x, a.S, E);
   if (!alone && blockIdx.x == 0 && tid == 0) *slots.done = 0;
 
@@ -252,7 +251,7 @@ __global__ void __launch_bounds__(64 * kWaves) balance_kernel(RouteLossArgs a, i
         flush();
       }
       if (more) break;
-      ++s;
+      s = from < to || alone || a.S <= 64 ? s + 1 : max(s + 1, seg.of(to));  // over a run of empty ones at once
     }
     float mine = -INFINITY;
 #pragma unroll
@@ -471,25 +470,29 @@ __global__ void __launch_bounds__(256) route_backward_kernel(RouteLossArgs a) {
   }
 }
 
-// How the forward pass deals out T tokens: at most 64 are one workgroup that writes the results itself;
-// else 2, 4 or 8 a wave, so that few tokens are many workgroups but a sequence has few slots to add
-// (one sequence of 16384 tokens of 256 experts: 19 us in 256 workgroups, 26 in 512, 40 in 1024), and at most 512 workgroups.
+// How the forward pass deals out T tokens: at most 64 in one or two sequences are one workgroup that writes the
+// results itself, one sequence after the other (64 x 256 in 1, 2, 4 and 64 sequences: 8.0, 9.3, 11.8 and 85 us,
+// with the second launch 10.0, 10.1, 10.5 and 29); else 2, 4 or 8 a wave, so that few tokens are many workgroups but a
+// sequence has few slots to add (one sequence of 16384 tokens of 256 experts: 19 us in 256 workgroups, 26 in 512, 40 in
+// 1024), and at most 512 workgroups.
+constexpr int64_t kMostAlone = 2;
 struct Deal {
   int tw;
   int64_t tb, blocks;
+  bool alone;
 };
-Deal deal_of(int64_t T) {
-  if (T <= 64) return {8, 64, 1};
+Deal deal_of(int64_t T, int64_t S) {
+  if (T <= 64 && S <= kMostAlone) return {8, 64, 1, true};
   const int tw = T <= 4096 ? 2 : T <= 8192 ? 4 : 8;
-  const int64_t one = kWaves * tw, tb = one * cdiv(cdiv(T, one), 512);
-  return {tw, tb, cdiv(T, tb)};
+  const int64_t one = kWaves * tw, tb = one * max(cdiv(cdiv(T, one), 512), (int64_t)1);
+  return {tw, tb, max(cdiv(T, tb), (int64_t)1), false};
 }
 
 template <bool kBF16, int V>
 void launch_forward(const RouteLossArgs& a, const Deal& d, hipStream_t stream) {
-  if (d.tw == 2) balance_kernel<kBF16, V, 2><<<(unsigned)d.blocks, 64 * kWaves, 0, stream>>>(a, d.tb);
-  else if (d.tw == 4) balance_kernel<kBF16, V, 4><<<(unsigned)d.blocks, 64 * kWaves, 0, stream>>>(a, d.tb);
-  else balance_kernel<kBF16, V, 8><<<(unsigned)d.blocks, 64 * kWaves, 0, stream>>>(a, d.tb);
+  if (d.tw == 2) balance_kernel<kBF16, V, 2><<<(unsigned)d.blocks, 64 * kWaves, 0, stream>>>(a, d.tb, d.alone);
+  else if (d.tw == 4) balance_kernel<kBF16, V, 4><<<(unsigned)d.blocks, 64 * kWaves, 0, stream>>>(a, d.tb, d.alone);
+  else balance_kernel<kBF16, V, 8><<<(unsigned)d.blocks, 64 * kWaves, 0, stream>>>(a, d.tb, d.alone);
 }
 
 template <bool kBF16, int V>
@@ -499,7 +502,7 @@ void launch_backward(const RouteLossArgs& a, hipStream_t stream) {
 
 template <bool kBF16>
 void launch_both(const RouteLossArgs& a, bool backward, hipStream_t stream) {
-  const Deal d = deal_of(a.T);
+  const Deal d = deal_of(a.T, a.S);
   if (a.E <= 64) backward ? launch_backward<kBF16, 1>(a, stream) : launch_forward<kBF16, 1>(a, d, stream);
   else if (a.E <= 128) backward ? launch_backward<kBF16, 2>(a, stream) : launch_forward<kBF16, 2>(a, d, stream);
   else if (a.E <= 256) backward ? launch_backward<kBF16, 4>(a, stream) : launch_forward<kBF16, 4>(a, d, stream);
@@ -510,15 +513,15 @@ void launch_both(const RouteLossArgs& a, bool backward, hipStream_t stream) {
 }  // namespace
 
 size_t route_loss_workspace(int64_t T, int64_t E, int64_t S) {
-  const Deal d = deal_of(T);
-  if (d.blocks == 1) return 0;
+  const Deal d = deal_of(T, S);
+  if (d.alone) return 0;
   return reinterpret_cast<size_t>(slots_at(nullptr, d.blocks, S, E).done) + sizeof(uint32_t);
 }
 
 int launch_route_loss(const RouteLossArgs& a, bool bf16, hipStream_t stream) {
   bf16 ? launch_both<true>(a, false, stream) : launch_both<false>(a, false, stream);
-  const Deal d = deal_of(a.T);
-  if (d.blocks > 1)
+  const Deal d = deal_of(a.T, a.S);
+  if (!d.alone)
     balance_finish_kernel<<<(unsigned)(a.S * cdiv(a.E, 64)), 64 * kFinishGroups, 0, stream>>>(a, d.tb, d.blocks);
   return hipGetLastError() == hipSuccess ? 0 : -1;
 }

@@ -76,6 +76,26 @@ def test_many_tokens_and_more_sequences_than_lanes(T, offsets):
     _check(*_case(T, 24, 2, T), None, offsets)
 
 
+@pytest.mark.parametrize("T,S", [(1, 65), (16, 100), (50, 3000), (700, 65), (700, 5000)])
+def test_runs_of_empty_sequences(T, S):
+    """Many sequences, nearly all of them empty: before the tokens, between them (inside a workgroup's tokens and at
+    their ends) and behind them; tokens of no sequence at both ends."""
+    g = torch.Generator().manual_seed(T + S)
+    cuts = sorted(torch.randint(0, T + 1, (6,), generator=g).tolist()) + [T]
+    runs = torch.multinomial(torch.ones(7), S + 1, replacement=True, generator=g).tolist()
+    offsets = sorted(cuts[k] for k in runs)
+    _check(*_case(T, 40, 3, S), None, offsets)
+    _check(*_case(T, 70, 2, S, True), None, [0] * (S // 2) + [min(3, T)] * (S + 1 - S // 2))
+
+
+@pytest.mark.parametrize("S", [1, 64, 65, 4000])
+def test_no_tokens_in_many_sequences(S):
+    d = ops.moe_balance_loss(torch.empty((0, 96)).cuda(), torch.empty((0, 2), dtype=torch.int32).cuda(),
+                             seg_offsets=torch.zeros(S + 1, dtype=torch.int32).cuda())
+    assert d["losses"].tolist() == [0.0, 0.0] and d["counts"].shape == (S, 96)
+    assert not d["counts"].any() and not d["prob_mean"].any() and not d["tokens"].any()
+
+
 def test_views_of_larger_tensors():
     logits, ids, gates, dgates = (t.cuda() for t in _case(130, 64, 4, 8))
     mask = torch.ones(200, dtype=torch.uint8).cuda()

@@ -72,6 +72,13 @@ def test_combine_backward_errors():
         assert call(fn, good, **change) == want, change
 
 
+def test_workspace_without_tokens():
+    """No tokens in many sequences: one workgroup's slots beside the sequences', as for any few tokens."""
+    fn = _lib().moe_balance_loss_workspace_bytes
+    assert fn(0, 60, 1) == fn(64, 60, 1) == 0
+    assert fn(0, 60, 5000) == fn(1, 60, 5000) >= 5000 * 60 * 8
+
+
 def test_token_counts_whose_products_pass_64_bits():
     """T * topk of 2^64 is 0 in 64 bits; so are the threads of such a call."""
     lib = _lib()
