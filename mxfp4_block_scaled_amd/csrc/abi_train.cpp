@@ -13,8 +13,8 @@ inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3
 int route_sizes(int64_t T, int32_t E, int32_t topk, int32_t S) {
   if (T < 0 || E < 1 || topk < 1 || topk > 8 || topk > E || S < 1) return MXF_ERR_SHAPE;
   if (E > 1024 || T > kMaxRows || T * (int64_t)topk > kMaxRows) return MXF_ERR_UNSUPPORTED;
-  // one wave per token; one workgroup of 512 threads per sequence and 64 experts
-  if (mxf::cdiv(T, 4) * 256 > mxf::kMaxThreads || S * mxf::cdiv(E, 64) * 512 > mxf::kMaxThreads) return MXF_ERR_UNSUPPORTED;
+  // one wave per token; pairs of a sequence and 64 experts counted in 32 bits
+  if (mxf::cdiv(T, 4) * 256 > mxf::kMaxThreads || S * mxf::cdiv(E, 64) >= (int64_t(1) << 23)) return MXF_ERR_UNSUPPORTED;
   return MXF_OK;
 }
 }  // namespace
