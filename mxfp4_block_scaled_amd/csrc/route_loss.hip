@@ -27,8 +27,8 @@ constexpr int kFinishGroups = 8;  // groups of 64 threads that share a sequence'
 constexpr int kFinishLoads = 8;   // slots of a group in flight
 constexpr int64_t kMostFinish = 512;  // workgroups
 
-// Rows [row, row + U) of an [T][E] matrix as a range-checked resource: rows past T read as zeros, and the
-// row's place is a scalar, so that a load costs no address arithmetic.
+// Rows [row, row + U) of an [T][E] matrix as a range-checked resource: rows past T read as zeros. A row's or column's
+// step goes into the vector offset: the check covers that for any size, a scalar offset only up to the resource's.
 template <int U>
 __device__ __forceinline__ buf_rsrc rows_of(const void* p, int64_t row, int64_t T, int E, int bytes) {
   const int64_t left = min((int64_t)U, T - row);
@@ -39,8 +39,9 @@ __device__ __forceinline__ buf_rsrc rows_of(const void* p, int64_t row, int64_t 
 template <bool kBF16>
 __device__ __forceinline__ float load_logit(buf_rsrc r, int u, int E, int e) {
 #if defined(__HIP_DEVICE_COMPILE__)
-  if (kBF16) return __uint_as_float((uint32_t)(uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, 2 * e, 2 * u * E, 0) << 16);
-  return __uint_as_float((uint32_t)__builtin_amdgcn_raw_buffer_load_b32(r, 4 * e, 4 * u * E, 0));
+  const int at = u * E + e;
+  if (kBF16) return __uint_as_float((uint32_t)(uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, 2 * at, 0, 0) << 16);
+  return __uint_as_float((uint32_t)__builtin_amdgcn_raw_buffer_load_b32(r, 4 * at, 0, 0));
 #else
   return 0.0f;
 #endif
@@ -474,8 +475,8 @@ __global__ void __launch_bounds__(256) route_backward_kernel(RouteLossArgs a) {
 #pragma unroll
   for (int v = 0; v < V; ++v) {  // lanes past the experts are out of the row's range
 #if defined(__HIP_DEVICE_COMPILE__)
-    if (kBF16) __builtin_amdgcn_raw_buffer_store_b16((short)bf16x2_bits(d[v], 0.0f), ro, 2 * lane, 128 * v, 0);
-    else __builtin_amdgcn_raw_buffer_store_b32((int)__float_as_uint(d[v]), ro, 4 * lane, 256 * v, 0);
+    if (kBF16) __builtin_amdgcn_raw_buffer_store_b16((short)bf16x2_bits(d[v], 0.0f), ro, 2 * (lane + 64 * v), 0, 0);
+    else __builtin_amdgcn_raw_buffer_store_b32((int)__float_as_uint(d[v]), ro, 4 * (lane + 64 * v), 0, 0);
 #endif
   }
 }
