@@ -74,9 +74,10 @@ __device__ __forceinline__ void lora_shrink(const ShrinkArgs& p, ShrinkLds<MF, R
     const int64_t lo = max(s_lo, row0), hi = min(s_hi, row1);
     if (s_lo >= row1) break;
     if (l < 0 || l >= p.L || hi <= lo) continue;
-    // the fragments' rows start at the segment's first; past its last they read as zero
-    const buf_rsrc ra = make_rsrc(p.a + lo * K, (uint32_t)((hi - lo) * K * 2));
-    const buf_rsrc rb = make_rsrc(p.lora_a + (int64_t)l * p.rank * K, (uint32_t)(p.rank * krow));  // ranks past: zero
+    // the fragments' rows start at the segment's first; past its last, and past the ranks, they read as zero or again
+    const int first = __builtin_amdgcn_readfirstlane((int)lo), rows = __builtin_amdgcn_readfirstlane((int)(hi - lo));
+    const buf_rsrc ra = make_rsrc(p.a + first * K, (uint32_t)rows * krow);
+    const buf_rsrc rb = make_rsrc(p.lora_a + (int64_t)l * p.rank * K, (uint32_t)(p.rank * krow));
     v4f acc[MF][RF];
 #pragma unroll
     for (int m = 0; m < MF; ++m)
@@ -91,9 +92,9 @@ __device__ __forceinline__ void lora_shrink(const ShrinkArgs& p, ShrinkLds<MF, R
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
 #pragma unroll
-          for (int m = 0; m < MF; ++m) xr[u][m][i] = buf_load16(ra, voff, (16 * m + 8 * i) * krow + kk);
+          for (int m = 0; m < MF; ++m) xr[u][m][i] = buf_load16(ra, voff, w16_held_step(16 * m + 8 * i, rows) * krow + kk);
 #pragma unroll
-          for (int f = 0; f < RF; ++f) wr[u][f][i] = buf_load16(rb, voff, (16 * f + 8 * i) * krow + kk);
+          for (int f = 0; f < RF; ++f) wr[u][f][i] = buf_load16(rb, voff, w16_held_step(16 * f + 8 * i, p.rank) * krow + kk);
         }
       }
       __builtin_amdgcn_sched_barrier(0);

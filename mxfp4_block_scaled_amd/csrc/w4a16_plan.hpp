@@ -324,6 +324,10 @@ MXF_BOTH int64_t w16_weight_row(bool swiglu, int BN, int64_t half, int n, int r)
   return (int64_t)n * BN + r;
 }
 
+// Step r of n that a range-checked load takes through its scalar offset: the check is certain only while that
+// offset stays below the resource's size, so a step past the last takes the last again (its values are not used)
+MXF_BOTH int w16_held_step(int r, int n) { return w16_min(r, n - 1); }
+
 // Issue order at stage st, the i-th of whole turns of the slots (NA of activations, two of 128 k of
 // codes and of a scale group of P stages): on even i the codes of stages st + 2, st + 3 and, where a
 // scale group begins (or the slice does), the next group, then the activations of st + NA - 1.

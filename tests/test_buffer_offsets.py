@@ -3,6 +3,7 @@ the instruction's own) only as long as the scalar offset does not pass the resou
 shorter than a step that the code takes (rows past the last token, columns past the experts), the step has to be in the
 vector offset: no access of these kernels has a scalar offset."""
 
+import ctypes
 import os
 import re
 import shutil
@@ -40,3 +41,16 @@ def test_the_router_steps_in_vector_offsets(tmp_path):
         assert len(found[k]) >= 2
         for name, scalar, line in found[k]:
             assert scalar in ("0", "null"), (k, line)
+
+
+def test_held_steps_stay_inside(tmp_path):
+    """Row (or rank, or k) steps that loads of the ragged FP4-weight kernels take through a scalar offset: below the
+    size whatever the fragment asks for, and the step itself where it is inside."""
+    src, so = tmp_path / "held.cpp", str(tmp_path / "held.so")
+    src.write_text('#include "w4a16_plan.hpp"\nextern "C" int held(int r, int n) { return mxf::w16_held_step(r, n); }\n')
+    subprocess.run(["g++", "-std=c++17", "-shared", "-fPIC", "-Wno-unknown-pragmas", "-I", build.CSRC, str(src), "-o", so],
+                   check=True)
+    held = ctypes.CDLL(so).held
+    for n in range(1, 140):
+        for r in range(0, 136):
+            assert 0 <= held(r, n) < n and (held(r, n) == r or r >= n)
