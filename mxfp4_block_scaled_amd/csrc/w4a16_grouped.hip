@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(kNV ? 
       // at most 4 rows: a load per step, all of them now; else the rows of step 0
       if (few) {
 #pragma unroll
-        for (int s = 0; s < 4; ++s) ax[s] = buf_load16(ar, avoff(0), (uint32_t)(ss * 1024 + 256 * s));
+        for (int s = 0; s < 4; ++s) ax[s] = buf_load16(ar, avoff(0), (uint32_t)(ss * 1024 + 256 * w16_held_step(s, steps)));
       } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i) ax[i] = buf_load16(ar, avoff(i), (uint32_t)(ss * 1024));
