@@ -536,7 +536,8 @@ int fp4_dequantize(const uint8_t* q, const uint8_t* q_scale, int64_t rows, int64
  *                (MXF_W_NVFP4), as fp4_quantize writes them;  b, b_scale  [N][K/2], [N][K/32] or [N][K/16]
  *   a_tensor_scale, b_tensor_scale  [1] fp32 on the device (4-byte aligned): g_a, g_b of NVFP4 (NULL: 1;
  *                MXFP4 has none)
- *   c            [M][N] fp32 or bf16 (c_dtype), one rounding at the end
+ *   c            [M][N] fp32 or bf16 (c_dtype): the fp32 sum times g_a g_b in fp32, rounded to c_dtype. The
+ *                scales' exponents are applied together, so that neither alone can overflow or underflow
  *   workspace    fp4_gemm_workspace_bytes(M, N, K, fmt) bytes (0: none needed, may be NULL), 16-byte
  *                aligned, contents irrelevant: K slices' sums, added in a fixed order; calls that may
  *                overlap need one each

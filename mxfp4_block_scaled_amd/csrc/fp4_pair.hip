@@ -19,8 +19,10 @@ __global__ void __launch_bounds__(256) fp4_pair_sum_kernel(const float4* part, i
     s.z += p.z;
     s.w += p.w;
   }
-  const float x = ga ? *ga : 1.0f, y = gb ? *gb : 1.0f;
-  s = make_float4(s.x * x * y, s.y * x * y, s.z * x * y, s.w * x * y);
+  if (ga || gb) {
+    const PairScale scale(ga, gb);
+    s = make_float4(scale(s.x), scale(s.y), scale(s.z), scale(s.w));
+  }
   if (kOutBF16) static_cast<uint2*>(out)[i] = make_uint2(bf16x2_bits(s.x, s.y), bf16x2_bits(s.z, s.w));
   else static_cast<float4*>(out)[i] = s;
 }
@@ -138,7 +140,7 @@ __global__ void __launch_bounds__(64 * kFewWaves) fp4_few_kernel(Fp4PairArgs a) 
     __builtin_amdgcn_sched_barrier(0);
   };
   if (st0 < nst) issue(slot[0], sc[0], st0);
-  const float ga = a.ga ? *a.ga : 1.0f, gb = a.gb ? *a.gb : 1.0f;
+  const PairScale scale(kNV ? a.ga : nullptr, kNV ? a.gb : nullptr);
   for (int st = st0; st < nst; st += 2) {
     step(std::integral_constant<int, 0>{}, st);
     if (st + 1 < nst) step(std::integral_constant<int, 1>{}, st + 1);
@@ -154,7 +156,7 @@ __global__ void __launch_bounds__(64 * kFewWaves) fp4_few_kernel(Fp4PairArgs a) 
     float s = 0.0f;
 #pragma unroll
     for (int w = 0; w < kFewWaves; ++w) s += lds.part[w][from];
-    s = s * ga * gb;
+    if constexpr (kNV) s = scale(s);
     if (r >= m || c >= n) continue;
     if (kOutBF16) static_cast<__bf16*>(a.out)[(row0 + r) * N + col0 + c] = (__bf16)s;
     else static_cast<float*>(a.out)[(row0 + r) * N + col0 + c] = s;

@@ -75,6 +75,25 @@ __device__ __forceinline__ v8h decode8_half(uint32_t codes, _Float16 scale) {
 #endif
 }
 
+// x g_a g_b (null: 1). Either scale may lie at an end of fp32's range, so their mantissas are multiplied first and the
+// exponents are applied together: x, a sum of products of 2^-20 and more, keeps its bits, whichever operand has which
+struct PairScale {
+  float m;
+  int e;
+  __device__ __forceinline__ PairScale(const float* ga, const float* gb) : m(1.0f), e(0) {
+    int i;
+    if (ga) {
+      m = frexpf(*ga, &i);
+      e = i;
+    }
+    if (gb) {
+      m *= frexpf(*gb, &i);
+      e += i;
+    }
+  }
+  __device__ __forceinline__ float operator()(float x) const { return ldexpf(x * m, e); }
+};
+
 template <int BM, int BN>
 struct alignas(16) Fp4PairRing {
   uint8_t SA[2][BM * 32], SB[2][BN * 32];
@@ -143,11 +162,7 @@ __global__ void __launch_bounds__(64 * WM * WN) fp4_pair_kernel(Fp4PairArgs a) {
   };
   issue_scales(st0 / G);
   issue(0, st0);
-  float ga = 1.0f, gb = 1.0f;
-  if constexpr (!kSlices) {
-    if (a.ga) ga = *a.ga;
-    if (a.gb) gb = *a.gb;
-  }
+  const PairScale scale(kNV && !kSlices ? a.ga : nullptr, kNV && !kSlices ? a.gb : nullptr);  // MXFP4 has none
 
   v16f acc[FM][FN];
 #pragma unroll
@@ -279,7 +294,7 @@ static_for<0, 4>([&](auto J_) __attribute__((always_inline)) {
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             v[k] = acc[i][p * PF + f][4 * j + k];
-            if constexpr (!kSlices) v[k] = v[k] * ga * gb;
+            if constexpr (kNV && !kSlices) v[k] = scale(v[k]);
           }
           if (kOutBF16) {
             const int c = (4 * f + j) ^ (r32 & (NCH - 1));
