@@ -489,7 +489,7 @@ int moe_combine_backward(const void* dout, int dout_dtype, const void* y, int y_
  * nvfp4_tensor_scale - the scale of a whole tensor for NVFP4: the smallest power of two g (at least
  * 2^-126) with max |x| <= 6 * 448 * g, and 1 for a tensor of zeros. A power of two, so that block scale
  * times g, and with it every quantised value, is exact.
- *   x  n values, fp32 or bf16 (n % 32 == 0);  scale [1] fp32 on the device (4-byte aligned)
+ *   x  n values, fp32 or bf16 (n % 32 == 0, not 0);  scale [1] fp32 on the device (4-byte aligned)
  *   workspace    nvfp4_tensor_scale_workspace_bytes(n, x_dtype) bytes (0: none needed, may be NULL),
  *                16-byte aligned, contents irrelevant; calls that may overlap need one each
  * Errors: NULL, SHAPE, ALIGN, FORMAT, WORKSPACE.
@@ -545,7 +545,8 @@ int fp4_dequantize(const uint8_t* q, const uint8_t* q_scale, int64_t rows, int64
  * fp4_gemm(q(dy), qt(W)), dW = fp4_gemm(qt(dy), qt(x)), q and qt as fp4_quantize's.
  * Every product is exact (NVFP4: code x scale is exact in the fp16 operands), accumulation in fp32.
  * Requires K % 128 == 0, N % 16 == 0, K < 2^24, M N < 2^34 and at most 2^21 tiles of 128 x 128. The
- * UE8M0 byte 255 and the UE4M3 byte 0x7F (NaN) are not valid scales. M == 0 is a no-op.
+ * UE8M0 byte 255 and the UE4M3 byte 0x7F (NaN) are not valid scales. M == 0 is a no-op; K == 0 is refused
+ * (SHAPE): the weight gradient of no tokens is zeros, which the caller writes.
  * Errors: NULL, SHAPE (a tensor scale with MXFP4, too), ALIGN, FORMAT, UNSUPPORTED, WORKSPACE.
  */
 size_t fp4_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K, int fmt);

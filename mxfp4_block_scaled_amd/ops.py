@@ -714,11 +714,13 @@ def moe_combine_backward(dout, y, gates, pair_row, want_dy=True, want_dgates=Tru
 
 def nvfp4_tensor_scale(x, workspace=None):
     """x [rows][cols] bf16/fp32 -> [1] fp32: the smallest power of two that takes max |x| to at most 6 * 448, for
-    fp4_quantize (1 for zeros)."""
+    fp4_quantize (1 for zeros and for no rows)."""
     i = _gpu(x)
     dt = _one_of(x.dtype, DTYPES, "x")
-    out = x.new_empty((1,), dtype=torch.float32)
     n = x.numel()
+    if n == 0:
+        return x.new_ones((1,), dtype=torch.float32)
+    out = x.new_empty((1,), dtype=torch.float32)
     need = (_lib or load()).nvfp4_tensor_scale_workspace_bytes(n, dt)
     if need or workspace is not None:
         workspace = _workspace(workspace, need, x)
@@ -773,9 +775,10 @@ def fp4_dequantize(q, q_scale, fmt="nvfp4", tensor_scale=None, out_dtype=torch.b
     _is(q, "q", torch.uint8, (n, half), i)
     _is(q_scale, "q_scale", torch.uint8, (n, half * 2 // (16 if f else 32)), i)
     _tensor_scale(tensor_scale, f, i)
+    dt = _one_of(out_dtype, DTYPES, "out_dtype")
     out = q.new_empty((n, 2 * half), dtype=out_dtype)
-    _call("fp4_dequantize", i, q.data_ptr(), q_scale.data_ptr(), n, 2 * half, f, _at(tensor_scale), out.data_ptr(),
-          _one_of(out_dtype, DTYPES, "out_dtype"))
+    if half:
+        _call("fp4_dequantize", i, q.data_ptr(), q_scale.data_ptr(), n, 2 * half, f, _at(tensor_scale), out.data_ptr(), dt)
     return out
 
 
@@ -783,7 +786,7 @@ def fp4_gemm(a, a_scale, b, b_scale, fmt="nvfp4", a_tensor_scale=None, b_tensor_
              out=None, workspace=None):
     """The product of two quantised matrices (as fp4_quantize writes them): a [M][K/2], b [N][K/2] uint8 codes with
     their scales [.][K/16] (fmt "nvfp4") or [.][K/32] ("mxfp4"), tensor scales [1] fp32 of NVFP4 (None: 1) ->
-    c [M][N] bf16 or fp32."""
+    c [M][N] bf16 or fp32. K = 0 (the weight gradient of no tokens) gives zeros."""
     i = _gpu(a)
     if a.dim() != 2 or b.dim() != 2:
         raise RuntimeError("a must be [M][K/2] and b [N][K/2]")
@@ -802,6 +805,8 @@ def fp4_gemm(a, a_scale, b, b_scale, fmt="nvfp4", a_tensor_scale=None, b_tensor_
         out = a.new_empty((M, N), dtype=out_dtype)
     else:
         _is(out, "out", (torch.float32, torch.bfloat16), (M, N), i)
+    if half == 0 and N > 0 and N % 16 == 0:
+        return out.zero_()
     need = (_lib or load()).fp4_gemm_workspace_bytes(M, N, 2 * half, f)
     if need or workspace is not None:
         workspace = _workspace(workspace, need, a)
