@@ -44,11 +44,15 @@ __device__ __forceinline__ float divide(float x, float d, float r) {
   return fmaf(fmaf(-q, d, x), r, q);
 }
 
-// what a matrix's block maxima are divided by: 6 g
+// what a matrix's block maxima are divided by: 6 g; both times a power of two where g lies so near an end of fp32's
+// range that 6 g or its reciprocal would leave it
 struct Top {
-  float g, six, inv;
+  float g, lift, six, inv;
   __device__ __forceinline__ explicit Top(const float* tensor_scale)
-      : g(tensor_scale ? *tensor_scale : 1.0f), six(6.0f * g), inv(reciprocal(six)) {}
+      : g(tensor_scale ? *tensor_scale : 1.0f),
+        lift(g > 0x1p100f ? 0x1p-40f : g < 0x1p-80f ? 0x1p40f : 1.0f),
+        six(6.0f * (g * lift)),
+        inv(reciprocal(six)) {}
 };
 
 // what a block's elements are divided by
@@ -61,7 +65,7 @@ template <bool kNV>
 __device__ __forceinline__ Divisor divisor_of(uint32_t amax_bits, const Top& top) {
   Divisor v;
   if (kNV) {
-    v.byte = e4m3_mag_code(fminf(divide(__uint_as_float(amax_bits), top.six, top.inv), 448.0f));  // infinity gives NaN
+    v.byte = e4m3_mag_code(fminf(divide(__uint_as_float(amax_bits) * top.lift, top.six, top.inv), 448.0f));  // infinity gives NaN
     v.d = ue4m3_to_f32(v.byte) * top.g;
     const bool ok = v.d >= kTiny && v.d <= 3.0e38f;  // else the block is stored as zeros (g of no use, too)
     v.byte = ok ? v.byte : 0;

@@ -1,0 +1,32 @@
+"""fp4_quantize with a tensor scale anywhere in fp32's range, subnormal ones included: scales and codes of the definition,
+and the transposed form alike. With bf16 values and powers of two x / d is exact enough for equality (as in
+test_gpu_fp4_quant.py), else codes beside a border may be one step off."""
+
+import numpy as np
+import pytest
+import torch
+
+from mxfp4_block_scaled_amd import ops
+from tests import train_exact as ex
+from tests.test_gpu_fp4_quant import _compare
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("g", [2.0 ** 127, 2.0 ** 126, 2.0 ** 124, 3.0e38, 2.0 ** 99, 2.0 ** -79, 2.0 ** -110, 2.0 ** -126, 2.0 ** -130,
+                               3 * 2.0 ** -137, 2.0 ** -149])
+@pytest.mark.parametrize("size", [0.4, 2.5, 600.0, 2500.0])
+def test_a_scale_from_either_end(g, size):
+    """Blocks around size x g: s from its subnormals to 448."""
+    rows, cols = 40, 96
+    gen = torch.Generator().manual_seed(int(size * 10))
+    x = torch.rand((rows, cols), generator=gen, dtype=torch.float64) * 2 - 1
+    x = x * torch.exp2(-torch.randint(0, 3, (rows, 1), generator=gen).double()) * size
+    x = (x * g).clamp(-3.3e38, 3.3e38).float().bfloat16()
+    gt = torch.tensor([g], dtype=torch.float32)
+    assert float(gt) > 0
+    exact = float(np.log2(float(gt))).is_integer()
+    xd = x.double().numpy()
+    d = ops.fp4_quantize(x.cuda(), "nvfp4", gt.cuda(), transposed=True)
+    _compare(d["q"], d["q_scale"], xd, "nvfp4", float(gt), None, exact)
+    _compare(d["qt"], d["qt_scale"], ex.transposed(xd), "nvfp4", float(gt), None, exact)
