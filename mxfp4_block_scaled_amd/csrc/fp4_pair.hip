@@ -54,7 +54,7 @@ __device__ __forceinline__ void load_scales(buf_rsrc r, uint32_t voff, uint32_t 
 
 template <bool kNV, bool kOutBF16>
 __global__ void __launch_bounds__(64 * kFewWaves) fp4_few_kernel(Fp4PairArgs a) {
-  constexpr int W = kNV ? 2 : 1;
+  constexpr int W = pair_scale_words(kNV);
   __shared__ union {
     FewSlot ring[kFewWaves][2];
     float part[kFewWaves][16 * 65];
@@ -74,11 +74,8 @@ __global__ void __launch_bounds__(64 * kFewWaves) fp4_few_kernel(Fp4PairArgs a) 
 
   uint32_t at[4];  // row 8 q + lane / 8, 16-byte chunk lane % 8 of a stage
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const int r = 8 * q + (lane >> 3);
-    at[q] = (uint32_t)(r * wrow) + 16 * ((lane & 7) ^ swz_a16(r));
-  }
-  const uint32_t sat = (uint32_t)(r32 * srow) + 4 * W * g;
+  for (int q = 0; q < 4; ++q) at[q] = (uint32_t)pair_copy_from(64 * q + lane, wrow);
+  const uint32_t sat = pair_few_scales(r32, g, srow, kNV);
   struct Scales {
     uint32_t a[W], b[W];
   };
@@ -89,22 +86,22 @@ __global__ void __launch_bounds__(64 * kFewWaves) fp4_few_kernel(Fp4PairArgs a) 
       buf_dma16(ra, slot.A + 1024 * q, at[q], (uint32_t)st * 128);
     }
     __builtin_amdgcn_sched_barrier(0);  // the copies first: step() counts on it
-    load_scales(rbs, sat, (uint32_t)st * 8 * W, sc.b);
-    load_scales(ras, sat, (uint32_t)st * 8 * W, sc.a);
+    load_scales(rbs, sat, pair_few_scales_step(st, kNV), sc.b);
+    load_scales(ras, sat, pair_few_scales_step(st, kNV), sc.a);
     __builtin_amdgcn_sched_barrier(0);
   };
   v16f acc = v16f{};
   auto compute = [&](const FewSlot& slot, Scales sc, int st) __attribute__((always_inline)) {
-    if (g == 1 && (int64_t)st * 256 + 128 >= K) {  // the half past K, as in fp4_pair.hpp
+    if (pair_past(g, st, K)) {
 #pragma unroll
       for (int k = 0; k < W; ++k) sc.a[k] = sc.b[k] = 0;
     }
     v4i fa[4], fb[4];
-    const int o = r32 * 128 + 16 * ((4 * g) ^ swz_a16(r32));
+    const int o = pair_block_at(r32, g);
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
-      fa[s] = *reinterpret_cast<const v4i*>(slot.A + (o ^ (16 * s)));
-      fb[s] = *reinterpret_cast<const v4i*>(slot.B + (o ^ (16 * s)));
+      fa[s] = *reinterpret_cast<const v4i*>(slot.A + pair_step(o, s));
+      fb[s] = *reinterpret_cast<const v4i*>(slot.B + pair_step(o, s));
     }
     static_for<0, 4>([&](auto S_) __attribute__((always_inline)) {
       constexpr int s = decltype(S_)::value;
@@ -123,13 +120,13 @@ __global__ void __launch_bounds__(64 * kFewWaves) fp4_few_kernel(Fp4PairArgs a) 
   };
   FewSlot* const slot = lds.ring[wave];
   Scales sc[2];
-  // A stage is 8 copies, then 2 loads; they return in order, so once at most the 10 of the next stage are
+  // A stage's copies, then its loads; they return in order, so once at most those of the next stage are
   // outstanding the copies of this one have landed. No barrier: the slots are the wave's own.
   auto step = [&](auto I, int st) __attribute__((always_inline)) {
     constexpr int i = decltype(I)::value;
     if (st + 1 < nst) {
       issue(slot[i ^ 1], sc[i ^ 1], st + 1);
-      wait_vmcnt<10>();
+      wait_vmcnt<kFewCopies + kFewLoads>();
     } else {
       wait_vmcnt<0>();
     }
@@ -151,8 +148,7 @@ __global__ void __launch_bounds__(64 * kFewWaves) fp4_few_kernel(Fp4PairArgs a) 
   __syncthreads();
 #pragma unroll
   for (int k = 0; k < 1024 / (64 * kFewWaves); ++k) {
-    const int o = (int)threadIdx.x + 64 * kFewWaves * k, r = o >> 5, c = o & 31,
-              from = 65 * (4 * (c >> 3) + (c & 3)) + r + 32 * ((c >> 2) & 1);
+    const int o = (int)threadIdx.x + 64 * kFewWaves * k, r = o >> 5, c = o & 31, from = pair_few_sum(r, c);
     float s = 0.0f;
 #pragma unroll
     for (int w = 0; w < kFewWaves; ++w) s += lds.part[w][from];

@@ -105,7 +105,7 @@ __global__ void __launch_bounds__(64 * WM * WN) fp4_pair_kernel(Fp4PairArgs a) {
   constexpr int NW = WM * WN, FM = BM / WM / 32, FN = BN / WN / 32;
   constexpr int IA = BM * 8 / 64 / NW, IB = BN * 8 / 64 / NW;  // 16-byte copies a lane and stage
   constexpr int ISA = BM * 2 / 64, ISB = BN * 2 / 64;          // of a scale group, in all
-  constexpr int G = kNV ? 2 : 4, SB = 32 / G;                  // stages and scale bytes a row of a group, a stage
+  constexpr int G = pair_group_stages(kNV);                    // stages of a scale group
   constexpr int IS = (ISA + ISB + NW - 1) / NW;                // of them a wave: A's, then B's
   static_assert(IA >= 1 && IB >= 1, "tile shape");
   __shared__ Fp4PairRing<BM, BN> ring;
@@ -133,18 +133,16 @@ __global__ void __launch_bounds__(64 * WM * WN) fp4_pair_kernel(Fp4PairArgs a) {
   uint32_t va[IA], vb[IB], vs[IS];
 #pragma unroll
   for (int q = 0; q < IA; ++q) {
-    const int chunk = (wave * IA + q) * 64 + lane, r = chunk >> 3;
-    va[q] = (uint32_t)(r * wrow + 16 * ((chunk & 7) ^ swz_a16(r)));
+    va[q] = (uint32_t)pair_copy_from((wave * IA + q) * 64 + lane, wrow);
   }
 #pragma unroll
   for (int q = 0; q < IB; ++q) {
-    const int chunk = (wave * IB + q) * 64 + lane, r = chunk >> 3;
-    vb[q] = (uint32_t)(r * wrow + 16 * ((chunk & 7) ^ swz_a16(r)));
+    vb[q] = (uint32_t)pair_copy_from((wave * IB + q) * 64 + lane, wrow);
   }
 #pragma unroll
   for (int q = 0; q < IS; ++q) {
     const int p = wave + NW * q;
-    vs[q] = (uint32_t)((32 * (p < ISA ? p : p - ISA) + r32) * srow + 16 * g);
+    vs[q] = (uint32_t)pair_scales_from(p < ISA ? p : p - ISA, lane, srow);
   }
   auto issue = [&](int slot, int st) {
 #pragma unroll
@@ -173,36 +171,33 @@ __global__ void __launch_bounds__(64 * WM * WN) fp4_pair_kernel(Fp4PairArgs a) {
 #pragma unroll
   for (int f = 0; f < FM; ++f) {
     arow[f] = 32 * (FM * wm + f) + r32;
-    aoff[f] = arow[f] * 128 + 16 * ((4 * g) ^ swz_a16(arow[f]));
+    aoff[f] = pair_block_at(arow[f], g);
   }
 #pragma unroll
   for (int f = 0; f < FN; ++f) {
     brow[f] = 32 * (FN * wn + f) + r32;
-    boff[f] = brow[f] * 128 + 16 * ((4 * g) ^ swz_a16(brow[f]));
+    boff[f] = pair_block_at(brow[f], g);
   }
 
   struct Frags {
     v4i a[FM], b[FN];
   };
   auto compute = [&](const uint8_t* As, const uint8_t* Bs, int st) __attribute__((always_inline)) {
-    constexpr int W = kNV ? 2 : 1;  // dwords of scales a lane and row
+    constexpr int W = pair_scale_words(kNV);
     uint32_t sa[FM][W], sb[FN][W];
-    // 32 rows' first 16 bytes, then their second: neighbouring rows on other banks
-    const int off = SB * (st % G) + 4 * W * g, part = 512 * (off >> 4) + (off & 15);
-    const uint8_t* const SAs = &ring.SA[(st / G) & 1][part];
-    const uint8_t* const SBs = &ring.SB[(st / G) & 1][part];
-    // the half of the last stage past K: lane group 1's blocks count for nothing
-    const bool past = g == 1 && ((int64_t)st * 256 + 128 >= K);
+    const uint8_t* const SAs = &ring.SA[(st / G) & 1][pair_scales_at(st, g, kNV)];
+    const uint8_t* const SBs = &ring.SB[(st / G) & 1][pair_scales_at(st, g, kNV)];
+    const bool past = pair_past(g, st, K);
 #pragma unroll
     for (int i = 0; i < W; ++i) {
 #pragma unroll
       for (int f = 0; f < FM; ++f) {
-        sa[f][i] = *reinterpret_cast<const uint32_t*>(SAs + 1024 * (FM * wm + f) + 16 * r32 + 4 * i);
+        sa[f][i] = *reinterpret_cast<const uint32_t*>(SAs + pair_scales_row(32 * (FM * wm + f) + r32) + 4 * i);
         if (past) sa[f][i] = 0;
       }
 #pragma unroll
       for (int f = 0; f < FN; ++f) {
-        sb[f][i] = *reinterpret_cast<const uint32_t*>(SBs + 1024 * (FN * wn + f) + 16 * r32 + 4 * i);
+        sb[f][i] = *reinterpret_cast<const uint32_t*>(SBs + pair_scales_row(32 * (FN * wn + f) + r32) + 4 * i);
         if (past) sb[f][i] = 0;
       }
     }
@@ -211,13 +206,13 @@ __global__ void __launch_bounds__(64 * WM * WN) fp4_pair_kernel(Fp4PairArgs a) {
       for (int f = 0; f < FM; ++f) {
         int o = aoff[f];
         asm volatile("" : "+v"(o));
-        F.a[f] = *reinterpret_cast<const v4i*>(As + (o ^ (16 * s)));
+        F.a[f] = *reinterpret_cast<const v4i*>(As + pair_step(o, s));
       }
 #pragma unroll
       for (int f = 0; f < FN; ++f) {
         int o = boff[f];
         asm volatile("" : "+v"(o));
-        F.b[f] = *reinterpret_cast<const v4i*>(Bs + (o ^ (16 * s)));
+        F.b[f] = *reinterpret_cast<const v4i*>(Bs + pair_step(o, s));
       }
     };
     Frags F[2];
@@ -264,7 +259,7 @@ static_for<0, 4>([&](auto J_) __attribute__((always_inline)) {
     wait_vmcnt<0>();
     lds_barrier();
     if (st + 1 < nst) issue(i ^ 1, st + 1);
-    if ((st % G == 0 || st == st0) && (st / G + 1) * G < nst) issue_scales(st / G + 1);
+    if (w16_begins_scales(st, st0, G, nst)) issue_scales(st / G + 1);
     __builtin_amdgcn_sched_barrier(0);
     if (active) compute(ring.A[i], ring.B[i], st);
   };
@@ -278,8 +273,8 @@ static_for<0, 4>([&](auto J_) __attribute__((always_inline)) {
   // epilogue: 32 rows x PF fragments at a time through the wave's 8 KB of the ring (runs of 4 columns
   // in, 16-byte pieces of whole row segments out)
   constexpr int ES = kOutBF16 ? 2 : 4, PF = FN * 32 * ES > 256 ? 256 / (32 * ES) : FN;
-  constexpr int RB = PF * 32 * ES, NCH = RB / 16;
-  static_assert(FN % PF == 0, "passes");
+  constexpr int NCH = PF * 32 * ES / 16;
+  static_assert(FN % PF == 0 && 32 * 16 * NCH <= 8192, "passes");
   uint8_t* const stg = reinterpret_cast<uint8_t*>(&ring) + wave * 8192;
   uint8_t* const out = static_cast<uint8_t*>(a.out) + (kSlices ? (int64_t)blockIdx.y * M * N * 4 : 0);
 #pragma unroll
@@ -297,19 +292,17 @@ static_for<0, 4>([&](auto J_) __attribute__((always_inline)) {
             if constexpr (kNV && !kSlices) v[k] = scale(v[k]);
           }
           if (kOutBF16) {
-            const int c = (4 * f + j) ^ (r32 & (NCH - 1));
-            *reinterpret_cast<uint2*>(stg + RB * r32 + 16 * c + 8 * g) =
+            *reinterpret_cast<uint2*>(stg + pair_out_to(f, j, g, r32, ES, NCH)) =
                 make_uint2(bf16x2_bits(v[0], v[1]), bf16x2_bits(v[2], v[3]));
           } else {
-            const int c = (8 * f + 2 * j + g) ^ (r32 & (NCH - 1));
-            *reinterpret_cast<float4*>(stg + RB * r32 + 16 * c) = make_float4(v[0], v[1], v[2], v[3]);
+            *reinterpret_cast<float4*>(stg + pair_out_to(f, j, g, r32, ES, NCH)) = make_float4(v[0], v[1], v[2], v[3]);
           }
         }
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
 #pragma unroll
       for (int k = 0; k < NCH / 2; ++k) {
         const int idx = lane + 64 * k, rr = idx / NCH, c = idx % NCH;
-        const v4i v = *reinterpret_cast<const v4i*>(stg + RB * rr + 16 * (c ^ (rr & (NCH - 1))));
+        const v4i v = *reinterpret_cast<const v4i*>(stg + pair_out_from(rr, c, NCH));
         const int lrow = 32 * (FM * wm + i) + rr, lcol = 32 * (FN * wn + p * PF) + c * (16 / ES);
         if (lrow < m && lcol < n)
           __builtin_nontemporal_store(v, reinterpret_cast<v4i*>(out + ((row0 + lrow) * N + col0 + lcol) * ES));

@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #if defined(__HIP__)
+#include <hip/hip_runtime.h>
 #define MXF_BOTH __host__ __device__ __forceinline__
 #else
 #define MXF_BOTH inline
