@@ -512,8 +512,10 @@ int nvfp4_tensor_scale(const void* x, int x_dtype, int64_t n, float* scale, void
  *   q, q_scale   [rows][cols/2], [rows][cols/B] (both NULL: not wanted)
  *   qt, qt_scale the codes of x^T, blocks along x's columns: [cols][R/2], [cols][R/B] with R = rows
  *                rounded up to 128; elements past the rows are zeros (both NULL: not wanted)
- * These are the operands of fp4_gemm, and q, q_scale the weights of the calls above. Values that are
- * not finite are not handled: they spoil their own block (and a tensor scale taken from them).
+ * These are the operands of fp4_gemm, which sums over K % 128 == 0: qt, qt_scale for any rows; q, q_scale where
+ * cols % 128 == 0 (x's columns filled up with zeros before this call give that and add nothing). q, q_scale are
+ * the weights of the calls above, too. MXFP4 along rows to nearest is mxfp4_quantize_act's MXF_E2M1, bit for bit.
+ * Values that are not finite are not handled: they spoil their own block (and a tensor scale taken from them).
  * Requires cols % 32 == 0, cols < 2^22 and at most 2^23 tiles of 128 x 128 (transposed), or rows cols
  * below 2^36. rows == 0 is a no-op. Errors: NULL, SHAPE (a tensor scale with MXFP4, too), ALIGN, FORMAT,
  * UNSUPPORTED.
@@ -522,8 +524,8 @@ int fp4_quantize(const void* x, int x_dtype, int64_t rows, int64_t cols, int fmt
                  const uint8_t* rnd, uint8_t* q, uint8_t* q_scale, uint8_t* qt, uint8_t* qt_scale, mxf_stream stream);
 
 /*
- * fp4_dequantize - out [rows][cols] (fp32 or bf16) = E2M1 value x block scale x g, one rounding to
- * out_dtype (none is needed where g is a power of two and nothing leaves the type's range). Arguments
+ * fp4_dequantize - out [rows][cols] (fp32 or bf16) = E2M1 value x block scale x g in fp32, rounded to
+ * out_dtype (exact where g is a power of two and nothing leaves the type's range). Arguments
  * as fp4_quantize writes them along the rows; a transposed result is read with its own rows and cols.
  * Requires cols % 32 == 0. rows == 0 is a no-op. Errors: NULL, SHAPE, ALIGN, FORMAT, UNSUPPORTED.
  */
@@ -541,7 +543,8 @@ int fp4_dequantize(const uint8_t* q, const uint8_t* q_scale, int64_t rows, int64
  *   workspace    fp4_gemm_workspace_bytes(M, N, K, fmt) bytes (0: none needed, may be NULL), 16-byte
  *                aligned, contents irrelevant: K slices' sums, added in a fixed order; calls that may
  *                overlap need one each
- * A linear layer y = x W^T of [T][I] by [O][I] and its gradients: y = fp4_gemm(q(x), q(W)), dx =
+ * A linear layer y = x W^T of [T][I] by [O][I] (I and O multiples of 128, or x, W and dy filled up with columns
+ * of zeros before they are quantised) and its gradients: y = fp4_gemm(q(x), q(W)), dx =
  * fp4_gemm(q(dy), qt(W)), dW = fp4_gemm(qt(dy), qt(x)), q and qt as fp4_quantize's.
  * Every product is exact (NVFP4: code x scale is exact in the fp16 operands), accumulation in fp32.
  * Requires K % 128 == 0, N % 16 == 0, K < 2^24, M N < 2^34 and at most 2^21 tiles of 128 x 128. The

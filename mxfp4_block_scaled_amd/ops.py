@@ -740,7 +740,7 @@ def fp4_quantize(x, fmt="nvfp4", tensor_scale=None, rnd=None, rows=True, transpo
     given) or "mxfp4" (32 elements, UE8M0). To nearest, or stochastically with rnd [rows][cols] uint8 random bytes.
     Returns a dict of q [rows][cols/2] and q_scale [rows][cols/B] (rows=True), and of qt [cols][R/2] and qt_scale
     [cols][R/B] (transposed=True): the codes of x^T, R = rows rounded up to 128 with zeros; else None. uint8, as fp4_gemm
-    takes them."""
+    takes them, q where cols % 128 == 0: fill x up with columns of zeros first where it is not."""
     i = _gpu(x)
     if x.dim() != 2:
         raise RuntimeError("x must be 2-d [rows][cols]")
@@ -786,7 +786,7 @@ def fp4_gemm(a, a_scale, b, b_scale, fmt="nvfp4", a_tensor_scale=None, b_tensor_
              out=None, workspace=None):
     """The product of two quantised matrices (as fp4_quantize writes them): a [M][K/2], b [N][K/2] uint8 codes with
     their scales [.][K/16] (fmt "nvfp4") or [.][K/32] ("mxfp4"), tensor scales [1] fp32 of NVFP4 (None: 1) ->
-    c [M][N] bf16 or fp32. K = 0 (the weight gradient of no tokens) gives zeros."""
+    c [M][N] bf16 or fp32. K % 128 == 0 and N % 16 == 0; K = 0 (the weight gradient of no tokens) gives zeros."""
     i = _gpu(a)
     if a.dim() != 2 or b.dim() != 2:
         raise RuntimeError("a must be [M][K/2] and b [N][K/2]")

@@ -30,3 +30,16 @@ def test_a_scale_from_either_end(g, size):
     d = ops.fp4_quantize(x.cuda(), "nvfp4", gt.cuda(), transposed=True)
     _compare(d["q"], d["q_scale"], xd, "nvfp4", float(gt), None, exact)
     _compare(d["qt"], d["qt_scale"], ex.transposed(xd), "nvfp4", float(gt), None, exact)
+
+
+@pytest.mark.parametrize("shuffled", [False, True])
+def test_mxfp4_rows_are_those_of_the_activations_for_every_value(shuffled):
+    """Every finite bf16 value, in blocks of neighbours and in mixed ones."""
+    bits = torch.arange(65536, dtype=torch.int32)
+    bits = bits[(bits & 0x7F80) != 0x7F80]
+    if shuffled:
+        bits = bits[torch.randperm(bits.numel(), generator=torch.Generator().manual_seed(1))]
+    x = bits.to(torch.int16).view(torch.bfloat16).view(-1, 64).cuda()
+    q, s = ops.mxfp4_quantize_act(x, "e2m1")
+    d = ops.fp4_quantize(x, "mxfp4")
+    assert torch.equal(d["q"], q) and torch.equal(d["q_scale"], s)
