@@ -12,8 +12,8 @@
 // sequence: both ascend along the tokens, so each pair that meets has a slot of its own) and added
 // in a fixed order by a second launch: no floating-point atomics, the same result every time.
 //
-// Latency bounds all but the largest calls: 16384 x 256 fp32 in 16 sequences 11.9 + 7.7 us forward and 12.0
-// backward, of which the bytes are 3.5 and 7; 64 tokens 7.9 and 3.7.
+// Latency bounds all but the largest calls: 16384 x 256 fp32 in 16 sequences 11.9 + 6.4 to 7.7 us
+// forward and 12.3 backward, of which the bytes are 3.5 and 7; 64 tokens 7.8 and 3.4.
 #include "launch.hpp"
 #include "w4a16_tile.hpp"
 #include "wave.hpp"
